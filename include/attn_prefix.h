@@ -51,7 +51,8 @@ typedef enum {
     ATTN_ERR_UNSUPPORTED = 2,   /* head dim not in {32,64,128,256}, or device not sm_100 */
     ATTN_ERR_CUDA = 3,          /* a CUDA runtime/driver call failed (launch, attribute) */
     ATTN_ERR_TIMEOUT = 4,       /* a bounded in-kernel wait gave up (device flag) */
-    ATTN_ERR_KVLEN_RANGE = 5    /* some kv_len[b] was outside [0, Tk] (device flag) */
+    ATTN_ERR_KVLEN_RANGE = 5,   /* some kv_len[b] was outside [0, Tk] (device flag) */
+    ATTN_ERR_CACHE_RANGE = 6    /* a page, slot or query range outside its bounds (device flag) */
 } attn_status;
 
 /* Element strides of a [B, H, T, D] operand whose d index is contiguous (stride 1):
@@ -209,8 +210,115 @@ attn_status attn_prefix_fwd_splitkv_noalloc(const void* q, const void* k, const 
                                             int B, int H, int Tq, int Tk, int D, float scale,
                                             cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * Serving: queries and keys as they leave a projection, a paged key/value cache, and
+ * attention of each sequence's new tokens over its pages.  The pages these entry
+ * points serve are the same kv_len[b] prefixes as above, kept in fixed-size pages
+ * instead of one padded buffer; the pages of the method describe no cache.
+ * All conventions above hold (caller-owned device memory, checks before any launch,
+ * no allocation, no synchronisation).  Index and length arrays are int32 in DEVICE
+ * memory, 4-byte aligned; the host never reads them.
+ * --------------------------------------------------------------------------------- */
+
+/* Per-head RMS norm and rotation by position of q and, in the same launch, k:
+ *     y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ *     for i < R/2, t = position * inv_freq[i], and (a, b) the pair i of the first R elements,
+ *     (a, b) -> attn_factor * (a cos t - b sin t, b cos t + a sin t);   elements >= R: y
+ * Pair i is elements (i, i + R/2), or (2i, 2i + 1) if `interleaved`.  fp32 arithmetic with
+ * one rounding to bf16 at the end; the angle is formed and reduced in fp64, so positions
+ * over the whole int32 range (negative ones included) rotate as exactly as near ones.
+ *   x, y:      bf16 [B, H, T, D] at their strides (see attn_strides; NULL: contiguous).
+ *              y may be x itself; other overlaps give undefined values.
+ *   weight:    [D] bf16, or fp32 if weight_fp32; NULL for no norm.
+ *   positions: int32 [B, T].      inv_freq: fp64 [R/2], 8-byte aligned (NULL if R = 0).
+ *   R: even, in [0, D].  k (and its fields) may be absent: k.x = NULL. */
+typedef struct {
+    const void* x;
+    void* y;
+    const void* weight;
+    int32_t H;
+    int32_t weight_fp32;
+    attn_strides x_strides, y_strides;   /* all-zero: contiguous [B, H, T, D] */
+} attn_rope_operand;
+attn_status attn_qk_norm_rope(const attn_rope_operand* q, const attn_rope_operand* k, const int32_t* positions,
+                              const double* inv_freq, int B, int T, int D, int R, int interleaved, float eps,
+                              float attn_factor, cudaStream_t stream);
+
+/* A paged cache: num_pages pages of page_size slots; a slot holds one token's row of D
+ * values for each of Hkv heads.  Element (page, head, slot, d) of k is at
+ * k + page * k_strides.b + head * k_strides.h + slot * k_strides.t + d.
+ *   format ATTN_CACHE_BF16: rows are bf16; k_scale, v_scale NULL.
+ *   format ATTN_CACHE_E4M3: rows are e4m3 codes (1 byte) with one scale byte per row in
+ *     k_scale, v_scale [num_pages, Hkv, page_size] (contiguous): the row's values are
+ *     code * 2^(scale - 127).  attn_cache_write takes the least exponent e in [-117, 120]
+ *     with amax / 2^e <= 448 (0 for a row of zeros), so that x / 2^e and code * 2^e are
+ *     exact and the only rounding is the one to e4m3 (half a step: 2^-4 of a normal
+ *     value); every code * 2^e is a bf16 number (at e = 120 magnitudes above 240 * 2^120 are
+ *     stored as that, the largest one below infinity).  A row that holds a NaN or an infinity
+ *     is stored as NaN (scale byte 255), and reads back as NaN.
+ * page_size: a multiple of 8.  Strides: multiples of 16 bytes, t >= D.
+ * num_pages * page_size <= 2^31 - 1; element offsets are 64-bit. */
+#define ATTN_CACHE_BF16 0
+#define ATTN_CACHE_E4M3 1
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    attn_strides k_strides, v_strides;   /* all-zero: contiguous [num_pages, Hkv, page_size, D] */
+    int32_t num_pages, page_size, Hkv, D;
+    int32_t format;
+} attn_cache;
+
+/* Stores T tokens' key and value rows: token i goes to slot slots[i] = page * page_size +
+ * row.  A negative slot skips the token (padding); one at or beyond num_pages * page_size
+ * skips it and raises the sticky ATTN_ERR_CACHE_RANGE flag.  The slots of one call must be
+ * distinct: a slot given twice is left with content of either token, in no order.
+ *   k, v: bf16 [T, Hkv, D] at strides (b ignored; all-zero or NULL: contiguous [T, Hkv, D]). */
+attn_status attn_cache_write(const attn_cache* cache, const void* k, const void* v, const attn_strides* k_strides,
+                             const attn_strides* v_strides, const int32_t* slots, int T, cudaStream_t stream);
+
+/* Reads sequences back from their pages as contiguous prefixes: row j < kv_len[b] of
+ * element b is slot j % page_size of page block_table[b * table_stride + j / page_size].
+ * Rows at or beyond kv_len[b] are left as they were.  This is the [B, H, Tk, D] prefix
+ * layout of attn_prefix_fwd.  kv_len[b] outside [0, min(Tk, max_pages * page_size)] is
+ * clamped (ATTN_ERR_KVLEN_RANGE); a needed page outside [0, num_pages) reads as zeros
+ * (ATTN_ERR_CACHE_RANGE).  Table entries behind the last needed page are never read.
+ *   k_out, v_out: bf16 [B, Hkv, Tk, D] at strides (NULL: contiguous).
+ *   block_table: int32 [B, max_pages], rows table_stride entries apart. */
+attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table, int64_t table_stride, int max_pages,
+                            const int32_t* kv_len, void* k_out, void* v_out, const attn_strides* k_strides,
+                            const attn_strides* v_strides, int B, int Tk, cudaStream_t stream);
+
+/* Attention of each sequence's new tokens over its pages, the new ones included (write
+ * them first).  Sequence b has query rows [q_start[b], q_start[b+1]) of q and attends to its
+ * first kv_len[b] keys; head h of the Hq query heads uses key head h / (Hq / Hkv).  With
+ * `causal`, the n query rows are the last n positions: row i sees keys j <= kv_len[b] - n + i,
+ * so a row whose position would be negative sees none.  A row that sees no key gives
+ * out = 0, lse = -inf.  Rows of q outside every sequence are not computed: their out and
+ * lse stay as they were.
+ *   q, out: bf16 [T, Hq, D] at strides (b ignored; NULL: contiguous).   lse: fp32 [T, Hq] or NULL.
+ *   q_start: int32 [B + 1], non-decreasing within [0, T]; NULL: B = T, one row each (single
+ *     tokens).  max_q: an upper bound on the rows of one sequence.  Bounds that decrease or
+ *     leave [0, T] are clamped and rows beyond max_q are not computed; either raises
+ *     ATTN_ERR_CACHE_RANGE.  kv_len and block_table as attn_cache_read, with
+ *     max_pages * page_size in Tk's place.
+ *   Hq: a multiple of Hkv, Hq / Hkv <= 128.
+ *   num_splits: parts that a sequence's keys are cut into, in [1, 256], or 0 to have it chosen
+ *     from the sizes.  workspace: attn_paged_workspace_bytes of device memory with the same
+ *     arguments, 16-byte aligned, or NULL where that is 0; no initialisation needed.  Calls
+ *     that share a workspace must not overlap on the GPU. */
+size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int max_q,
+                                  int num_splits);
+attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_strides* q_strides,
+                           const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* kv_len,
+                           const int32_t* q_start, void* out, const attn_strides* out_strides, float* lse,
+                           void* workspace, int B, int T, int Hq, int max_q, int causal, int num_splits, float scale,
+                           cudaStream_t stream);
+
 /* Synchronizes `stream`, then reads and clears the sticky device flags raised by
- * earlier launches: ATTN_ERR_TIMEOUT has priority over ATTN_ERR_KVLEN_RANGE; ATTN_OK if
+ * earlier launches: ATTN_ERR_TIMEOUT has priority over ATTN_ERR_KVLEN_RANGE, that over
+ * ATTN_ERR_CACHE_RANGE; ATTN_OK if
  * none.  A CUDA error during the synchronization returns ATTN_ERR_CUDA. */
 attn_status attn_get_device_status(cudaStream_t stream);
 

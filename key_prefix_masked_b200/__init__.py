@@ -5,6 +5,13 @@
     out, lse = attn_prefix_fwd_split_fused(q, k, v, kv_len, num_splits=64)  # one launch
     out, lse = attn_prefix_fwd_segments(q, k, v, seg_start, seg_len)        # multi-range keys
 
+and for serving over a paged key/value cache (see paged.py):
+
+    q, k = attn_qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight) # per-head norm + rotation
+    attn_cache_write(k, v, slots, k_cache, v_cache)                         # rows into pages, bf16 or e4m3
+    out, lse = attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start, max_q)
+    k, v = attn_cache_read(k_cache, v_cache, block_table, kv_len)           # pages back to a prefix
+
 q, k, v: bf16 CUDA tensors [B, H, T, D] with D in {32, 64, 128, 256} and d contiguous (the
 single-pass, split and combine calls take other strides as given, so [B, T, H, D] views
 and slices of a packed QKV run without copies; the fused-split and multi-range calls want
@@ -22,6 +29,7 @@ from ._binding import (  # noqa: F401
     ATTN_ERR_CUDA,
     ATTN_ERR_TIMEOUT,
     ATTN_ERR_KVLEN_RANGE,
+    ATTN_ERR_CACHE_RANGE,
     ATTN_DEBUG_DROP_COPY,
     SUPPORTED_HEAD_DIMS,
     LIB_PATH,
@@ -39,4 +47,12 @@ from ._binding import (  # noqa: F401
     split_chunk_len,
     status_string,
     version,
+)
+from .paged import (  # noqa: F401
+    PagedCache,
+    attn_cache_read,
+    attn_cache_write,
+    attn_paged_fwd,
+    attn_qk_norm_rope,
+    rope_inv_freq,
 )

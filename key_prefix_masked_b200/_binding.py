@@ -22,6 +22,7 @@ ATTN_ERR_UNSUPPORTED = 2
 ATTN_ERR_CUDA = 3
 ATTN_ERR_TIMEOUT = 4
 ATTN_ERR_KVLEN_RANGE = 5
+ATTN_ERR_CACHE_RANGE = 6
 ATTN_DEBUG_DROP_COPY = 1
 
 SUPPORTED_HEAD_DIMS = (32, 64, 128, 256)
@@ -30,6 +31,7 @@ SUPPORTED_HEAD_DIMS = (32, 64, 128, 256)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_int64
 _SIGNATURES = {
     "attn_prefix_fwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
     "attn_prefix_fwd_strided": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P]),
@@ -46,6 +48,11 @@ _SIGNATURES = {
     "attn_segments_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "attn_prefix_fwd_segments": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
     "attn_prefix_fwd_splitkv_noalloc": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
+    "attn_qk_norm_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P]),
+    "attn_cache_write": (_I, [_P, _P, _P, _P, _P, _P, _I, _P]),
+    "attn_cache_read": (_I, [_P, _P, _L, _I, _P, _P, _P, _P, _P, _I, _I, _P]),
+    "attn_paged_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "attn_paged_fwd": (_I, [_P, _P, _P, _P, _L, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "attn_get_device_status": (_I, [_P]),
     "attn_set_wait_limit_ns": (None, [ctypes.c_uint64]),
     "attn_set_debug_flags": (None, [ctypes.c_uint]),

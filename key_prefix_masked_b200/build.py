@@ -15,13 +15,14 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libattn_prefix.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
-SOURCES = ["attn_prefix.cu"]
-HEADERS = ["ptx.cuh", "tmem_ops.cuh", "softmax_math.cuh", "pair_kernel.cuh", "segments.cuh"]
+SOURCES = ["attn_prefix.cu", "paged.cu"]
+HEADERS = ["host_common.h", "ptx.cuh", "tmem_ops.cuh", "softmax_math.cuh", "pair_kernel.cuh", "segments.cuh",
+           "rope.cuh", "cache.cuh", "paged_simple.cuh"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared", "--cudart", "static",
-    "-Xptxas", "-v",
+    "-Xptxas", "-v", "--threads", "0",
 ]
 
 

@@ -63,6 +63,7 @@
 #include "ptx.cuh"
 #include "tmem_ops.cuh"
 #include "softmax_math.cuh"
+#include "host_common.h"
 
 namespace attn {
 
@@ -75,10 +76,6 @@ constexpr float RESCALE_LOG2 = 8.0f;  // rescale O only when the max grows by > 
 constexpr uint32_t XCH_ID = 9;     // named barrier: the two softmax groups' epilogue exchange
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.44269504088896340736f;
-
-constexpr unsigned STATUS_TIMEOUT = 1u;
-constexpr unsigned STATUS_KVLEN = 2u;
-constexpr unsigned STATUS_LAYOUT = 4u;   // dynamic shared memory not 1024-byte aligned
 
 template <int D>
 struct Cfg {
@@ -944,49 +941,14 @@ using attn::BN;
 using attn::Cfg;
 using attn::Params;
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Test hooks (attn_set_wait_limit_ns, attn_set_debug_flags): process-wide settings read
-// by every launch that starts after they are written, from any host thread.
-std::atomic<unsigned long long> g_wait_ns{1000000000ull};
-std::atomic<unsigned> g_debug{0u};
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(f);
-    });
-    return fn;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Element strides of one [B, H, T, D] operand (d contiguous).
-struct Strides {
-    long long b, h, t;
-};
-Strides contiguous(int H, int T, int D) {
-    return {static_cast<long long>(H) * T * D, static_cast<long long>(T) * D, static_cast<long long>(D)};
-}
-// Caller strides, or the contiguous [B,H,T,D] layout for NULL.  Every stride must be a
-// non-negative multiple of 8 elements (16-byte rows for TMA and vector stores), and a
-// row may not overlap the next one (t >= D).
-bool resolve_strides(const attn_strides* in, int H, int T, int D, Strides* out) {
-    if (in == nullptr) {
-        *out = contiguous(H, T, D);
-        return true;
-    }
-    if (in->b < 0 || in->h < 0 || in->t < D || (in->b & 7) || (in->h & 7) || (in->t & 7)) return false;
-    *out = {static_cast<long long>(in->b), static_cast<long long>(in->h), static_cast<long long>(in->t)};
-    return true;
-}
+using attn::aligned16;
+using attn::check_device;
+using attn::contiguous;
+using attn::g_debug;
+using attn::g_wait_ns;
+using attn::make_map;
+using attn::resolve_strides;
+using attn::Strides;
 
 // Host checks that need no CUDA call.
 attn_status check_args(const void* q, const void* k, const void* v, const void* kv_len, const void* out,
@@ -999,49 +961,6 @@ attn_status check_args(const void* q, const void* k, const void* v, const void* 
     if (!isfinite(scale)) return ATTN_ERR_INVALID_ARG;
     if (D != 32 && D != 64 && D != 128 && D != 256) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
-}
-
-// Device must be compute capability 10.0 (B200 / sm_100a).  Cached per device ordinal
-// (0 = not looked up yet, 1 = supported, 2 = not supported); host threads may race on an
-// entry, and every one of them writes the same value.
-attn_status check_device() {
-    static std::atomic<int> cached[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return ATTN_ERR_CUDA;
-    }
-    if (dev < 0 || dev >= 64) return ATTN_ERR_UNSUPPORTED;
-    int c = cached[dev].load(std::memory_order_relaxed);
-    if (c == 0) {
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-            cudaGetLastError();
-            return ATTN_ERR_CUDA;
-        }
-        c = (major == 10 && minor == 0) ? 1 : 2;
-        cached[dev].store(c, std::memory_order_relaxed);
-    }
-    return c == 1 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
-}
-
-// A [B, H, T, D] bf16 tensor at element strides s (d contiguous) as a 4-D TMA map with
-// dims (D, T, H, B); a box is box_rows rows x box_cols columns of one (b, h).
-bool make_map(CUtensorMap* map, const void* base, int B, int H, int T, int D, const Strides& s, int box_cols,
-              int box_rows, CUtensorMapSwizzle swz) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(H),
-                          static_cast<cuuint64_t>(B)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(s.t) * 2ull, static_cast<cuuint64_t>(s.h) * 2ull,
-                             static_cast<cuuint64_t>(s.b) * 2ull};
-    cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u, 1u};
-    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
 }
 
 template <int D, bool SPLIT>
@@ -1324,8 +1243,12 @@ attn_status attn_get_device_status(cudaStream_t stream) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
     }
+    unsigned int paged = 0;
+    if (!attn::take_paged_flags(&paged)) return ATTN_ERR_CUDA;
+    flags |= paged;
     if (flags & attn::STATUS_TIMEOUT) return ATTN_ERR_TIMEOUT;
     if (flags & attn::STATUS_KVLEN) return ATTN_ERR_KVLEN_RANGE;
+    if (flags & attn::STATUS_CACHE) return ATTN_ERR_CACHE_RANGE;
     if (flags & attn::STATUS_LAYOUT) return ATTN_ERR_CUDA;
     return ATTN_OK;
 }
@@ -1344,6 +1267,7 @@ const char* attn_status_string(attn_status s) {
         case ATTN_ERR_CUDA: return "ATTN_ERR_CUDA";
         case ATTN_ERR_TIMEOUT: return "ATTN_ERR_TIMEOUT";
         case ATTN_ERR_KVLEN_RANGE: return "ATTN_ERR_KVLEN_RANGE";
+        case ATTN_ERR_CACHE_RANGE: return "ATTN_ERR_CACHE_RANGE";
     }
     return "ATTN_ERR_UNKNOWN";
 }

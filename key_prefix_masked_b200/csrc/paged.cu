@@ -1,0 +1,347 @@
+// paged.cu -- serving operators around the prefix-masked attention: per-head norm and
+// rotation of q and k (rope.cuh), a paged key/value cache written and read back
+// (cache.cuh), and attention of new tokens over the pages (paged_simple.cuh).  The C ABI is
+// in include/attn_prefix.h.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "attn_prefix.h"
+#include "host_common.h"
+
+namespace attn {
+
+static __device__ unsigned int g_paged_status = 0;
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// kv_len[b] clamped to [0, cap]; `report`: this thread raises the flag.
+__device__ __forceinline__ int paged_kv_len(const int32_t* kv_len, int b, int cap, bool report) {
+    const int kv = __ldg(kv_len + b);
+    if (kv >= 0 && kv <= cap) return kv;
+    if (report) atomicOr(&g_paged_status, STATUS_KVLEN);
+    return kv < 0 ? 0 : cap;
+}
+
+#include "rope.cuh"
+#include "cache.cuh"
+
+struct PagedParams {
+    CacheView c;
+    const __nv_bfloat16* q;
+    __nv_bfloat16* out;
+    float* lse;
+    long long q_t, q_h, out_t, out_h;   // element strides
+    const int32_t* table;
+    long long table_stride;
+    const int32_t* kv_len;
+    const int32_t* q_start;             // null: one row per sequence
+    int B, T, Hq, G, max_q, kv_cap, causal;
+    float scale_log2;
+};
+
+// Rows [t0, t0 + n) of q belong to sequence b.
+struct QueryRange {
+    int t0, n;
+};
+__device__ __forceinline__ QueryRange query_range(const PagedParams& p, int b, bool report) {
+    if (p.q_start == nullptr) return {b, 1};
+    const int a = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
+    const int t0 = min(max(a, 0), p.T), t1 = min(max(e, t0), p.T);
+    if (report && (t0 != a || t1 != e || t1 - t0 > p.max_q)) atomicOr(&g_paged_status, STATUS_CACHE);
+    return {t0, t1 - t0};
+}
+// The page that holds sequence b's keys [pj * page_size, ...), -1 if the table names none.
+__device__ __forceinline__ int checked_page(const PagedParams& p, int b, int pj, bool report) {
+    const int page = __ldg(p.table + b * p.table_stride + pj);
+    if (page >= 0 && page < p.c.num_pages) return page;
+    if (report) atomicOr(&g_paged_status, STATUS_CACHE);
+    return -1;
+}
+
+#include "paged_simple.cuh"
+
+bool take_paged_flags(unsigned* flags) {
+    const unsigned zero = 0;
+    return cudaMemcpyFromSymbol(flags, g_paged_status, sizeof *flags) == cudaSuccess &&
+           cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero) == cudaSuccess;
+}
+
+}  // namespace attn
+
+// =========================================================================== host side
+namespace {
+
+using namespace attn;
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Strides given by value or by pointer; absent or all-zero: contiguous.
+bool strides_of(const attn_strides* s, int H, int T, int D, Strides* out) {
+    if (s != nullptr && s->b == 0 && s->h == 0 && s->t == 0) s = nullptr;
+    return resolve_strides(s, H, T, D, out);
+}
+// Token-major [T, H, D] rows (b ignored); absent or all-zero: contiguous.
+bool token_strides_of(const attn_strides* s, int H, int D, Strides* out) {
+    if (s == nullptr || (s->h == 0 && s->t == 0)) {
+        *out = {0, D, static_cast<long long>(H) * D};
+        return true;
+    }
+    if (s->h < 0 || s->t < 0 || (s->h & 7) || (s->t & 7)) return false;
+    *out = {0, static_cast<long long>(s->h), static_cast<long long>(s->t)};
+    return true;
+}
+bool head_dim_ok(int D) { return D == 32 || D == 64 || D == 128 || D == 256; }
+
+attn_status cache_view(const attn_cache* c, CacheView* v) {
+    if (c == nullptr || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return ATTN_ERR_INVALID_ARG;
+    if (c->num_pages <= 0 || c->page_size <= 0 || c->Hkv <= 0) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(c->num_pages) * c->page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    if (c->format != ATTN_CACHE_BF16 && c->format != ATTN_CACHE_E4M3) return ATTN_ERR_UNSUPPORTED;
+    if (!head_dim_ok(c->D) || (c->page_size & 7)) return ATTN_ERR_UNSUPPORTED;
+    const bool e4m3 = c->format == ATTN_CACHE_E4M3;
+    if (e4m3 && (!c->k_scale || !c->v_scale)) return ATTN_ERR_INVALID_ARG;
+    const int size = e4m3 ? 1 : 2;
+    Strides s[2];
+    if (!strides_of(&c->k_strides, c->Hkv, c->page_size, c->D, &s[0]) ||
+        !strides_of(&c->v_strides, c->Hkv, c->page_size, c->D, &s[1]))
+        return ATTN_ERR_INVALID_ARG;
+    memset(v, 0, sizeof *v);
+    for (int i = 0; i < 2; ++i) {
+        if ((s[i].b * size) & 15 || (s[i].h * size) & 15 || (s[i].t * size) & 15) return ATTN_ERR_INVALID_ARG;
+        v->data[i] = static_cast<uint8_t*>(i ? c->v : c->k);
+        v->scale[i] = e4m3 ? (i ? c->v_scale : c->k_scale) : nullptr;
+        v->sp[i] = s[i].b * size;
+        v->sh[i] = s[i].h * size;
+        v->st[i] = s[i].t * size;
+    }
+    v->num_pages = c->num_pages;
+    v->page_size = c->page_size;
+    v->Hkv = c->Hkv;
+    v->D = c->D;
+    v->e4m3 = e4m3;
+    return ATTN_OK;
+}
+
+attn_status launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+template <int D>
+attn_status launch_rope(const RopeParams& prm, int mode, long long tokens, cudaStream_t stream) {
+    constexpr int RPI = ROPE_THREADS / (D / 8);
+    RopeParams p = prm;
+    const int rows = p.op[0].H + p.op[1].H;
+    // Few tokens: their heads are spread over blocks until there are about four blocks per SM.
+    const int steps = (rows + RPI - 1) / RPI;
+    long long ny = tokens >= 592 ? 1 : 592 / tokens;
+    if (ny > steps) ny = steps;
+    if (ny > 65535) ny = 65535;
+    p.rows_per_y = static_cast<int>((steps + ny - 1) / ny) * RPI;
+    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>((rows + p.rows_per_y - 1) / p.rows_per_y));
+    if (mode == ROPE_INTERLEAVED) qk_norm_rope_kernel<D, ROPE_INTERLEAVED><<<grid, ROPE_THREADS, 0, stream>>>(p);
+    else if (mode == ROPE_HALF) qk_norm_rope_kernel<D, ROPE_HALF><<<grid, ROPE_THREADS, 0, stream>>>(p);
+    else qk_norm_rope_kernel<D, ROPE_HALF_SCALAR><<<grid, ROPE_THREADS, 0, stream>>>(p);
+    return launched();
+}
+
+template <int D>
+attn_status launch_write(const CacheWriteParams& p, cudaStream_t stream) {
+    constexpr int ROWS = CACHE_THREADS / (D / 8) * CACHE_WRITE_U;
+    const long long grid = (p.rows + ROWS - 1) / ROWS;
+    if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    if (p.c.e4m3) cache_write_kernel<D, true><<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
+    else cache_write_kernel<D, false><<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
+    return launched();
+}
+
+template <int D>
+attn_status launch_read(const CacheReadParams& prm, int B, cudaStream_t stream) {
+    constexpr int ROWS = CACHE_THREADS / (D / 8) * CACHE_READ_U;
+    CacheReadParams p = prm;
+    const long long n_rb = (static_cast<long long>(p.Tk) + ROWS - 1) / ROWS;
+    const long long grid = n_rb * B * p.c.Hkv;
+    if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    p.n_rb = static_cast<int>(n_rb);
+    if (p.c.e4m3) cache_read_kernel<D, true><<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
+    else cache_read_kernel<D, false><<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
+    return launched();
+}
+
+template <int D>
+attn_status launch_paged(const PagedParams& p, cudaStream_t stream) {
+    const long long grid = (static_cast<long long>(p.B) * p.Hq * p.max_q + 3) / 4;
+    if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    if (p.c.e4m3) paged_simple_kernel<D, true><<<static_cast<unsigned>(grid), 128, 0, stream>>>(p);
+    else paged_simple_kernel<D, false><<<static_cast<unsigned>(grid), 128, 0, stream>>>(p);
+    return launched();
+}
+
+#define ATTN_BY_HEAD_DIM(D, CALL)          \
+    switch (D) {                           \
+        case 32: return CALL(32);          \
+        case 64: return CALL(64);          \
+        case 128: return CALL(128);        \
+        default: return CALL(256);         \
+    }
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_qk_norm_rope(const attn_rope_operand* q, const attn_rope_operand* k, const int32_t* positions,
+                              const double* inv_freq, int B, int T, int D, int R, int interleaved, float eps,
+                              float attn_factor, cudaStream_t stream) {
+    if (!q || !q->x || B <= 0 || T <= 0 || D <= 0) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(B) * T > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    if (R < 0 || R > D || (R & 1) || !isfinite(eps) || eps < 0.0f || !isfinite(attn_factor)) return ATTN_ERR_INVALID_ARG;
+    if (R > 0 && (!positions || !aligned(positions, 4) || !inv_freq || !aligned(inv_freq, 8))) return ATTN_ERR_INVALID_ARG;
+    if (!head_dim_ok(D)) return ATTN_ERR_UNSUPPORTED;
+    RopeParams p;
+    memset(&p, 0, sizeof p);
+    const attn_rope_operand* ops[2] = {q, k != nullptr && k->x != nullptr ? k : nullptr};
+    for (int i = 0; i < 2; ++i) {
+        const attn_rope_operand* o = ops[i];
+        if (o == nullptr) continue;
+        if (!o->y || !aligned16(o->x) || !aligned16(o->y) || o->H <= 0) return ATTN_ERR_INVALID_ARG;
+        if (o->weight && !aligned16(o->weight)) return ATTN_ERR_INVALID_ARG;
+        Strides x, y;
+        if (!strides_of(&o->x_strides, o->H, T, D, &x) || !strides_of(&o->y_strides, o->H, T, D, &y))
+            return ATTN_ERR_INVALID_ARG;
+        p.op[i] = {static_cast<const __nv_bfloat16*>(o->x), static_cast<__nv_bfloat16*>(o->y), o->weight, o->H,
+                   o->weight_fp32 != 0, x.b, x.h, x.t, y.b, y.h, y.t};
+    }
+    if (static_cast<long long>(p.op[0].H) + p.op[1].H > 65535) return ATTN_ERR_INVALID_ARG;
+    attn_status st = check_device();
+    if (st != ATTN_OK) return st;
+    p.pos = positions;
+    p.inv_freq = inv_freq;
+    p.T = T;
+    p.R = R;
+    p.eps = eps;
+    p.factor = attn_factor;
+    const int mode = interleaved ? ROPE_INTERLEAVED : (R & 7) == 0 ? ROPE_HALF : ROPE_HALF_SCALAR;
+    const long long tokens = static_cast<long long>(B) * T;
+#define CALL(DD) launch_rope<DD>(p, mode, tokens, stream)
+    ATTN_BY_HEAD_DIM(D, CALL)
+#undef CALL
+}
+
+attn_status attn_cache_write(const attn_cache* cache, const void* k, const void* v, const attn_strides* k_strides,
+                             const attn_strides* v_strides, const int32_t* slots, int T, cudaStream_t stream) {
+    CacheWriteParams p;
+    memset(&p, 0, sizeof p);
+    attn_status st = cache_view(cache, &p.c);
+    if (st != ATTN_OK) return st;
+    if (!k || !v || !aligned16(k) || !aligned16(v) || !slots || !aligned(slots, 4) || T <= 0) return ATTN_ERR_INVALID_ARG;
+    Strides s[2];
+    if (!token_strides_of(k_strides, cache->Hkv, cache->D, &s[0]) || !token_strides_of(v_strides, cache->Hkv, cache->D, &s[1]))
+        return ATTN_ERR_INVALID_ARG;
+    if ((st = check_device()) != ATTN_OK) return st;
+    p.src[0] = static_cast<const __nv_bfloat16*>(k);
+    p.src[1] = static_cast<const __nv_bfloat16*>(v);
+    for (int i = 0; i < 2; ++i) {
+        p.st[i] = s[i].t;
+        p.sh[i] = s[i].h;
+    }
+    p.slots = slots;
+    p.rows = 2LL * T * cache->Hkv;
+#define CALL(DD) launch_write<DD>(p, stream)
+    ATTN_BY_HEAD_DIM(cache->D, CALL)
+#undef CALL
+}
+
+attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table, int64_t table_stride, int max_pages,
+                            const int32_t* kv_len, void* k_out, void* v_out, const attn_strides* k_strides,
+                            const attn_strides* v_strides, int B, int Tk, cudaStream_t stream) {
+    CacheReadParams p;
+    memset(&p, 0, sizeof p);
+    attn_status st = cache_view(cache, &p.c);
+    if (st != ATTN_OK) return st;
+    if (!block_table || !aligned(block_table, 4) || !kv_len || !aligned(kv_len, 4)) return ATTN_ERR_INVALID_ARG;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return ATTN_ERR_INVALID_ARG;
+    if (B <= 0 || Tk <= 0 || max_pages <= 0 || table_stride < 0) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(B) * cache->Hkv > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    Strides s[2];
+    if (!strides_of(k_strides, cache->Hkv, Tk, cache->D, &s[0]) || !strides_of(v_strides, cache->Hkv, Tk, cache->D, &s[1]))
+        return ATTN_ERR_INVALID_ARG;
+    if ((st = check_device()) != ATTN_OK) return st;
+    p.dst[0] = static_cast<__nv_bfloat16*>(k_out);
+    p.dst[1] = static_cast<__nv_bfloat16*>(v_out);
+    for (int i = 0; i < 2; ++i) {
+        p.sb[i] = s[i].b;
+        p.sh[i] = s[i].h;
+        p.st[i] = s[i].t;
+    }
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.kv_len = kv_len;
+    p.max_pages = max_pages;
+    p.Tk = Tk;
+#define CALL(DD) launch_read<DD>(p, B, stream)
+    ATTN_BY_HEAD_DIM(cache->D, CALL)
+#undef CALL
+}
+
+size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int max_q,
+                                  int num_splits) {
+    (void)B, (void)T, (void)Hq, (void)Hkv, (void)D, (void)page_size, (void)max_pages, (void)max_q, (void)num_splits;
+    return 0;
+}
+
+attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_strides* q_strides,
+                           const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* kv_len,
+                           const int32_t* q_start, void* out, const attn_strides* out_strides, float* lse,
+                           void* workspace, int B, int T, int Hq, int max_q, int causal, int num_splits, float scale,
+                           cudaStream_t stream) {
+    PagedParams p;
+    memset(&p, 0, sizeof p);
+    attn_status st = cache_view(cache, &p.c);
+    if (st != ATTN_OK) return st;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || !block_table || !aligned(block_table, 4)) return ATTN_ERR_INVALID_ARG;
+    if (!kv_len || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
+    if (B <= 0 || T <= 0 || Hq <= 0 || max_q <= 0 || max_pages <= 0 || table_stride < 0) return ATTN_ERR_INVALID_ARG;
+    if (Hq % cache->Hkv != 0 || Hq / cache->Hkv > 128 || (q_start == nullptr && B != T)) return ATTN_ERR_INVALID_ARG;
+    if (!isfinite(scale) || num_splits < 0 || num_splits > 256) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(B) * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    const long long cap = static_cast<long long>(max_pages) * cache->page_size;
+    if (cap > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    Strides sq, so;
+    if (!token_strides_of(q_strides, Hq, cache->D, &sq) || !token_strides_of(out_strides, Hq, cache->D, &so))
+        return ATTN_ERR_INVALID_ARG;
+    if ((st = check_device()) != ATTN_OK) return st;
+    (void)workspace;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.q_t = sq.t;
+    p.q_h = sq.h;
+    p.out_t = so.t;
+    p.out_h = so.h;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.kv_len = kv_len;
+    p.q_start = q_start;
+    p.B = B;
+    p.T = T;
+    p.Hq = Hq;
+    p.G = Hq / cache->Hkv;
+    p.max_q = q_start == nullptr ? 1 : max_q < T ? max_q : T;
+    p.kv_cap = static_cast<int>(cap);
+    p.causal = causal != 0;
+    p.scale_log2 = scale * 1.44269504088896340736f;
+#define CALL(DD) launch_paged<DD>(p, stream)
+    ATTN_BY_HEAD_DIM(cache->D, CALL)
+#undef CALL
+}
+
+}  // extern "C"

@@ -1,0 +1,350 @@
+"""Serving around the prefix-masked attention: q and k as a projection leaves them, a paged
+key/value cache, and attention of each sequence's new tokens over its pages.
+
+    q, k = attn_qk_norm_rope(q, k, positions, inv_freq, q_weight=wq, k_weight=wk)
+    attn_cache_write(k, v, slots, k_cache, v_cache)
+    out, lse = attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start, max_q)
+
+``attn_cache_read`` copies sequences back from their pages into the [B, H, T, D] prefix
+layout of ``attn_prefix_fwd``.  ``PagedCache`` holds a pool of pages and runs the three
+calls in order.  As in the rest of the package, every step runs in the C library; this
+module checks and marshals arguments.
+"""
+from __future__ import annotations
+
+import math
+import struct
+
+import torch
+
+from . import _binding
+from ._binding import _check, lib
+
+CACHE_BF16 = 0
+CACHE_E4M3 = 1
+
+_CACHE = struct.Struct("4P6q5i4x")      # attn_cache
+_OPERAND = struct.Struct("3P2i6q")      # attn_rope_operand
+_STRIDES = struct.Struct("3q")          # attn_strides
+
+
+def _call(name, device, *args):
+    """The library's function `name` on the device's current stream, with that device current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
+    _check(st, name)
+
+
+def _strides4(t, name):
+    """(page or batch, head, row) strides of a [*, H, T, D] view; a dim of size 1 gets a stride that
+    is never used but passes the checks."""
+    if t.stride(3) != 1 and t.shape[3] != 1:
+        raise ValueError(f"{name}: the head dim must be contiguous (stride 1)")
+    B, H, T, D = t.shape
+    b, h, s, _ = t.stride()
+    s = D if T == 1 else s
+    h = T * D if H == 1 else h
+    b = H * T * D if B == 1 else b
+    if s == 0:
+        raise ValueError(f"{name}: rows may not be broadcast")
+    return b, h, s
+
+
+def _strides3(t, name):
+    """(0, head, token) strides of a [T, H, D] view."""
+    if t.stride(2) != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}: the head dim must be contiguous (stride 1)")
+    T, H, D = t.shape
+    s, h, _ = t.stride()
+    s = H * D if T == 1 else s
+    h = D if H == 1 else h
+    if s == 0:
+        raise ValueError(f"{name}: rows may not be broadcast")
+    return 0, h, s
+
+
+def _bf16(t, dim, name):
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() not in dim:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor of {' or '.join(map(str, dim))} dimensions")
+
+
+def _int32(t, shape, name, device):
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+
+
+def _not_overlapping(t, name):
+    """Rows that are written must not share memory (a broadcast head or batch)."""
+    if any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
+        raise ValueError(f"{name} may not be a broadcast view")
+
+
+# ---------------------------------------------------------------------------------- norm and rotation
+def rope_inv_freq(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_context=None, beta_fast=32.0,
+                  beta_slow=1.0, device="cuda"):
+    """(inv_freq, attn_factor) for attn_qk_norm_rope: fp64 [rotary_dim / 2] angles per position.
+
+    scaling, for contexts `factor` times as long as the trained one:
+      None      base^(-2i / rotary_dim)
+      "linear"  the same divided by factor (positions interpolated)
+      "ntk"     base * factor^(rotary_dim / (rotary_dim - 2)): the slowest pair interpolated, the fastest kept
+      "yarn"    by parts: pairs that turn more than beta_fast times over original_context are kept, those
+                that turn less than beta_slow times are divided by factor, a linear ramp in the number
+                of turns between; attn_factor 0.1 ln(factor) + 1 on the rotated values
+    """
+    R = int(rotary_dim)
+    if R < 2 or R % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not factor >= 1.0 or not base > 0.0:
+        raise ValueError("factor must be at least 1 and base positive")
+    i = torch.arange(0, R, 2, dtype=torch.float64)
+    attn_factor = 1.0
+    if scaling == "ntk":
+        if R < 4:
+            raise ValueError("scaling 'ntk' needs rotary_dim >= 4")
+        base = base * factor ** (R / (R - 2))
+    f = float(base) ** (-i / R)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if not original_context:
+            raise ValueError("scaling 'yarn' needs original_context")
+        turns = original_context * f / (2 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        attn_factor = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device), attn_factor
+
+
+def _operand(x, y, weight, name):
+    if weight is not None:
+        if (weight.dtype not in (torch.bfloat16, torch.float32) or weight.device != x.device
+                or tuple(weight.shape) != (x.shape[-1],) or not weight.is_contiguous()):
+            raise ValueError(f"{name}_weight must be a contiguous bf16 or fp32 tensor [D] on {x.device}")
+    st = _strides4 if x.dim() == 4 else _strides3
+    return _OPERAND.pack(x.data_ptr(), y.data_ptr(), 0 if weight is None else weight.data_ptr(), x.shape[-3 if x.dim() == 4 else -2],
+                         0 if weight is None else weight.dtype == torch.float32, *st(x, name), *st(y, name + "_out"))
+
+
+def _rope_out(x, out, name):
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError(f"{name}_out must be a bf16 tensor of {name}'s shape on {x.device}")
+    _not_overlapping(out, name + "_out")
+    return out
+
+
+def attn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                      attn_factor=1.0, q_out=None, k_out=None):
+    """Per-head RMS norm and rotation by position (attn_qk_norm_rope): returns (q_out, k_out).
+
+    q: bf16 [T, Hq, D] (tokens first) or [B, H, T, D], views included (e.g. slices of a packed
+    projection); k: the same with its own head count, or None.  positions: int32 [T], or [B, T].
+    inv_freq: fp64 [R/2] (rope_inv_freq), R <= D elements of each head are rotated; None: norm only.
+    A weight that is None leaves its operand unnormalised.  q_out may be q (in place)."""
+    _bf16(q, (3, 4), "q")
+    four = q.dim() == 4
+    B, T = (q.shape[0], q.shape[2]) if four else (1, q.shape[0])
+    D = q.shape[-1]
+    R = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != q.device or not inv_freq.is_contiguous():
+            raise ValueError(f"inv_freq must be a contiguous fp64 tensor [R / 2] on {q.device}")
+        R = 2 * inv_freq.numel()
+        _int32(positions, (B, T) if four else (T,), "positions", q.device)
+    if k is not None:
+        _bf16(k, (q.dim(),), "k")
+        if k.device != q.device or k.shape[-1] != D or (k.shape[0], k.shape[2] if four else 0) != (q.shape[0], T if four else 0):
+            raise ValueError("k must have q's tokens, head dim and device")
+    if q.numel() == 0 or (k is not None and k.numel() == 0):
+        raise ValueError("q and k may not be empty")
+    q_out = _rope_out(q, q_out, "q")
+    op_q = _operand(q, q_out, q_weight, "q")
+    op_k = None
+    if k is not None:
+        k_out = _rope_out(k, k_out, "k")
+        op_k = _operand(k, k_out, k_weight, "k")
+    _call("attn_qk_norm_rope", q.device, op_q, op_k, positions.data_ptr() if R else None,
+          inv_freq.data_ptr() if R else None, B, T, D, R, bool(interleaved), eps, attn_factor)
+    return q_out, k_out if k is not None else None
+
+
+# ---------------------------------------------------------------------------------- cache
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """The packed attn_cache of a pool's tensors."""
+    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+    if not k_cache.is_cuda or k_cache.dim() != 4 or not (e4m3 or k_cache.dtype == torch.bfloat16):
+        raise ValueError("k_cache must be a bf16 or float8_e4m3fn CUDA tensor [num_pages, Hkv, page_size, D]")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
+        raise ValueError("v_cache must match k_cache")
+    P, H, page, D = k_cache.shape
+    if e4m3:
+        for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if (s is None or s.dtype != torch.uint8 or s.device != k_cache.device or s.shape != k_cache.shape[:3]
+                    or not s.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous uint8 tensor [num_pages, Hkv, page_size]")
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("bf16 pages have no scales")
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if e4m3 else 0,
+                       v_scale.data_ptr() if e4m3 else 0, *_strides4(k_cache, "k_cache"),
+                       *_strides4(v_cache, "v_cache"), P, page, H, D, CACHE_E4M3 if e4m3 else CACHE_BF16)
+
+
+def attn_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
+    """Stores rows k, v (bf16 [T, Hkv, D], views included) at slots (int32 [T], page * page_size + row;
+    negative: skipped) of the pages (attn_cache_write).
+
+    k_cache, v_cache: [num_pages, Hkv, page_size, D], views of other layouts included, bf16, or
+    float8_e4m3fn with k_scale, v_scale uint8 [num_pages, Hkv, page_size].  The slots of one call must
+    be distinct."""
+    c = _cache(k_cache, v_cache, k_scale, v_scale)
+    _not_overlapping(k_cache, "k_cache")
+    _not_overlapping(v_cache, "v_cache")
+    _bf16(k, (3,), "k")
+    _bf16(v, (3,), "v")
+    T = k.shape[0]
+    if v.shape != k.shape or tuple(k.shape[1:]) != (k_cache.shape[1], k_cache.shape[3]):
+        raise ValueError("k and v must be [T, Hkv, D] with the cache's Hkv and D")
+    if k.device != k_cache.device or v.device != k_cache.device:
+        raise ValueError("all tensors must be on one device")
+    _int32(slots, (T,), "slots", k.device)
+    if T == 0:
+        return
+    _call("attn_cache_write", k.device, c, k.data_ptr(), v.data_ptr(), _STRIDES.pack(*_strides3(k, "k")),
+          _STRIDES.pack(*_strides3(v, "v")), slots.data_ptr(), T)
+
+
+def _table(block_table, kv_len, device):
+    if block_table.dtype != torch.int32 or block_table.device != device or block_table.dim() != 2 or (
+            block_table.stride(1) != 1 and block_table.shape[1] != 1):
+        raise ValueError(f"block_table must be an int32 tensor [B, max_pages] on {device} with contiguous rows")
+    B, n = block_table.shape
+    if B == 0 or n == 0:
+        raise ValueError("block_table may not be empty")
+    _int32(kv_len, (B,), "kv_len", device)
+    return B, n
+
+
+def attn_cache_read(k_cache, v_cache, block_table, kv_len, Tk=None, k_scale=None, v_scale=None, k_out=None, v_out=None):
+    """Sequences read back from their pages as contiguous prefixes (attn_cache_read): (k, v) bf16
+    [B, Hkv, Tk, D], as attn_prefix_fwd takes them.
+
+    block_table: int32 [B, max_pages]; kv_len: int32 [B].  Rows at or beyond kv_len[b] are left as
+    they were (uninitialised where k_out, v_out are made here).  Tk: by default max_pages * page_size."""
+    c = _cache(k_cache, v_cache, k_scale, v_scale)
+    B, n = _table(block_table, kv_len, k_cache.device)
+    _, H, page, D = k_cache.shape
+    if k_out is None or v_out is None:
+        if k_out is not None or v_out is not None:
+            raise ValueError("k_out and v_out are given together")
+        shape = (B, H, n * page if Tk is None else int(Tk), D)
+        k_out, v_out = (torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) for _ in range(2))
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if (t.dim() != 4 or t.shape[:2] != (B, H) or t.shape[3] != D or t.dtype != torch.bfloat16
+                or t.device != k_cache.device or t.shape != k_out.shape or Tk not in (None, t.shape[2])):
+            raise ValueError(f"{name} must be a bf16 tensor [B, Hkv, Tk, D] on {k_cache.device}")
+        _not_overlapping(t, name)
+    if k_out.shape[2] == 0:
+        return k_out, v_out
+    _call("attn_cache_read", k_cache.device, c, block_table.data_ptr(), block_table.stride(0), n, kv_len.data_ptr(),
+          k_out.data_ptr(), v_out.data_ptr(), _STRIDES.pack(*_strides4(k_out, "k_out")),
+          _STRIDES.pack(*_strides4(v_out, "v_out")), B, k_out.shape[2])
+    return k_out, v_out
+
+
+# ---------------------------------------------------------------------------------- attention
+def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q=None, causal=True, scale=None,
+                   k_scale=None, v_scale=None, num_splits=0, workspace=None, out=None, lse=None, need_lse=True):
+    """Attention of each sequence's new tokens over its pages (attn_paged_fwd): (out bf16 [T, Hq, D],
+    lse fp32 [T, Hq]).
+
+    q: bf16 [T, Hq, D], sequence b's rows at [q_start[b], q_start[b+1]) (int32 [B + 1]); without
+    q_start one row per sequence.  max_q: an upper bound on a sequence's rows (by default T).  The
+    pages hold the new tokens' keys too; with `causal`, the rows are the last positions of their
+    sequence.  Rows outside every sequence are left as they were (uninitialised where out is made
+    here).  num_splits: 0 to have it chosen; workspace: a buffer of attn_paged_workspace_bytes,
+    allocated here when not given."""
+    c = _cache(k_cache, v_cache, k_scale, v_scale)
+    B, n = _table(block_table, kv_len, k_cache.device)
+    _bf16(q, (3,), "q")
+    T, Hq, D = q.shape
+    _, Hkv, page, Dc = k_cache.shape
+    dev = q.device
+    if D != Dc or dev != k_cache.device:
+        raise ValueError("q must have the cache's head dim and device")
+    if Hq == 0 or Hkv == 0 or Hq % Hkv:
+        raise ValueError("q's head count must be a multiple of the cache's")
+    if q_start is not None:
+        _int32(q_start, (B + 1,), "q_start", dev)
+    elif T != B:
+        raise ValueError("without q_start, q must have one row per sequence")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev:
+        raise ValueError("out must be a bf16 tensor of q's shape on q's device")
+    else:
+        _not_overlapping(out, "out")
+    if lse is not None:
+        if tuple(lse.shape) != (T, Hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 tensor [T, Hq] on q's device")
+    elif need_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    if T == 0:
+        return out, lse
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    max_q = 1 if q_start is None else T if max_q is None else int(max_q)
+    need = lib().attn_paged_workspace_bytes(B, T, Hq, Hkv, D, page, n, max_q, num_splits)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif need and (workspace.device != dev or not workspace.is_contiguous()
+                   or workspace.numel() * workspace.element_size() < need):
+        raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {need} bytes")
+    _call("attn_paged_fwd", dev, c, q.data_ptr(), _STRIDES.pack(*_strides3(q, "q")), block_table.data_ptr(),
+          block_table.stride(0), n, kv_len.data_ptr(), None if q_start is None else q_start.data_ptr(), out.data_ptr(),
+          _STRIDES.pack(*_strides3(out, "out")), None if lse is None else lse.data_ptr(),
+          workspace.data_ptr() if need else None, B, T, Hq, max_q, bool(causal), num_splits, scale)
+    return out, lse
+
+
+class PagedCache:
+    """A pool of key/value pages and the serving step over it.
+
+    quantised: e4m3 rows with a power-of-two scale each, otherwise bf16.  Which page belongs to
+    which sequence is the caller's (block_table, slots)."""
+
+    def __init__(self, num_pages, page_size, Hkv, D, quantised=False, device=None):
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        shape = (int(num_pages), int(Hkv), int(page_size), int(D))
+        dtype = torch.float8_e4m3fn if quantised else torch.bfloat16
+        self.page_size = int(page_size)
+        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8 if quantised else dtype, device=dev).view(dtype)
+                          for _ in range(2))
+        self.scales = {}
+        if quantised:
+            self.scales = {n: torch.full(shape[:3], 127, dtype=torch.uint8, device=dev) for n in ("k_scale", "v_scale")}
+
+    def write(self, k, v, slots):
+        attn_cache_write(k, v, slots, self.k, self.v, **self.scales)
+
+    def read(self, block_table, kv_len, Tk=None):
+        return attn_cache_read(self.k, self.v, block_table, kv_len, Tk, **self.scales)
+
+    def attend(self, q, block_table, kv_len, q_start=None, max_q=None, **kw):
+        return attn_paged_fwd(q, self.k, self.v, block_table, kv_len, q_start, max_q, **self.scales, **kw)
+
+    def step(self, q, k, v, positions, slots, block_table, kv_len, q_start=None, max_q=None, inv_freq=None, rope=None,
+             **kw):
+        """One serving step of new tokens: q [T, Hq, D], k, v [T, Hkv, D] as the projection leaves
+        them.  Norm and rotation (`rope`: further arguments of attn_qk_norm_rope), the new rows into
+        their slots, attention over the pages.  kv_len counts the new tokens.  Returns (out, lse)."""
+        q, k = attn_qk_norm_rope(q, k, positions, inv_freq, **(rope or {}))
+        self.write(k, v, slots)
+        return self.attend(q, block_table, kv_len, q_start, max_q, **kw)

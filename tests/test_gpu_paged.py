@@ -1,0 +1,311 @@
+"""attn_paged_fwd against a 64-bit implementation over the same pages (tolerances: paged_reference)."""
+import math
+import random
+
+import pytest
+import torch
+
+import paged_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kp():
+    from key_prefix_masked_b200 import build
+    build.build()
+    import key_prefix_masked_b200 as kp
+    torch.cuda.init()
+    assert kp.device_status() == kp.ATTN_OK
+    return kp
+
+
+def make(kv, n_q, Hq, Hkv, D, page, e4m3, seed=0, std=1.0, slack=0, layout="head", spread=0):
+    """A batch on the CPU: pages whose slots behind each sequence are NaN, and unused table entries that
+    name no page.  slack: rows of q in front of the first and behind the last sequence."""
+    g = torch.Generator().manual_seed(seed)
+    rnd = random.Random(seed)
+    need = [-(-n // page) for n in kv]
+    P = sum(need) + 2
+    order = list(range(P))
+    rnd.shuffle(order)
+    table = torch.full((len(kv), max(max(need), 1) + 1), -1, dtype=torch.int32)
+    owned = torch.zeros(P, page, dtype=torch.bool)
+    at = 0
+    for b, m in enumerate(need):
+        table[b, :m] = torch.tensor(order[at:at + m], dtype=torch.int32)
+        for j in range(m):
+            owned[order[at + j], :min(page, kv[b] - j * page)] = True
+        at += m
+    c = dict(kv=kv, causal=True, scale=D ** -0.5, table=table, Hq=Hq, Hkv=Hkv, D=D)
+    for name in ("k", "v"):
+        x = (torch.randn(P, Hkv, page, D, generator=g) * std).to(torch.bfloat16)
+        if spread:
+            x = (x.float() * 2.0 ** torch.randint(-spread, spread + 1, (P, Hkv, page, 1), generator=g)).to(torch.bfloat16)
+        if e4m3:
+            codes = x.float()
+            m, e = torch.frexp(codes.abs().amax(-1))
+            e = e - 9 + (m > 0.875).int()
+            s = (e + 127).to(torch.uint8)
+            codes = (codes * 2.0 ** (-e[..., None])).to(torch.float8_e4m3fn).view(torch.uint8)
+            codes[~owned[:, None, :].expand(P, Hkv, page)] = 0x7F
+            s[~owned[:, None, :].expand(P, Hkv, page)] = 255
+            c[name + "s"], c[name + "vals"] = s, torch.nan_to_num(ref.dequantise(codes, s))
+            c[name] = codes
+        else:
+            x[~owned[:, None, :].expand(P, Hkv, page)] = math.nan
+            c[name + "s"], c[name + "vals"], c[name] = None, torch.nan_to_num(x.double()), x
+        if layout == "slot":
+            c[name] = c[name].transpose(1, 2).contiguous().transpose(1, 2)
+    start = [slack]
+    for n in n_q:
+        start.append(start[-1] + n)
+    c["start"] = start
+    c["q"] = (torch.randn(start[-1] + slack, Hq, D, generator=g) * std).to(torch.bfloat16)
+    return c
+
+
+def call(kp, c, **kw):
+    dc = [c[n].cuda() for n in ("k", "v")]
+    ds = {}
+    if c["ks"] is not None:
+        dc = [x.view(torch.float8_e4m3fn) for x in dc]
+        ds = dict(k_scale=c["ks"].cuda(), v_scale=c["vs"].cuda())
+    T, Hq, D = c["q"].shape
+    out = torch.full((T, Hq, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), 5.0, device="cuda")
+    args = dict(q_start=torch.tensor(c["start"], dtype=torch.int32).cuda(), max_q=max(b - a for a, b in zip(c["start"], c["start"][1:])),
+                causal=c["causal"], scale=c["scale"], out=out, lse=lse)
+    args.update(kw)
+    args["max_q"] = max(args["max_q"] or 1, 1)
+    return kp.attn_paged_fwd(c["q"].cuda(), dc[0], dc[1], c["table"].cuda(), torch.tensor(c["kv"], dtype=torch.int32).cuda(), **ds, **args)
+
+
+def check(kp, c, **kw):
+    out, lse = call(kp, c, **kw)
+    assert kp.device_status() == kp.ATTN_OK
+    r = ref.paged(c["q"], c["kvals"], c["vvals"], c["table"], c["kv"], c["start"], c["causal"], c["scale"])
+    ref.assert_paged_close(out, lse, r)
+    outside = torch.isnan(r[1])                    # rows of no sequence stay as they were
+    assert (out.cpu()[outside] == 3.0).all() and (lse.cpu()[outside] == 5.0).all()
+    return out, lse
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv,page", [(4, 4, 16), (8, 2, 8), (6, 2, 24), (16, 1, 64), (5, 1, 256), (32, 1, 16)])
+def test_single_tokens(kp, D, Hq, Hkv, page, e4m3):
+    kv = [1, 0, 15, 16, 17, 64, 127, 128, 129, 700]
+    c = make(kv, [1] * len(kv), Hq, Hkv, D, page, e4m3, seed=D + Hq)
+    check(kp, c)
+    assert torch.equal(call(kp, c)[0], call(kp, c, q_start=None, max_q=None)[0])
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv,page", [(2, 2, 16), (6, 2, 32), (5, 1, 8), (8, 1, 128)])
+def test_chunks(kp, D, Hq, Hkv, page, causal, e4m3):
+    """Chunks of 0 to 300 rows; sequences shorter than their chunk (rows without keys), and empty ones."""
+    kv = [300, 0, 129, 128, 40, 1, 515, 90]
+    n_q = [300, 3, 1, 128, 60, 2, 77, 0]
+    c = make(kv, n_q, Hq, Hkv, D, page, e4m3, seed=D + Hq + page, slack=3)
+    c["causal"] = causal
+    check(kp, c)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("splits", [1, 2, 3, 7, 256])
+@pytest.mark.parametrize("n_q", [1, 9, 150])
+def test_splits(kp, n_q, splits, e4m3):
+    kv = [1500, 130, 0, 1]
+    c = make(kv, [n_q] * 4, 4, 2, 64, 16, e4m3, seed=splits)
+    check(kp, c, num_splits=splits)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 3, 7, 64, 128])
+def test_head_groups(kp, G, D):
+    for n_q in (1, 2, 5, 40):
+        c = make([333, 50], [n_q, min(n_q, 3)], G, 1, D, 16, False, seed=G + n_q)
+        check(kp, c)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n_q", [1, 33, 200])
+def test_layouts(kp, n_q, e4m3):
+    """Pages with heads innermost ([P, page, H, D] memory), q out of a packed projection, out in another layout."""
+    c = make([400, 7, 250], [n_q, 2, 1], 6, 2, 64, 16, e4m3, seed=n_q, layout="slot")
+    want, wl = check(kp, c)
+    T, Hq, D = c["q"].shape
+    packed = torch.zeros(T, Hq + 4, D, dtype=torch.bfloat16)
+    packed[:, 2:2 + Hq] = c["q"]
+    d = dict(c)
+    d["q"] = packed.cuda()[:, 2:2 + Hq]
+    out = torch.zeros(Hq, T, D, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    lse = torch.zeros(T, Hq, device="cuda")
+    got, gl = call(kp, d, out=out, lse=lse)
+    live = slice(c["start"][0], c["start"][-1])
+    assert torch.equal(got[live], want[live]) and torch.equal(gl[live], wl[live])
+
+
+@pytest.mark.parametrize("n_q", [1, 100])
+def test_scales_and_spread(kp, n_q):
+    """Zero and negative scales; rows whose magnitudes differ by 2^16; an e4m3 cache with scales beyond 2^7."""
+    for scale in (0.0, -0.3, 2.0):
+        c = make([200, 65], [n_q, 1], 4, 2, 64, 16, False, seed=4)
+        c["scale"] = scale
+        check(kp, c)
+    c = make([300], [n_q], 4, 2, 64, 16, True, seed=5, spread=8)
+    c["scale"] = 1e-3
+    check(kp, c)
+    c = make([300], [n_q], 4, 2, 64, 16, True, seed=6, std=1e6)
+    c["q"] = (c["q"].float() * 1e-6).to(torch.bfloat16)
+    c["scale"] = 1e-6
+    check(kp, c)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n_q", [1, 140])
+def test_rising_scores(kp, n_q, e4m3):
+    """Scores that grow along the keys, so that the running maximum moves in every tile."""
+    c = make([900], [n_q], 2, 1, 64, 16, e4m3, seed=8)
+    ramp = torch.ones(64, dtype=torch.float64)
+    for j in range(900):
+        row = (int(c["table"][0, j // 16]), 0, j % 16)
+        val = torch.tensor(j / 900 * 3.0, dtype=torch.bfloat16)
+        if e4m3:
+            codes, s = ref.quantise(val.expand(1, 64))
+            c["k"][row], c["ks"][row] = codes[0], s[0]
+            c["kvals"][row] = ref.dequantise(codes, s)[0]
+        else:
+            c["k"][row], c["kvals"][row] = val * ramp, val.double() * ramp
+    c["q"] = torch.ones_like(c["q"])
+    c["scale"] = 1.0
+    check(kp, c)
+
+
+def test_ranges_are_clamped_and_flagged(kp):
+    c = make([100, 60], [5, 4], 4, 2, 64, 16, False, seed=11)
+    d = dict(c)
+    d["kv"] = [100, 60]
+    bad_table = c["table"].clone()
+    bad_table[0, 1] = 10 ** 6
+    d["table"] = bad_table
+    out, lse = call(kp, d)
+    assert kp.device_status() == kp.ATTN_ERR_CACHE_RANGE       # that page's keys and values count as zeros
+    r = ref.paged(c["q"], c["kvals"], c["vvals"], bad_table, c["kv"], c["start"], True, c["scale"])
+    ref.assert_paged_close(out, lse, r)
+    for kv in (-3, 16 * c["table"].shape[1] + 1):
+        d = dict(c)
+        d["kv"] = [kv, 60]
+        d["table"] = c["table"].clamp_min(0)
+        call(kp, d)
+        assert kp.device_status() == kp.ATTN_ERR_KVLEN_RANGE
+    for start in ([0, 9, 5], [-1, 5, 9], [0, 5, 99]):
+        d = dict(c)
+        call(kp, d, q_start=torch.tensor(start, dtype=torch.int32).cuda(), max_q=9)
+        assert kp.device_status() == kp.ATTN_ERR_CACHE_RANGE
+    out, lse = call(kp, c, max_q=3)                             # rows beyond max_q are not computed
+    assert kp.device_status() == kp.ATTN_ERR_CACHE_RANGE
+    full, _ = call(kp, c)
+    assert torch.equal(out[:3], full[:3]) and (out[3:5] == 3.0).all() and torch.equal(out[5:8], full[5:8])
+    assert kp.device_status() == kp.ATTN_OK
+
+
+@pytest.mark.parametrize("n_q", [1, 130])
+def test_repeats_graphs_and_streams_agree(kp, n_q):
+    c = make([2000, 31, 0, 700], [n_q, 1, 1, n_q], 8, 2, 128, 16, True, seed=12)
+    want, wl = call(kp, c)
+    for _ in range(2):
+        a, al = call(kp, c)
+        assert torch.equal(a, want) and torch.equal(al, wl)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        a, al = call(kp, c)
+    s.synchronize()
+    assert torch.equal(a, want) and torch.equal(al, wl)
+    dev = dict(q=c["q"].cuda(), k=c["k"].cuda().view(torch.float8_e4m3fn), v=c["v"].cuda().view(torch.float8_e4m3fn), ks=c["ks"].cuda(),
+               vs=c["vs"].cuda(), table=c["table"].cuda(), kv=torch.tensor(c["kv"], dtype=torch.int32).cuda(),
+               start=torch.tensor(c["start"], dtype=torch.int32).cuda())
+    outs = [torch.zeros_like(want) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, o in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            kp.attn_paged_fwd(dev["q"], dev["k"], dev["v"], dev["table"], dev["kv"], dev["start"], n_q, scale=c["scale"],
+                              k_scale=dev["ks"], v_scale=dev["vs"], out=o)
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    live = slice(0, c["start"][-1])
+    assert all(torch.equal(o[live], want[live]) for o in outs)
+    dev["kv"].copy_(torch.tensor([1000, 31, 5, 700], dtype=torch.int32))
+    d = dict(c)
+    d["kv"] = [1000, 31, 5, 700]
+    d["table"] = c["table"].clone()
+    d["table"][2, 0] = d["table"][0, -2]
+    dev["table"].copy_(d["table"])
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][live], call(kp, d)[0][live])
+    assert kp.device_status() == kp.ATTN_OK
+
+
+def test_a_whole_serving_step(kp):
+    """PagedCache.step over prompt chunks and single tokens, against the 64-bit chain."""
+    g = torch.Generator().manual_seed(20)
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    for quantised in (False, True):
+        cache = kp.PagedCache(20, page, Hkv, D, quantised=quantised)
+        table = torch.randperm(20, generator=g)[:18].view(2, 9).to(torch.int32)
+        inv, f = kp.rope_inv_freq(D, scaling="yarn", factor=4.0, original_context=64)
+        wq, wk = (torch.randn(D, generator=g).to(torch.bfloat16) + 1 for _ in range(2))
+        have = [0, 0]
+        kvals = torch.zeros(20, Hkv, page, D, dtype=torch.float64)
+        vvals = kvals.clone()
+        for n_q in ([40, 17], [1, 1], [5, 60], [1, 1]):
+            start = [0, n_q[0], sum(n_q)]
+            q, k, v = (torch.randn(sum(n_q), h, D, generator=g).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+            pos = torch.tensor([have[b] + i for b in range(2) for i in range(n_q[b])], dtype=torch.int32)
+            seq = [b for b in range(2) for _ in range(n_q[b])]
+            slots = torch.tensor([int(table[b, p // page]) * page + p % page for b, p in zip(seq, pos.tolist())], dtype=torch.int32)
+            have = [have[b] + n_q[b] for b in range(2)]
+            out, lse = cache.step(q.cuda(), k.cuda(), v.cuda(), pos.cuda(), slots.cuda(), table.cuda(),
+                                  torch.tensor(have, dtype=torch.int32).cuda(), torch.tensor(start, dtype=torch.int32).cuda(),
+                                  max(n_q), inv_freq=inv, rope=dict(q_weight=wq.cuda(), k_weight=wk.cuda(), attn_factor=f))
+            # the rotated rows as the kernel rounds them (compared with 64 bits in test_gpu_rope)
+            qr, kr = kp.attn_qk_norm_rope(q.cuda(), k.cuda(), pos.cuda(), inv, q_weight=wq.cuda(), k_weight=wk.cuda(), attn_factor=f)
+            for x, vals in ((kr.cpu(), kvals), (v, vvals)):
+                rows = ref.dequantise(*ref.quantise(x)) if quantised else x.double()
+                for t, s in enumerate(slots.tolist()):
+                    vals[s // page, :, s % page] = rows[t]
+            r = ref.paged(qr.cpu(), kvals, vvals, table, have, start, True, D ** -0.5)
+            ref.assert_paged_close(out, lse, r)
+            kb, vb = cache.read(table.cuda(), torch.tensor(have, dtype=torch.int32).cuda())
+            for b in range(2):
+                assert torch.equal(kb[b, :, :have[b]].cpu().double(), ref.gather(kvals, table[b], have[b]))
+                assert torch.equal(vb[b, :, :have[b]].cpu().double(), ref.gather(vvals, table[b], have[b]))
+    assert kp.device_status() == kp.ATTN_OK
+
+
+def test_refusals(kp):
+    c = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(5, 4, 64, dtype=torch.bfloat16, device="cuda")
+    table, kv = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
+    ok = dict(q=q, k_cache=c, v_cache=c, block_table=table, kv_len=kv, q_start=start, max_q=3)
+    kp.attn_paged_fwd(**ok)
+    for bad in (dict(q=q.float()), dict(q=q[..., :32]), dict(q=q[:, :3]), dict(q_start=None), dict(q_start=start[:2]),
+                dict(q_start=start.long()), dict(kv_len=kv.long()), dict(block_table=table[:1]), dict(out=q[:4]),
+                dict(out=q.float()), dict(lse=torch.zeros(4, 4, device="cuda")), dict(q=q[:1].expand(5, 4, 64)),
+                dict(out=torch.zeros(5, 1, 64, dtype=torch.bfloat16, device="cuda").expand(5, 4, 64))):
+        with pytest.raises(ValueError):
+            kp.attn_paged_fwd(**{**ok, **bad})
+    for bad in (dict(max_q=0), dict(num_splits=257), dict(num_splits=-1), dict(scale=math.inf)):
+        with pytest.raises(kp.AttnError):
+            kp.attn_paged_fwd(**{**ok, **bad})
+    out, _ = kp.attn_paged_fwd(q[:0], c, c, table, kv, torch.zeros(3, dtype=torch.int32, device="cuda"))   # no rows
+    assert out.shape == (0, 4, 64)
+    assert kp.device_status() == kp.ATTN_OK
