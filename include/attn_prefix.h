@@ -304,16 +304,14 @@ attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table,
  *     ATTN_ERR_CACHE_RANGE.  kv_len and block_table as attn_cache_read, with
  *     max_pages * page_size in Tk's place.
  *   Hq: a multiple of Hkv, Hq / Hkv <= 128.
- *   num_splits: parts that a sequence's keys are cut into, in [1, 256], or 0 to have it chosen
- *     from the sizes.  workspace: attn_paged_workspace_bytes of device memory with the same
- *     arguments, 16-byte aligned, or NULL where that is 0; no initialisation needed.  Calls
- *     that share a workspace must not overlap on the GPU. */
-size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int max_q,
-                                  int num_splits);
+ *   workspace: attn_paged_workspace_bytes of device memory with the same arguments (max_q = 1
+ *     without q_start), 16-byte aligned, or NULL where that is 0; no initialisation needed.
+ *     Calls that share a workspace must not overlap on the GPU. */
+size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int max_q);
 attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_strides* q_strides,
                            const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* kv_len,
                            const int32_t* q_start, void* out, const attn_strides* out_strides, float* lse,
-                           void* workspace, int B, int T, int Hq, int max_q, int causal, int num_splits, float scale,
+                           void* workspace, int B, int T, int Hq, int max_q, int causal, float scale,
                            cudaStream_t stream);
 
 /* Synchronizes `stream`, then reads and clears the sticky device flags raised by

@@ -51,8 +51,8 @@ _SIGNATURES = {
     "attn_qk_norm_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P]),
     "attn_cache_write": (_I, [_P, _P, _P, _P, _P, _P, _I, _P]),
     "attn_cache_read": (_I, [_P, _P, _L, _I, _P, _P, _P, _P, _P, _I, _I, _P]),
-    "attn_paged_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
-    "attn_paged_fwd": (_I, [_P, _P, _P, _P, _L, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
+    "attn_paged_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "attn_paged_fwd": (_I, [_P, _P, _P, _P, _L, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]),
     "attn_get_device_status": (_I, [_P]),
     "attn_set_wait_limit_ns": (None, [ctypes.c_uint64]),
     "attn_set_debug_flags": (None, [ctypes.c_uint]),

@@ -1,6 +1,6 @@
 // paged.cu -- serving operators around the prefix-masked attention: per-head norm and
 // rotation of q and k (rope.cuh), a paged key/value cache written and read back
-// (cache.cuh), and attention of new tokens over the pages (paged_simple.cuh).  The C ABI is
+// (cache.cuh), and attention of new tokens over the pages (paged_rows.cuh, paged_simple.cuh).  The C ABI is
 // in include/attn_prefix.h.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -16,6 +16,7 @@
 
 #include "attn_prefix.h"
 #include "host_common.h"
+#include "ptx.cuh"
 
 namespace attn {
 
@@ -47,7 +48,10 @@ struct PagedParams {
     long long table_stride;
     const int32_t* kv_len;
     const int32_t* q_start;             // null: one row per sequence
+    float* part_out;                    // partial results of sequences shared by several CTAs
+    float* part_lse;
     int B, T, Hq, G, max_q, kv_cap, causal;
+    int min_units;                      // least tiles that a CTA takes (paged_rows.cuh)
     float scale_log2;
 };
 
@@ -71,6 +75,7 @@ __device__ __forceinline__ int checked_page(const PagedParams& p, int b, int pj,
 }
 
 #include "paged_simple.cuh"
+#include "paged_rows.cuh"
 
 bool take_paged_flags(unsigned* flags) {
     const unsigned zero = 0;
@@ -177,8 +182,38 @@ attn_status launch_read(const CacheReadParams& prm, int B, cudaStream_t stream) 
     return launched();
 }
 
+constexpr int SM_COUNT = 148;   // B200
+
+// CTAs of the few-row kernel: every resident slot, or fewer where the largest possible work
+// (every sequence of kv_cap keys) needs fewer.
+constexpr int ROWS_MIN_UNITS = 2;
+int rows_ctas(int per_sm, int B, int Hkv, long long kv_cap) {
+    const long long units = static_cast<long long>(B) * Hkv * ((kv_cap + PR_TK - 1) / PR_TK);
+    const long long most = (units + ROWS_MIN_UNITS - 1) / ROWS_MIN_UNITS;
+    return static_cast<int>(most < SM_COUNT * per_sm ? most : SM_COUNT * per_sm);
+}
+// Few rows per key head: at most one m16 tile of them.
+bool few_rows(long long max_q, int G) { return max_q * G <= PR_ROWS; }
+
+template <int D, bool E4M3>
+attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
+    using C = RowsCfg<D, E4M3>;
+    const int n = rows_ctas(C::PER_SM, p.B, p.c.Hkv, p.kv_cap);
+    p.min_units = ROWS_MIN_UNITS;
+    p.part_out = static_cast<float*>(workspace);
+    p.part_lse = p.part_out + 2LL * n * PR_ROWS * D;
+    if (cudaFuncSetAttribute(paged_rows_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    paged_rows_kernel<D, E4M3><<<n, PR_THREADS, C::SMEM, stream>>>(p, n);
+    paged_rows_combine_kernel<D><<<p.B * p.c.Hkv, PR_THREADS, 0, stream>>>(p, n);
+    return launched();
+}
+
 template <int D>
-attn_status launch_paged(const PagedParams& p, cudaStream_t stream) {
+attn_status launch_paged(const PagedParams& p, void* workspace, cudaStream_t stream) {
+    if (few_rows(p.max_q, p.G)) return p.c.e4m3 ? launch_rows<D, true>(p, workspace, stream) : launch_rows<D, false>(p, workspace, stream);
     const long long grid = (static_cast<long long>(p.B) * p.Hq * p.max_q + 3) / 4;
     if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     if (p.c.e4m3) paged_simple_kernel<D, true><<<static_cast<unsigned>(grid), 128, 0, stream>>>(p);
@@ -292,16 +327,18 @@ attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table,
 #undef CALL
 }
 
-size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int max_q,
-                                  int num_splits) {
-    (void)B, (void)T, (void)Hq, (void)Hkv, (void)D, (void)page_size, (void)max_pages, (void)max_q, (void)num_splits;
+size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int max_q) {
+    if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || page_size <= 0 || max_pages <= 0 || max_q <= 0)
+        return 0;
+    if (few_rows(max_q < T ? max_q : T, Hq / Hkv))
+        return 2ull * rows_ctas(2, B, Hkv, static_cast<long long>(max_pages) * page_size) * PR_ROWS * (D + 1) * sizeof(float);
     return 0;
 }
 
 attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_strides* q_strides,
                            const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* kv_len,
                            const int32_t* q_start, void* out, const attn_strides* out_strides, float* lse,
-                           void* workspace, int B, int T, int Hq, int max_q, int causal, int num_splits, float scale,
+                           void* workspace, int B, int T, int Hq, int max_q, int causal, float scale,
                            cudaStream_t stream) {
     PagedParams p;
     memset(&p, 0, sizeof p);
@@ -311,15 +348,17 @@ attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_st
     if (!kv_len || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
     if (B <= 0 || T <= 0 || Hq <= 0 || max_q <= 0 || max_pages <= 0 || table_stride < 0) return ATTN_ERR_INVALID_ARG;
     if (Hq % cache->Hkv != 0 || Hq / cache->Hkv > 128 || (q_start == nullptr && B != T)) return ATTN_ERR_INVALID_ARG;
-    if (!isfinite(scale) || num_splits < 0 || num_splits > 256) return ATTN_ERR_INVALID_ARG;
+    if (!isfinite(scale)) return ATTN_ERR_INVALID_ARG;
     if (static_cast<long long>(B) * Hq > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     const long long cap = static_cast<long long>(max_pages) * cache->page_size;
     if (cap > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     Strides sq, so;
     if (!token_strides_of(q_strides, Hq, cache->D, &sq) || !token_strides_of(out_strides, Hq, cache->D, &so))
         return ATTN_ERR_INVALID_ARG;
+    const int rows_q = q_start == nullptr ? 1 : max_q < T ? max_q : T;
+    const size_t need = attn_paged_workspace_bytes(B, T, Hq, cache->Hkv, cache->D, cache->page_size, max_pages, rows_q);
+    if (need != 0 && (!workspace || !aligned16(workspace))) return ATTN_ERR_INVALID_ARG;
     if ((st = check_device()) != ATTN_OK) return st;
-    (void)workspace;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
@@ -335,11 +374,11 @@ attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_st
     p.T = T;
     p.Hq = Hq;
     p.G = Hq / cache->Hkv;
-    p.max_q = q_start == nullptr ? 1 : max_q < T ? max_q : T;
+    p.max_q = rows_q;
     p.kv_cap = static_cast<int>(cap);
     p.causal = causal != 0;
     p.scale_log2 = scale * 1.44269504088896340736f;
-#define CALL(DD) launch_paged<DD>(p, stream)
+#define CALL(DD) launch_paged<DD>(p, workspace, stream)
     ATTN_BY_HEAD_DIM(cache->D, CALL)
 #undef CALL
 }

@@ -1,0 +1,550 @@
+// paged_rows.cuh -- attention over pages for few query rows per key head (at most 16):
+// single tokens of grouped heads, and short chunks.  Included by paged.cu inside namespace attn.
+//
+// What bounds it: every key and value row is read once, with at most 16 query rows to use it,
+// so HBM does.  The kernel is built around keeping loads in flight:
+//
+// - The keys of all (sequence, key head) pairs are cut into tiles of 64, laid end to end,
+//   and dealt to the CTAs in equal contiguous runs, so a batch of ragged lengths keeps every
+//   SM busy to the end (each CTA finds its run with a scan over kv_len).  A pair whose tiles
+//   fall to several CTAs is put together by paged_rows_combine_kernel, by log-sum-exp weights.
+// - Each of a CTA's four warps takes 16 of a tile's keys through a ring of shared memory of
+//   its own, filled with 16-byte cp.async (keys behind the sequence and pages that do not
+//   exist are filled with zeros), so no warp waits for another inside a run.
+// - The 16 rows and 16 keys make one m16n8k16 tile: S = Q K^T (two MMAs per 16 dims), and
+//   P, already in the A layout, times V.  mma.sync is enough here: at HBM's rate the
+//   tensor work of a tile is a small part of its load time.
+// - e4m3 rows are widened to bf16 in registers on their way from shared memory: a code's
+//   bits moved to a bf16's place are the value times 2^-120, so one packed multiply by
+//   2^(120 + e) gives the row's value exactly (e the row's scale exponent).  To load 16 codes of
+//   one key at once, the head dims are taken in a permuted order, the same for Q and K; V is
+//   transposed by the byte permutes that place the codes.
+// - The running maximum moves only when a score exceeds it by 2^8 (a vote per tile): the
+//   weights stay below 2^8 and the result is the same up to rounding.
+
+constexpr int PR_THREADS = 128;
+constexpr int PR_WARPS = 4;
+constexpr int PR_WK = 16;                  // keys per warp and tile
+constexpr int PR_TK = PR_WARPS * PR_WK;    // keys per tile
+constexpr int PR_ROWS = 16;                // query rows per CTA
+
+template <int D, bool E4M3>
+struct RowsCfg {
+    static constexpr int ROW = D * (E4M3 ? 1 : 2);      // bytes of one row
+    static constexpr int CPR = ROW / 16;                // 16-byte chunks per row
+    static constexpr int HALF = PR_WK * ROW;            // K or V part of a stage
+    static constexpr int STAGE = 2 * HALF + (E4M3 ? 32 : 0);   // + 16 K and 16 V scale bytes
+    // about 96 KB of rings per CTA (two CTAs per SM), 192 KB where a stage is 16 KB (one)
+    static constexpr int NST_RAW = 24576 / (2 * HALF);
+    static constexpr int NST = NST_RAW < 3 ? 3 : NST_RAW > 8 ? 8 : NST_RAW;
+    static constexpr int RING = PR_WARPS * NST * STAGE;
+    static constexpr int MERGE = PR_WARPS * PR_ROWS * (D + 4) * 4;   // reuses the ring
+    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int PER_SM = SMEM > 110 * 1024 ? 1 : 2;
+};
+
+// Byte offset of 16-byte chunk c of row r in a stage's K (w = 0) or V (w = 1) part.  The
+// chunk's place within its 128-byte line is permuted so that the reads below touch every
+// bank once: ldmatrix takes one chunk of 8 rows; an e4m3 key takes 16 bytes a lane, two rows to
+// a quarter warp; an e4m3 value takes 4 bytes of rows 2 q4 (+1, +8, +9) for q4 = 0..3.
+template <int D, bool E4M3>
+__device__ __forceinline__ uint32_t rows_swizzle(int w, int r, int c) {
+    constexpr int CPR = RowsCfg<D, E4M3>::CPR;
+    constexpr int RPL = CPR >= 8 ? 1 : 8 / CPR;            // rows per line
+    const int line = r * CPR / 8 + (CPR >= 8 ? c >> 3 : 0);
+    int pos = CPR >= 8 ? c & 7 : (r % RPL) * CPR + c;
+    if constexpr (!E4M3) pos ^= CPR >= 8 ? r & 7 : (r >> 1) & 3;
+    else if (w == 0) pos ^= CPR >= 8 ? (r & 1) << 2 : 0;
+    else pos ^= CPR >= 4 ? r & 6 : ((r >> 2) & 1) << 1;
+    return static_cast<uint32_t>(line * 128 + pos * 16);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool fill) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(fill ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Two e4m3 codes in bytes 1 and 3 of t (other bytes: anything) to bf16: values times the
+// factors f (2^(120 + e)).  Sign to bit 15, exponent and mantissa to bits 10..4.
+__device__ __forceinline__ uint32_t widen2(uint32_t t, uint32_t f) {
+    return mul_bf16x2((t & 0x80008000u) | ((t >> 4) & 0x07f007f0u), f);
+}
+// bf16 pattern of 2^(120 + e) cut to 2^127, for a scale code e + 127; NaN for 255.  What the
+// cut leaves (e > 7) is scale_rest.
+__device__ __forceinline__ uint32_t scale_factor(uint32_t code) {
+    return code == SCALE_NAN ? 0x7fffu : min(code + 120u, 254u) << 7;
+}
+__device__ __forceinline__ float scale_rest(uint32_t code) {
+    return __uint_as_float((code > 134u && code != SCALE_NAN ? code - 7u : 127u) << 23);
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Tiles of sequence b for one key head: at least one where it has query rows, so that empty
+// sequences get their zeros.
+__device__ __forceinline__ int rows_units(const PagedParams& p, int b, bool report = false) {
+    const int n = query_range(p, b, report).n;
+    const int kv = paged_kv_len(p.kv_len, b, p.kv_cap, report);
+    if (n == 0) return 0;
+    return max(1, (kv + PR_TK - 1) / PR_TK);
+}
+
+// The deal: `total` units per key head over the batch, `per` of all heads' units to a CTA.
+struct RowsDeal {
+    long long total, per;
+    __device__ __forceinline__ long long all(int Hkv) const { return total * Hkv; }
+};
+// Block-wide sum over the batch (PR_THREADS threads).
+__device__ __forceinline__ RowsDeal rows_deal(const PagedParams& p, int n_ctas, long long* s_sum, bool report) {
+    long long sum = 0;
+    for (int b = threadIdx.x; b < p.B; b += PR_THREADS) sum += rows_units(p, b, report);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    RowsDeal d;
+    d.total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+    __syncthreads();
+    d.per = max(static_cast<long long>(p.min_units), (d.all(p.c.Hkv) + n_ctas - 1) / n_ctas);
+    return d;
+}
+// Calls f(b, first unit of b, units of b) on the one thread whose sequence satisfies pick.
+template <typename Pick, typename F>
+__device__ __forceinline__ void rows_scan(const PagedParams& p, long long* s_sum, Pick pick, F f) {
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += PR_THREADS) {
+        const int b = b0 + threadIdx.x;
+        const long long n = b < p.B ? rows_units(p, b) : 0;
+        long long incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+            if ((threadIdx.x & 31) >= o) incl += t;
+        }
+        if ((threadIdx.x & 31) == 31) s_sum[threadIdx.x >> 5] = incl;
+        __syncthreads();
+        for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) incl += s_sum[w];
+        const long long all = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+        incl += base;
+        if (n > 0 && pick(b, incl - n, incl)) f(b, incl - n, static_cast<int>(n));
+        base += all;
+        __syncthreads();
+    }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
+    paged_rows_kernel(const PagedParams p, const int n_ctas) {
+    using C = RowsCfg<D, E4M3>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_sum[PR_WARPS];
+    __shared__ long long s_first;
+    __shared__ int s_b;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int q4 = lane & 3, r8 = lane >> 2;
+
+    const RowsDeal deal = rows_deal(p, n_ctas, s_sum, blockIdx.x == 0);
+    const long long all = deal.all(p.c.Hkv);
+    long long unit = blockIdx.x * deal.per;
+    const long long unit_end = min(all, unit + deal.per);
+    if (unit >= all) return;
+    rows_scan(p, s_sum, [&](int, long long lo, long long hi) { return lo * p.c.Hkv <= unit && unit < hi * p.c.Hkv; },
+              [&](int b, long long lo, int) {
+                  s_b = b;
+                  s_first = lo;
+              });
+    int b = s_b;
+    long long rem = unit - s_first * p.c.Hkv;
+    const uint32_t ring = smem_u32(smem) + warp * C::NST * C::STAGE;
+
+    while (unit < unit_end) {
+        int units = rows_units(p, b);
+        while (units == 0) units = rows_units(p, ++b);   // a later one exists: unit < all
+        const int h = static_cast<int>(rem / units);
+        const int tile0 = static_cast<int>(rem - static_cast<long long>(h) * units);
+        const int tile1 = static_cast<int>(min(static_cast<long long>(units), tile0 + (unit_end - unit)));
+        const QueryRange qr = query_range(p, b, false);
+        const int kv = paged_kv_len(p.kv_len, b, p.kv_cap, false);
+        const int rows = min(qr.n, p.max_q) * p.G;
+
+        // ---- Q fragments (rows beyond the last one: zeros) and what each of the two rows sees
+        uint32_t qf[D / 16][4];
+        int seen[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = r8 + 8 * e;
+            const int i = r / p.G;
+            seen[e] = r < rows ? (p.causal ? min(kv, max(0, kv - qr.n + i + 1)) : kv) : 0;
+            const __nv_bfloat16* src = p.q + (qr.t0 + (r < rows ? i : 0)) * p.q_t + (h * p.G + (r < rows ? r - i * p.G : 0)) * p.q_h;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                uint2 v = make_uint2(0u, 0u);
+                if (r < rows) {
+                    if constexpr (E4M3) {
+                        // dims in the order the e4m3 rows are loaded: lane q4 holds D/4 of them in runs of
+                        // 16 (8 at D = 32), four of a run per step
+                        constexpr int RUN = D >= 64 ? 16 : 8;
+                        const int d = (s / (RUN / 4)) * (RUN * 4) + q4 * RUN + (s % (RUN / 4)) * 4;
+                        v = *reinterpret_cast<const uint2*>(src + d);
+                    } else {
+                        v.x = *reinterpret_cast<const uint32_t*>(src + s * 16 + q4 * 2);
+                        v.y = *reinterpret_cast<const uint32_t*>(src + s * 16 + q4 * 2 + 8);
+                    }
+                }
+                qf[s][e] = v.x;
+                qf[s][2 + e] = v.y;
+            }
+        }
+        const int all_seen = p.causal ? max(0, kv - qr.n + 1) : kv;   // keys that every row sees
+
+        // ---- loads: this warp's 16 keys of tile t; two 8-key groups, each within one page
+        const int32_t* table = p.table + b * p.table_stride;
+        auto page_of = [&](int t) {   // lanes 0, 1: the page of the group, -1: none
+            const int key = t * PR_TK + warp * PR_WK + (lane & 1) * 8;
+            int page = -1;
+            if (t < tile1 && key < kv) {
+                page = __ldg(table + key / p.c.page_size);
+                if (page < 0 || page >= p.c.num_pages) {
+                    if (lane < 2) atomicOr(&g_paged_status, STATUS_CACHE);
+                    page = -1;
+                }
+            }
+            return page;
+        };
+        auto load = [&](int t, int page_l, int slot) {
+            const uint32_t dst = ring + slot * C::STAGE;
+            const int key0 = t * PR_TK + warp * PR_WK;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int page = __shfl_sync(0xffffffffu, page_l, g);
+                const int k0 = key0 + 8 * g;
+                const int r0 = k0 - k0 / p.c.page_size * p.c.page_size;
+                const int n = page < 0 ? 0 : kv - k0;   // rows of the group that exist
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint8_t* src = p.c.data[w];
+                    if (page >= 0) src += page * p.c.sp[w] + h * p.c.sh[w] + r0 * p.c.st[w];
+#pragma unroll
+                    for (int x = 0; x < 8 * C::CPR / 32 + (8 * C::CPR % 32 != 0); ++x) {
+                        const int idx = x * 32 + lane;
+                        const int r = idx / C::CPR, c = idx % C::CPR;
+                        if (8 * C::CPR % 32 == 0 || idx < 8 * C::CPR)
+                            cp_async16(dst + w * C::HALF + rows_swizzle<D, E4M3>(w, 8 * g + r, c), src + (r < n ? r * p.c.st[w] + c * 16 : 0), r < n);
+                    }
+                }
+                if constexpr (E4M3) {
+                    if (lane < 2) {
+                        const uint8_t* sc = p.c.scale[lane];
+                        if (page >= 0) sc += (static_cast<long long>(page) * p.c.Hkv + h) * p.c.page_size + r0;
+                        cp_async8(dst + 2 * C::HALF + 16 * lane + 8 * g, sc, page >= 0);
+                    }
+                }
+            }
+        };
+        float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+
+        int page_next = page_of(tile0);
+#pragma unroll 1
+        for (int s = 0; s < C::NST - 1; ++s) {
+            const int pg = page_next;
+            page_next = page_of(tile0 + s + 1);
+            if (tile0 + s < tile1) load(tile0 + s, pg, s);
+            cp_commit();
+        }
+        int slot = 0;
+#pragma unroll 1
+        for (int t = tile0; t < tile1; ++t) {
+            __syncwarp();   // every lane is done with the slot that is filled next
+            {
+                const int tn = t + C::NST - 1;
+                const int pg = page_next;
+                page_next = page_of(tn + 1);
+                if (tn < tile1) load(tn, pg, slot == 0 ? C::NST - 1 : slot - 1);
+                cp_commit();
+            }
+            cp_wait<C::NST - 1>();
+            __syncwarp();
+            const uint32_t kb = ring + slot * C::STAGE, vb = kb + C::HALF;
+            const int key0 = t * PR_TK + warp * PR_WK;
+            float s[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+            uint32_t vsc[2] = {0u, 0u};        // e4m3: factors of keys 2 q4, +1 and 2 q4 + 8, +9
+            float ks[2][2], vs[2][2];          // what the packed factors leave (1 in ordinary use)
+            if constexpr (E4M3) {
+                const uint8_t* sc = smem + (kb - smem_u32(smem)) + 2 * C::HALF;
+                uint32_t kf[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const uint32_t code = sc[8 * n + r8];
+                    kf[n] = scale_factor(code) * 0x10001u;
+                    const uint32_t k2 = *reinterpret_cast<const uint16_t*>(sc + 8 * n + 2 * q4);
+                    const uint32_t v2 = *reinterpret_cast<const uint16_t*>(sc + 16 + 8 * n + 2 * q4);
+                    vsc[n] = scale_factor(v2 & 255u) | scale_factor(v2 >> 8) << 16;
+                    ks[n][0] = scale_rest(k2 & 255u);
+                    ks[n][1] = scale_rest(k2 >> 8);
+                    vs[n][0] = scale_rest(v2 & 255u);
+                    vs[n][1] = scale_rest(v2 >> 8);
+                    if (key0 + PR_WK > kv) {   // scale bytes behind the sequence are anybody's
+                        const int left = kv - (key0 + 8 * n + 2 * q4);
+                        vsc[n] &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                    }
+                }
+                constexpr int RUN = D >= 64 ? 16 : 8;
+#pragma unroll
+                for (int c = 0; c < D / (RUN * 4); ++c) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int r = 8 * n + r8;
+                        uint32_t w[RUN / 4];
+                        if constexpr (RUN == 16) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(smem + (kb - smem_u32(smem)) + rows_swizzle<D, true>(0, r, c * 4 + q4));
+                            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2*>(smem + (kb - smem_u32(smem)) + rows_swizzle<D, true>(0, r, q4 >> 1) + (q4 & 1) * 8);
+                            w[0] = x.x; w[1] = x.y;
+                        }
+#pragma unroll
+                        for (int e = 0; e < RUN / 4; ++e)
+                            mma16816(s[n], qf[c * (RUN / 4) + e], widen2(__byte_perm(w[e], 0u, 0x1404), kf[n]),
+                                     widen2(__byte_perm(w[e], 0u, 0x3424), kf[n]));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int st = 0; st < D / 16; ++st) {
+                    uint32_t kf[4];   // keys 0-7 dims 0-7, 8-15; keys 8-15 dims 0-7, 8-15
+                    ldsm4(kb + rows_swizzle<D, false>(0, (lane & 7) + ((lane >> 4) << 3), st * 2 + ((lane >> 3) & 1)), kf);
+                    mma16816(s[0], qf[st], kf[0], kf[1]);
+                    mma16816(s[1], qf[st], kf[2], kf[3]);
+                }
+            }
+            // ---- scores in the log2 domain, masked by selection
+            float x[2][4];
+            const bool masked = key0 + PR_WK > all_seen;   // uniform
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float y = s[n][e] * p.scale_log2;
+                    if constexpr (E4M3) y *= ks[n][e & 1];
+                    if (masked && key0 + 8 * n + 2 * q4 + (e & 1) >= seen[e >> 1]) y = -INFINITY;
+                    x[n][e] = y;
+                    mx[e >> 1] = fmaxf(mx[e >> 1], y);
+                }
+            if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.0f || mx[1] > m[1] + 8.0f)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mn = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                    mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
+                    mn = fmaxf(m[e], mn);
+                    const float f = m[e] == -INFINITY ? 0.0f : exp2_approx(m[e] - mn);
+                    m[e] = mn;
+                    l[e] *= f;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        o[i][2 * e] *= f;
+                        o[i][2 * e + 1] *= f;
+                    }
+                }
+            }
+            uint32_t pf[4];
+            const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = exp2_approx(x[n][e] - (e < 2 ? m0 : m1));
+                    l[e >> 1] += w[e];
+                    if constexpr (E4M3) w[e] *= vs[n][e & 1];
+                }
+                pf[2 * n] = pack_bf16(w[0], w[1]);
+                pf[2 * n + 1] = pack_bf16(w[2], w[3]);
+            }
+            // ---- O += P V
+            if constexpr (E4M3) {
+                const uint8_t* v = smem + (vb - smem_u32(smem));
+#pragma unroll
+                for (int g = 0; g < D / 32; ++g) {
+                    uint32_t w[4];   // keys 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9: dims 32 g + 4 r8 + {0..3}
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 2 * q4 + (k & 1) + 8 * (k >> 1);
+                        w[k] = *reinterpret_cast<const uint32_t*>(v + rows_swizzle<D, true>(1, r, 2 * g + (r8 >> 2)) + (r8 & 3) * 4);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mma16816(o[4 * g + e], pf, widen2(__byte_perm(w[0], w[1], e << 4 | (4 + e) << 12), vsc[0]),
+                                 widen2(__byte_perm(w[2], w[3], e << 4 | (4 + e) << 12), vsc[1]));
+                }
+            } else {
+#pragma unroll
+                for (int st = 0; st < D / 16; ++st) {
+                    uint32_t vf[4];   // dims 0-7: keys 0-7, 8-15; dims 8-15: keys 0-7, 8-15
+                    ldsm4_trans(vb + rows_swizzle<D, false>(1, lane & 15, st * 2 + (lane >> 4)), vf);
+                    mma16816(o[2 * st], pf, vf[0], vf[1]);
+                    mma16816(o[2 * st + 1], pf, vf[2], vf[3]);
+                }
+            }
+            slot = slot + 1 == C::NST ? 0 : slot + 1;
+        }
+        cp_wait<0>();
+
+        // ---- the four warps' results into one: m, l and o of each warp through shared memory
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        }
+        __syncthreads();   // every warp is done with its ring
+        float* so = reinterpret_cast<float*>(smem);                      // [4][16][D + 2]
+        float* sm = so + PR_WARPS * PR_ROWS * (D + 2);                   // [4][16][2]: m, l
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = r8 + 8 * e;
+            float* dst = so + (warp * PR_ROWS + r) * (D + 2);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                if constexpr (E4M3) {
+                    // n-tile 4 g + t holds dims 32 g + 4 n + t, this lane n = 2 q4 and 2 q4 + 1
+                    const int d = (i >> 2) * 32 + (i & 3) + 8 * q4;
+                    dst[d] = o[i][2 * e];
+                    dst[d + 4] = o[i][2 * e + 1];
+                } else {
+                    *reinterpret_cast<float2*>(dst + i * 8 + q4 * 2) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+                }
+            }
+            if (q4 == 0) {
+                sm[(warp * PR_ROWS + r) * 2] = m[e];
+                sm[(warp * PR_ROWS + r) * 2 + 1] = l[e];
+            }
+        }
+        __syncthreads();
+        const bool whole = tile0 == 0 && tile1 == units;
+        const long long part = 2LL * blockIdx.x + (tile0 == 0 ? 1 : 0);
+        for (int idx = tid; idx < rows * (D / 4); idx += PR_THREADS) {
+            const int r = idx / (D / 4), d = idx % (D / 4) * 4;
+            float mm = -INFINITY, ll = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < PR_WARPS; ++w) mm = fmaxf(mm, sm[(w * PR_ROWS + r) * 2]);
+#pragma unroll
+            for (int w = 0; w < PR_WARPS; ++w) {
+                const float mw = sm[(w * PR_ROWS + r) * 2];
+                const float f = mw == -INFINITY ? 0.0f : exp2_approx(mw - mm);
+                ll += f * sm[(w * PR_ROWS + r) * 2 + 1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] += f * so[(w * PR_ROWS + r) * (D + 2) + d + e];
+            }
+            const bool some = mm != -INFINITY || ll != 0.0f;   // (a NaN sum counts as some)
+            const float inv = some ? 1.0f / ll : 0.0f;
+            const float lse = some ? (mm + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] *= inv;
+            if (whole) {
+                const int i = r / p.G, hq = h * p.G + r - i * p.G;
+                *reinterpret_cast<uint2*>(p.out + (qr.t0 + i) * p.out_t + hq * p.out_h + d) =
+                    make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
+                if (d == 0 && p.lse != nullptr) p.lse[static_cast<long long>(qr.t0 + i) * p.Hq + hq] = lse;
+            } else {
+                *reinterpret_cast<float4*>(p.part_out + (part * PR_ROWS + r) * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                if (d == 0) p.part_lse[part * PR_ROWS + r] = lse;
+            }
+        }
+        __syncthreads();
+        unit += tile1 - tile0;
+        rem += tile1 - tile0;
+        if (rem >= static_cast<long long>(units) * p.c.Hkv) {
+            rem = 0;
+            ++b;
+        }
+    }
+}
+
+// Puts together the pairs that several CTAs of paged_rows_kernel worked on: one block per
+// (sequence, key head).  CTA c's part is slot 2c where the pair's tiles reach its run's
+// start from an earlier CTA, 2c + 1 where the pair begins in its run.
+template <int D>
+__global__ void __launch_bounds__(PR_THREADS) paged_rows_combine_kernel(const PagedParams p, const int n_ctas) {
+    __shared__ long long s_sum[PR_WARPS];
+    __shared__ long long s_first;
+    __shared__ int s_units;
+    const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x - b * p.c.Hkv;
+    const int tid = threadIdx.x;
+    if (tid == 0) s_units = 0;
+    const RowsDeal deal = rows_deal(p, n_ctas, s_sum, false);
+    rows_scan(p, s_sum, [&](int bb, long long, long long) { return bb == b; },
+              [&](int, long long lo, int n) {
+                  s_first = lo;
+                  s_units = n;
+              });
+    const int units = s_units;
+    if (units == 0) return;
+    const long long u0 = s_first * p.c.Hkv + static_cast<long long>(h) * units;
+    const long long c0 = u0 / deal.per, c1 = (u0 + units - 1) / deal.per;
+    if (c0 == c1) return;   // one CTA had it whole
+    const QueryRange qr = query_range(p, b, false);
+    const int rows = min(qr.n, p.max_q) * p.G;
+    auto slot = [&](long long c) { return 2 * c + (c == c0 ? 1 : 0); };
+    for (int idx = tid; idx < rows * (D / 4); idx += PR_THREADS) {
+        const int r = idx / (D / 4), d = idx % (D / 4) * 4;
+        float M = -INFINITY;
+        for (long long c = c0; c <= c1; ++c) M = fmaxf(M, __ldg(p.part_lse + slot(c) * PR_ROWS + r));
+        float s = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (long long c = c0; c <= c1; ++c) {
+            const float lc = __ldg(p.part_lse + slot(c) * PR_ROWS + r);
+            const float w = lc == -INFINITY ? 0.0f : expf(lc - M);
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p.part_out + (slot(c) * PR_ROWS + r) * D + d));
+            s += w;
+            acc[0] += w * v.x;
+            acc[1] += w * v.y;
+            acc[2] += w * v.z;
+            acc[3] += w * v.w;
+        }
+        const bool some = s != 0.0f;
+        const float inv = some ? 1.0f / s : 0.0f;
+        const int i = r / p.G, hq = h * p.G + r - i * p.G;
+        *reinterpret_cast<uint2*>(p.out + (qr.t0 + i) * p.out_t + hq * p.out_h + d) =
+            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+        if (d == 0 && p.lse != nullptr) p.lse[static_cast<long long>(qr.t0 + i) * p.Hq + hq] = some ? M + logf(s) : -INFINITY;
+    }
+}

@@ -262,7 +262,7 @@ def attn_cache_read(k_cache, v_cache, block_table, kv_len, Tk=None, k_scale=None
 
 # ---------------------------------------------------------------------------------- attention
 def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q=None, causal=True, scale=None,
-                   k_scale=None, v_scale=None, num_splits=0, workspace=None, out=None, lse=None, need_lse=True):
+                   k_scale=None, v_scale=None, workspace=None, out=None, lse=None, need_lse=True):
     """Attention of each sequence's new tokens over its pages (attn_paged_fwd): (out bf16 [T, Hq, D],
     lse fp32 [T, Hq]).
 
@@ -270,8 +270,7 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q
     q_start one row per sequence.  max_q: an upper bound on a sequence's rows (by default T).  The
     pages hold the new tokens' keys too; with `causal`, the rows are the last positions of their
     sequence.  Rows outside every sequence are left as they were (uninitialised where out is made
-    here).  num_splits: 0 to have it chosen; workspace: a buffer of attn_paged_workspace_bytes,
-    allocated here when not given."""
+    here).  workspace: a buffer of attn_paged_workspace_bytes, allocated here when not given."""
     c = _cache(k_cache, v_cache, k_scale, v_scale)
     B, n = _table(block_table, kv_len, k_cache.device)
     _bf16(q, (3,), "q")
@@ -301,7 +300,7 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q
         return out, lse
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     max_q = 1 if q_start is None else T if max_q is None else int(max_q)
-    need = lib().attn_paged_workspace_bytes(B, T, Hq, Hkv, D, page, n, max_q, num_splits)
+    need = lib().attn_paged_workspace_bytes(B, T, Hq, Hkv, D, page, n, max_q)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif need and (workspace.device != dev or not workspace.is_contiguous()
@@ -310,7 +309,7 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q
     _call("attn_paged_fwd", dev, c, q.data_ptr(), _STRIDES.pack(*_strides3(q, "q")), block_table.data_ptr(),
           block_table.stride(0), n, kv_len.data_ptr(), None if q_start is None else q_start.data_ptr(), out.data_ptr(),
           _STRIDES.pack(*_strides3(out, "out")), None if lse is None else lse.data_ptr(),
-          workspace.data_ptr() if need else None, B, T, Hq, max_q, bool(causal), num_splits, scale)
+          workspace.data_ptr() if need else None, B, T, Hq, max_q, bool(causal), scale)
     return out, lse
 
 

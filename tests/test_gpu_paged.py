@@ -115,12 +115,11 @@ def test_chunks(kp, D, Hq, Hkv, page, causal, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
-@pytest.mark.parametrize("splits", [1, 2, 3, 7, 256])
-@pytest.mark.parametrize("n_q", [1, 9, 150])
-def test_splits(kp, n_q, splits, e4m3):
-    kv = [1500, 130, 0, 1]
-    c = make(kv, [n_q] * 4, 4, 2, 64, 16, e4m3, seed=splits)
-    check(kp, c, num_splits=splits)
+@pytest.mark.parametrize("n_q", [1, 4, 9, 150])
+@pytest.mark.parametrize("kv", [[30000], [1], [0], [64, 20000, 0, 65], [1500, 130, 0, 1] * 40])
+def test_sequences_shared_by_many_blocks(kp, kv, n_q, e4m3):
+    """One long sequence over all of the GPU, a few of very different lengths, and more sequences than blocks."""
+    check(kp, make(kv, [n_q] * len(kv), 4, 2, 64, 16, e4m3, seed=len(kv)))
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -303,7 +302,7 @@ def test_refusals(kp):
                 dict(out=torch.zeros(5, 1, 64, dtype=torch.bfloat16, device="cuda").expand(5, 4, 64))):
         with pytest.raises(ValueError):
             kp.attn_paged_fwd(**{**ok, **bad})
-    for bad in (dict(max_q=0), dict(num_splits=257), dict(num_splits=-1), dict(scale=math.inf)):
+    for bad in (dict(max_q=0), dict(scale=math.inf)):
         with pytest.raises(kp.AttnError):
             kp.attn_paged_fwd(**{**ok, **bad})
     out, _ = kp.attn_paged_fwd(q[:0], c, c, table, kv, torch.zeros(3, dtype=torch.int32, device="cuda"))   # no rows

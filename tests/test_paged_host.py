@@ -57,7 +57,7 @@ def test_every_cache_call_rejects_a_bad_cache(lib, kw, want):
     c = _cache(**kw)
     assert lib.attn_cache_write(c, A, A, None, None, A, 3, NULL) == want
     assert lib.attn_cache_read(c, A, 4, 4, A, A, A, None, None, 2, 32, NULL) == want
-    assert lib.attn_paged_fwd(c, A, None, A, 4, 4, A, A, A, None, NULL, A, 2, 8, 4, 8, 1, 1, 0.1, NULL) == want
+    assert lib.attn_paged_fwd(c, A, None, A, 4, 4, A, A, A, None, NULL, A, 2, 8, 4, 8, 1, 0.1, NULL) == want
 
 
 def test_cache_calls_reject_bad_arguments(lib):
@@ -83,15 +83,15 @@ def test_cache_calls_reject_bad_arguments(lib):
 def test_paged_rejects_bad_arguments(lib):
     c = _cache()
 
-    def f(q=A, table=A, stride=4, n=4, kv=A, qs=A, out=A, lse=NULL, ws=A, B=2, T=8, Hq=4, mq=8, splits=1, scale=0.1,
+    def f(q=A, table=A, stride=4, n=4, kv=A, qs=A, out=A, lse=NULL, ws=A, B=2, T=8, Hq=4, mq=8, scale=0.1,
           qst=None):
-        return lib.attn_paged_fwd(c, q, qst, table, stride, n, kv, qs, out, None, lse, ws, B, T, Hq, mq, 1, splits, scale, NULL)
+        return lib.attn_paged_fwd(c, q, qst, table, stride, n, kv, qs, out, None, lse, ws, B, T, Hq, mq, 1, scale, NULL)
 
     bad = ctypes.c_void_p(0x10002)
     for kw in (dict(q=NULL), dict(q=ctypes.c_void_p(0x10008)), dict(out=NULL), dict(table=NULL), dict(table=bad), dict(kv=NULL),
                dict(kv=bad), dict(qs=bad), dict(lse=bad), dict(stride=-1), dict(n=0), dict(n=1 << 28), dict(B=0), dict(T=0),
-               dict(Hq=0), dict(Hq=5), dict(Hq=2 * 129), dict(mq=0), dict(splits=-1), dict(splits=257), dict(scale=math.nan),
-               dict(qs=NULL), dict(qst=struct.pack("3q", 0, 64, 252))):
+               dict(Hq=0), dict(Hq=5), dict(Hq=2 * 129), dict(mq=0), dict(scale=math.nan),
+               dict(qs=NULL), dict(ws=NULL, mq=1), dict(ws=ctypes.c_void_p(0x10008), mq=1), dict(qst=struct.pack("3q", 0, 64, 252))):
         assert f(**kw) == 1, kw
 
 
