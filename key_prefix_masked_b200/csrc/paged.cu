@@ -17,6 +17,8 @@
 #include "attn_prefix.h"
 #include "host_common.h"
 #include "ptx.cuh"
+#include "softmax_math.cuh"
+#include "tmem_ops.cuh"
 
 namespace attn {
 
@@ -51,9 +53,17 @@ struct PagedParams {
     float* part_out;                    // partial results of sequences shared by several CTAs
     float* part_lse;
     int B, T, Hq, G, max_q, kv_cap, causal;
-    int min_units;                      // least tiles that a CTA takes (paged_rows.cuh)
+    int min_units;                      // least tiles that a CTA takes
+    int page_shift;                     // log2(page_size), -1 if it is no power of two
+    int tpt, box_rows;                  // paged_chunk.cuh: tokens per row tile, rows per copied box
+    unsigned debug;
+    unsigned long long wait_ns;
     float scale_log2;
 };
+// Index into the block table of the page that holds `key`.
+__device__ __forceinline__ int page_index(const PagedParams& p, int key) {
+    return p.page_shift >= 0 ? key >> p.page_shift : key / p.c.page_size;
+}
 
 // Rows [t0, t0 + n) of q belong to sequence b.
 struct QueryRange {
@@ -76,6 +86,7 @@ __device__ __forceinline__ int checked_page(const PagedParams& p, int b, int pj,
 
 #include "paged_simple.cuh"
 #include "paged_rows.cuh"
+#include "paged_chunk.cuh"
 
 bool take_paged_flags(unsigned* flags) {
     const unsigned zero = 0;
@@ -211,9 +222,47 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
     return launched();
 }
 
+// CTAs of the chunk kernel: one per SM, or fewer where the largest possible work needs fewer.
+constexpr int CHUNK_MIN_UNITS = 2;
+int chunk_ctas(int B, int Hkv, int G, long long max_q, long long kv_cap) {
+    const int tokens = 2 * (128 / G);
+    const long long tiles = static_cast<long long>(B) * Hkv * ((max_q + tokens - 1) / tokens);
+    const long long units = tiles * ((kv_cap + PC_BN - 1) / PC_BN);
+    const long long most = (units + CHUNK_MIN_UNITS - 1) / CHUNK_MIN_UNITS;
+    return static_cast<int>(most < SM_COUNT ? most : SM_COUNT);
+}
+
+template <int D, bool E4M3>
+attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
+    using C = ChunkCfg<D, E4M3>;
+    const int n = chunk_ctas(p.B, p.c.Hkv, p.G, p.max_q, p.kv_cap);
+    p.min_units = CHUNK_MIN_UNITS;
+    p.part_out = static_cast<float*>(workspace);
+    p.part_lse = p.part_out + 512LL * n * D;
+    p.tpt = 128 / p.G;
+    p.box_rows = p.c.page_size & -p.c.page_size;   // the largest power of two that divides it
+    if (p.box_rows > PC_BN) p.box_rows = PC_BN;
+    const CUtensorMapSwizzle swz = C::SW == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, p.q, p.T, p.c.Hkv, p.G, D, {p.q_t, p.G * p.q_h, p.q_h}, C::BLK, p.G, swz, p.tpt)) return ATTN_ERR_CUDA;
+    mk = mv = mq;
+    if (!E4M3 && (!make_map(&mk, p.c.data[0], p.c.num_pages, p.c.Hkv, p.c.page_size, D, {p.c.sp[0] / 2, p.c.sh[0] / 2, p.c.st[0] / 2}, C::BLK, p.box_rows, swz) ||
+                  !make_map(&mv, p.c.data[1], p.c.num_pages, p.c.Hkv, p.c.page_size, D, {p.c.sp[1] / 2, p.c.sh[1] / 2, p.c.st[1] / 2}, C::BLK, p.box_rows, swz)))
+        return ATTN_ERR_CUDA;
+    if (cudaFuncSetAttribute(paged_chunk_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    paged_chunk_kernel<D, E4M3><<<n, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, p, n);
+    if (n > 1) paged_chunk_combine_kernel<D><<<dim3(n - 1, 8), 128, 0, stream>>>(p, n);
+    return launched();
+}
+
 template <int D>
 attn_status launch_paged(const PagedParams& p, void* workspace, cudaStream_t stream) {
     if (few_rows(p.max_q, p.G)) return p.c.e4m3 ? launch_rows<D, true>(p, workspace, stream) : launch_rows<D, false>(p, workspace, stream);
+    if constexpr (D <= 128)
+        return p.c.e4m3 ? launch_chunk<D, true>(p, workspace, stream) : launch_chunk<D, false>(p, workspace, stream);
     const long long grid = (static_cast<long long>(p.B) * p.Hq * p.max_q + 3) / 4;
     if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     if (p.c.e4m3) paged_simple_kernel<D, true><<<static_cast<unsigned>(grid), 128, 0, stream>>>(p);
@@ -328,10 +377,12 @@ attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table,
 }
 
 size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int max_q) {
-    if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || page_size <= 0 || max_pages <= 0 || max_q <= 0)
+    if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || D <= 0 || page_size <= 0 || max_pages <= 0 || max_q <= 0)
         return 0;
     if (few_rows(max_q < T ? max_q : T, Hq / Hkv))
         return 2ull * rows_ctas(2, B, Hkv, static_cast<long long>(max_pages) * page_size) * PR_ROWS * (D + 1) * sizeof(float);
+    if (D <= 128)
+        return 512ull * chunk_ctas(B, Hkv, Hq / Hkv, max_q < T ? max_q : T, static_cast<long long>(max_pages) * page_size) * (D + 1) * sizeof(float);
     return 0;
 }
 
@@ -377,6 +428,11 @@ attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_st
     p.max_q = rows_q;
     p.kv_cap = static_cast<int>(cap);
     p.causal = causal != 0;
+    p.page_shift = -1;
+    if ((cache->page_size & (cache->page_size - 1)) == 0)
+        for (p.page_shift = 0; (1 << p.page_shift) < cache->page_size;) ++p.page_shift;
+    p.debug = g_debug.load(std::memory_order_relaxed);
+    p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     p.scale_log2 = scale * 1.44269504088896340736f;
 #define CALL(DD) launch_paged<DD>(p, workspace, stream)
     ATTN_BY_HEAD_DIM(cache->D, CALL)

@@ -1,0 +1,733 @@
+// paged_chunk.cuh -- attention over pages for many query rows per key head, head dims 32,
+// 64 and 128: chunks of prompts.  Included by paged.cu inside namespace attn.
+//
+// Rows: the G query heads of a key head see the same keys, so a 128-row tile is 128 / G tokens
+// times G heads (row = token * G + head, loaded by one 4-D TMA box per 64 dims).  A CTA
+// works on two such tiles of consecutive tokens, one per softmax warpgroup, against the same
+// 128-key tiles of K and V: while one tile's scores are in its softmax warps, the tensor
+// pipe runs the other tile's MMAs, and each K/V byte brought to shared memory serves 256 rows.
+//
+// TMEM: S_0, S_1 (128 columns each, P_g stored over S_g), O_0, O_1.  MMA order per key
+// tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1).  One thread's MMAs run in issue order, so
+// "S_g(j) ready" also means PV_g(j-1) is complete and the group may rescale O_g.
+//
+// The work, (sequence, key head, token tile, key tile), is laid end to end and dealt to
+// one persistent CTA per SM in equal contiguous runs, like the few-row kernel's: ragged
+// batches and causal triangles leave no SM idle at the end, and only a run's first and last
+// token tile can be shared with another CTA; paged_chunk_combine_kernel puts those together.
+//
+// K and V: bf16 pages are copied by TMA, in boxes of the largest power of two of rows (up
+// to 128) that divides the page size, each box from its page; a box behind the
+// sequence or of a page that does not exist has its page coordinate outside the pool and reads as
+// zeros.  The rows of the last box behind the sequence are cleared in shared memory before
+// PV reads them.  e4m3 pages go through four converter warps: 16 codes a load, widened to
+// bf16 in registers (exactly, see paged_rows.cuh) and stored in the layout TMA would have
+// written, with the next tile's loads in flight meanwhile.
+//
+// Every wait is bounded; on expiry the CTA raises the timeout flag, drains and exits.
+
+constexpr int PC_BN = 128;                 // keys per tile
+constexpr float PC_RESCALE_LOG2 = 8.0f;
+
+template <int D, bool E4M3>
+struct ChunkCfg {
+    static constexpr int SW = D >= 64 ? 128 : 64;       // swizzle span in bytes
+    static constexpr int BLK = SW / 2;                  // columns per swizzle block
+    static constexpr int NBLK = D / BLK;
+    static constexpr int QT_BYTES = 128 * D * 2;        // one 128-row tile
+    static constexpr int SLOT = PC_BN * D * 2;          // a K or V tile
+    static constexpr int CTRL = 1024;
+    static constexpr int NS_FIT = (232448 - 1024 - CTRL - 2 * QT_BYTES) / SLOT;
+    static constexpr int NS = NS_FIT < 12 ? NS_FIT : 12;
+    static constexpr int SMEM = 1024 + 2 * QT_BYTES + NS * SLOT + CTRL;
+    static constexpr uint32_t LAYOUT = SW == 128 ? 2u : 4u;
+    static constexpr uint32_t O_COL = 256;
+    // warps 0-7 softmax; bf16: 8 copies, 9 MMA; e4m3: 8-11 converters, 12 MMA, 13 Q copies
+    static constexpr int WARP_MMA = E4M3 ? 12 : 9;
+    static constexpr int WARP_COPY = E4M3 ? 13 : 8;
+    static constexpr int THREADS = E4M3 ? 512 : 320;
+    // Score columns in a softmax thread's registers at once.  512 threads leave 128 registers
+    // each, so the e4m3 kernel reads the second half of a row twice (for its maximum first).
+    static constexpr int COLS = E4M3 ? 64 : 128;
+    static_assert(O_COL + 2 * D <= 512, "TMEM");
+};
+
+enum : int {
+    PCB_QFULL = 0, PCB_QEMPTY = 1, PCB_S = 2 /* [2] */, PCB_P = 4 /* [2] */, PCB_O = 6 /* [2] */, PCB_DRAIN = 8,
+    PCB_FULL = 9 /* [12] */, PCB_EMPTY = 21 /* [12] */, PCB_NUM = 33
+};
+
+__device__ __noinline__ bool chunk_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > limit_ns) {
+            *abort_flag = 1;
+            atomicOr(&g_paged_status, STATUS_TIMEOUT);
+            return false;
+        }
+    }
+}
+// The same for a whole warp that stays converged: lane 0's answer.
+__device__ __forceinline__ bool chunk_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
+    return __shfl_sync(0xffffffffu, chunk_wait(bar, parity, abort_flag, limit_ns) ? 1 : 0, 0) != 0;
+}
+
+// Keys that query row i of a sequence with n rows and kv keys sees.
+__device__ __forceinline__ int keys_seen(int causal, int kv, int n, int i) {
+    return causal ? min(kv, max(0, kv - n + i + 1)) : kv;
+}
+
+// One (sequence, key head, token tile): `n` units (key tiles, at least one), n_g of them
+// for row tile g.
+struct ChunkPair {
+    int n, ng0, ng1, tok0, ntok0, ntok1, tpt;   // first token (of tile 0), token counts
+    __device__ __forceinline__ int tok(int g) const { return tok0 + (g ? tpt : 0); }
+    __device__ __forceinline__ int ntok(int g) const { return g ? ntok1 : ntok0; }
+};
+__device__ __forceinline__ ChunkPair chunk_pair(const PagedParams& p, int n_q, int n_live, int kv, int qt) {
+    ChunkPair c;
+    c.tpt = p.tpt;
+    c.tok0 = qt * 2 * p.tpt;
+    c.ntok0 = max(0, min(p.tpt, n_live - c.tok0));
+    c.ntok1 = max(0, min(p.tpt, n_live - c.tok0 - p.tpt));
+    auto tiles = [&](int tok, int n) { return n > 0 ? (keys_seen(p.causal, kv, n_q, tok + n - 1) + PC_BN - 1) / PC_BN : 0; };
+    c.ng0 = tiles(c.tok0, c.ntok0);
+    c.ng1 = tiles(c.tok0 + p.tpt, c.ntok1);
+    c.n = max(1, max(c.ng0, c.ng1));
+    return c;
+}
+__device__ __forceinline__ int chunk_qtiles(const PagedParams& p, int n_live) { return (n_live + 2 * p.tpt - 1) / (2 * p.tpt); }
+// Units of sequence b for one key head.
+__device__ __forceinline__ long long chunk_units(const PagedParams& p, int b, bool report) {
+    const int n = query_range(p, b, report).n;
+    const int kv = paged_kv_len(p.kv_len, b, p.kv_cap, report);
+    const int live = min(n, p.max_q), nq = chunk_qtiles(p, live);
+    if (!p.causal) return static_cast<long long>(nq) * max(1, (kv + PC_BN - 1) / PC_BN);
+    long long sum = 0;
+    for (int qt = 0; qt < nq; ++qt)   // what the tile's last row sees
+        sum += max(1, (keys_seen(1, kv, n, min((qt + 1) * 2 * p.tpt, live) - 1) + PC_BN - 1) / PC_BN);
+    return sum;
+}
+
+// Walks a CTA's run of units.  Every role of the CTA walks the same segments.
+struct ChunkWalk {
+    int b, h, qt, t0, t1;            // key tiles [t0, t1) of the pair
+    int n_q, n_live, kv, q0;         // the sequence's rows (all, computed), keys, first row
+    long long left;                  // units of the run from t0 on
+    ChunkPair c;
+
+    __device__ __forceinline__ void sequence(const PagedParams& p) {
+        const QueryRange r = query_range(p, b, false);
+        n_q = r.n;
+        n_live = min(r.n, p.max_q);
+        q0 = r.t0;
+        kv = paged_kv_len(p.kv_len, b, p.kv_cap, false);
+    }
+    __device__ __forceinline__ void segment(const PagedParams& p) {
+        c = chunk_pair(p, n_q, n_live, kv, qt);
+        t1 = static_cast<int>(min(static_cast<long long>(c.n), t0 + left));
+    }
+    // At sequence b, `at` units into it, with `left` units to walk.
+    __device__ __forceinline__ void begin(const PagedParams& p, int b_, long long at, long long left_) {
+        b = b_;
+        left = left_;
+        sequence(p);
+        const long long units = chunk_units(p, b, false);
+        h = static_cast<int>(at / units);
+        at -= h * units;
+        qt = 0;
+        c = chunk_pair(p, n_q, n_live, kv, 0);
+        while (at >= c.n) {
+            at -= c.n;
+            c = chunk_pair(p, n_q, n_live, kv, ++qt);
+        }
+        t0 = static_cast<int>(at);
+        segment(p);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == c.n; }
+    __device__ __forceinline__ void next(const PagedParams& p) {
+        left -= t1 - t0;
+        if (left <= 0) return;
+        t0 = 0;   // a segment that ends inside its pair ends the run
+        if (++qt == chunk_qtiles(p, n_live)) {
+            qt = 0;
+            if (++h == p.c.Hkv) {
+                h = 0;
+                do {
+                    ++b;
+                    sequence(p);
+                } while (n_live == 0);   // a later one has rows: left > 0
+            }
+        }
+        segment(p);
+    }
+    // key tiles of this segment that row tile g takes
+    __device__ __forceinline__ int end(int g) const { return min(t1, g ? c.ng1 : c.ng0); }
+};
+
+// Block-wide: the run's length, and for CTA blockIdx.x its first sequence and the units into it.
+template <int THREADS>
+__device__ __forceinline__ long long chunk_deal(const PagedParams& p, int n_ctas, long long first_of, long long* s_scr, bool report,
+                                                int* b_out, long long* at_out, long long* all_out) {
+    constexpr int W = THREADS / 32;
+    const int tid = threadIdx.x;
+    long long sum = 0;
+    for (int b = tid; b < p.B; b += THREADS) sum += chunk_units(p, b, report);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((tid & 31) == 0) s_scr[tid >> 5] = sum;
+    __syncthreads();
+    long long all = 0;
+    for (int w = 0; w < W; ++w) all += s_scr[w];
+    all *= p.c.Hkv;
+    const long long per = max(static_cast<long long>(p.min_units), (all + n_ctas - 1) / n_ctas);
+    const long long unit = first_of * per;
+    __syncthreads();
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+        const int b = b0 + tid;
+        const long long n = b < p.B ? chunk_units(p, b, false) : 0;
+        long long incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+            if ((tid & 31) >= o) incl += t;
+        }
+        if ((tid & 31) == 31) s_scr[tid >> 5] = incl;
+        __syncthreads();
+        long long block = 0;
+        for (int w = 0; w < W; ++w) {
+            if (w < (tid >> 5)) incl += s_scr[w];
+            block += s_scr[w];
+        }
+        incl += base;
+        if (n > 0 && (incl - n) * p.c.Hkv <= unit && unit < incl * p.c.Hkv) {
+            s_scr[W] = b;
+            s_scr[W + 1] = unit - (incl - n) * p.c.Hkv;
+        }
+        base += block;
+        __syncthreads();
+    }
+    *b_out = static_cast<int>(s_scr[W]);
+    *at_out = s_scr[W + 1];
+    *all_out = all;
+    return per;
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int n_ctas) {
+    using C = ChunkCfg<D, E4M3>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* sKV = smem + 2 * C::QT_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + C::NS * C::SLOT);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + PCB_NUM);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    long long* s_scr = reinterpret_cast<long long*>(tmem_holder + 2);   // 18 words of 8 bytes
+    const uint32_t bar0 = smem_u32(bars), sQ_addr = smem_u32(smem), sKV_addr = smem_u32(sKV);
+#define CBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    int b_first;
+    long long at, all;
+    const long long per = chunk_deal<C::THREADS>(p, n_ctas, blockIdx.x, s_scr, blockIdx.x == 0, &b_first, &at, &all);
+    const long long unit0 = blockIdx.x * per;
+    if (unit0 >= all) return;
+    const long long run = min(per, all - unit0);
+
+    if (tid == 0) {
+        mbar_init(CBAR(PCB_QFULL), 1);
+        mbar_init(CBAR(PCB_QEMPTY), 1);
+        mbar_init(CBAR(PCB_DRAIN), 1);
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(CBAR(PCB_S + g), 1);
+            mbar_init(CBAR(PCB_P + g), 4);
+            mbar_init(CBAR(PCB_O + g), 1);
+        }
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(CBAR(PCB_FULL + s), E4M3 ? 4 : 1);
+            mbar_init(CBAR(PCB_EMPTY + s), 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::WARP_MMA) {
+        tmem_alloc(smem_u32(tmem_holder), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const unsigned long long wlim = p.wait_ns;
+    ChunkWalk w;
+    if (warp < 8) {
+        // ================================================================ softmax and epilogue
+        const int g = warp >> 2, r = tid & 127;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + static_cast<uint32_t>(g) * PC_BN;
+        const uint32_t o_addr = tmem + lane_base + C::O_COL + static_cast<uint32_t>(g) * D;
+        const float sl2 = p.scale_log2;
+        const bool pos_scale = sl2 > 0.0f;
+        const float mul = pos_scale ? sl2 : 1.0f;
+        const int r_tok = r / p.G, r_head = r - r_tok * p.G;
+        uint32_t s_phase = 0, o_phase = 0;
+        bool ok = true;
+        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+            const bool live = r_tok < w.c.ntok(g) && r_tok < p.tpt;
+            const int i = w.c.tok(g) + r_tok;
+            const int seen = live ? keys_seen(p.causal, w.kv, w.n_q, i) : 0;
+            const int all_seen = keys_seen(p.causal, w.kv, w.n_q, w.c.tok(g));   // by every live row of the tile
+            float m_ref = -INFINITY, l_sum = 0.0f;
+            const int j1 = w.end(g);
+#pragma unroll 1
+            for (int j = w.t0; j < j1; ++j) {
+                ok = __all_sync(0xffffffffu, chunk_wait(CBAR(PCB_S + g), s_phase, abort_flag, wlim));
+                if (!ok) break;
+                s_phase ^= 1u;
+                tc_fence_after();
+                float x[C::COLS];
+                // columns [c0, c0 + COLS) of the row, masked by selection
+                auto load = [&](int c0) {
+                    uint32_t raw[C::COLS];
+                    if constexpr (C::COLS == 128) tmem_ld128_wait(s_addr, raw);
+                    else tmem_ld64_wait(s_addr + c0, raw);
+                    if ((j + 1) * PC_BN > all_seen) {
+                        const int lim = seen - j * PC_BN - c0;   // columns this row sees
+#pragma unroll
+                        for (int c = 0; c < C::COLS; ++c) x[c] = c < lim ? __uint_as_float(raw[c]) * (pos_scale ? 1.0f : sl2) : -INFINITY;
+                    } else if (pos_scale) {
+#pragma unroll
+                        for (int c = 0; c < C::COLS; ++c) x[c] = __uint_as_float(raw[c]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < C::COLS; ++c) x[c] = __uint_as_float(raw[c]) * sl2;
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c0 = PC_BN - C::COLS; c0 >= 0; c0 -= C::COLS) {
+                    load(c0);
+                    mx = fmaxf(mx, row_max(x));
+                }
+                mx *= mul;
+                float factor = 1.0f;
+                bool rescale = false;
+                if (j == w.t0) {
+                    m_ref = mx;
+                } else if (__any_sync(0xffffffffu, mx > m_ref + PC_RESCALE_LOG2)) {
+                    const float m_new = fmaxf(m_ref, mx);
+                    factor = m_ref == -INFINITY ? 0.0f : exp2_approx(m_ref - m_new);
+                    m_ref = m_new;
+                    rescale = true;
+                }
+                const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;   // a row with no key so far: 2^-inf, not NaN
+                float2 sp[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) sp[t] = make_float2(0.0f, 0.0f);
+                const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(neg_m, neg_m);
+#pragma unroll
+                for (int cc = 0; cc < PC_BN / 32; ++cc) {
+                    constexpr int PER = C::COLS / 32;
+                    if (cc != 0 && cc % PER == 0) load(cc * 32);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = fma2(make_float2(x[cc % PER * 32 + 2 * e], x[cc % PER * 32 + 2 * e + 1]), mul2, neg2);
+                        const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+                        sp[e & 3] = add2(sp[e & 3], make_float2(p0, p1));   // the sum takes the weights unrounded
+                        pk[e] = pack_bf16(p0, p1);
+                    }
+                    tmem_st16(s_addr + cc * 16, pk);
+                }
+                l_sum = l_sum * factor + (((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y)));
+                if (rescale) {
+#pragma unroll 1
+                    for (int oc = 0; oc < D / 32; ++oc) {
+                        uint32_t o[32];
+                        tmem_ld32_wait(o_addr + oc * 32, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+                        tmem_st32(o_addr + oc * 32, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(CBAR(PCB_P + g));
+            }
+            if (!ok) break;
+            const bool has = j1 > w.t0;
+            if (has) {
+                ok = __all_sync(0xffffffffu, chunk_wait(CBAR(PCB_O + g), o_phase, abort_flag, wlim));
+                if (!ok) break;
+                o_phase ^= 1u;
+                tc_fence_after();
+            }
+            const bool some = !(l_sum == 0.0f);   // NaN counts
+            const float inv = some ? 1.0f / l_sum : 0.0f;
+            const float lse = some ? (m_ref + log2f(l_sum)) * 0.69314718055994530942f : -INFINITY;
+            const bool whole = w.whole();
+            const long long row = static_cast<long long>(w.q0) + i;
+            const int hq = w.h * p.G + r_head;
+            const long long part = ((2LL * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * 2 + g) * 128 + r;
+#pragma unroll 1
+            for (int oc = 0; oc < D / 32; ++oc) {
+                uint32_t o[32];
+                if (has) {
+                    tmem_ld32_wait(o_addr + oc * 32, o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (!live) continue;
+                if (whole) {
+                    __nv_bfloat16* dst = p.out + row * p.out_t + hq * p.out_h + oc * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 v;
+                        v.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                        v.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                        v.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                        v.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                        *reinterpret_cast<uint4*>(dst + e) = v;
+                    }
+                } else if (some) {
+                    float* dst = p.part_out + part * D + oc * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(dst + e) = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                                                          __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                }
+            }
+            if (live) {
+                if (!whole) p.part_lse[part] = lse;
+                else if (p.lse != nullptr) p.lse[row * p.Hq + hq] = lse;
+            }
+            tc_fence_before();   // the reads of O_g above, before the next segment's first P
+        }
+    } else if (warp == C::WARP_MMA) {
+        // ================================================================ MMA issuer
+        // The whole warp runs converged; its elected lane issues.
+        constexpr uint32_t IDESC_S = make_idesc_bf16(128, PC_BN, false);
+        constexpr uint32_t IDESC_PV = make_idesc_bf16(128, D, true);
+        const uint64_t q_desc0 = make_smem_desc(sQ_addr, 16, 8 * C::SW, C::LAYOUT);
+        const uint64_t k_desc0 = make_smem_desc(sKV_addr, 16, 8 * C::SW, C::LAYOUT);
+        const uint64_t v_desc0 = make_smem_desc(sKV_addr, PC_BN * C::SW, 8 * C::SW, C::LAYOUT);
+        int k_slot = 0, v_slot = 0;
+        uint32_t item = 0;                       // ring items consumed: K_t0, then V_j, K_{j+1}
+        uint32_t p_phase[2] = {0, 0}, q_phase = 0;
+        bool ok = true;
+        auto next_item = [&]() -> int {          // waits for the next K or V tile; its slot
+            const int slot = static_cast<int>(item % C::NS);
+            ok = ok && chunk_wait_warp(CBAR(PCB_FULL + slot), (item / C::NS) & 1u, abort_flag, wlim);
+            ++item;
+            tc_fence_after();
+            return slot;
+        };
+        auto issue_s = [&](int g) {
+            const uint64_t kd = k_desc0 + static_cast<uint64_t>(k_slot) * (C::SLOT >> 4);
+            const uint64_t qd = q_desc0 + static_cast<uint64_t>(g) * (C::QT_BYTES >> 4);
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                const int c = t / (C::BLK / 16), kk = t % (C::BLK / 16);
+                const uint64_t off = static_cast<uint64_t>(((c * 128 * C::SW) >> 4) + kk * 2);
+                mma_ss_elect(tmem + static_cast<uint32_t>(g) * PC_BN, qd + off, kd + off, IDESC_S, t != 0 ? 1u : 0u);
+            }
+            tc_commit_elect(CBAR(PCB_S + g));
+        };
+        auto issue_pv = [&](int g, bool first) {
+            const uint64_t vd = v_desc0 + static_cast<uint64_t>(v_slot) * (C::SLOT >> 4);
+#pragma unroll
+            for (int kb = 0; kb < PC_BN / 16; ++kb)
+                mma_ts_elect(tmem + C::O_COL + static_cast<uint32_t>(g) * D, tmem + static_cast<uint32_t>(g) * PC_BN + kb * 8u,
+                             vd + static_cast<uint64_t>((kb * 16 * C::SW) >> 4), IDESC_PV, kb == 0 && first ? 0u : 1u);
+        };
+        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+            const int e0 = w.end(0), e1 = w.end(1), je = max(e0, e1);
+            if (je <= w.t0) continue;            // no keys: nothing was loaded
+            ok = chunk_wait_warp(CBAR(PCB_QFULL), q_phase, abort_flag, wlim);
+            q_phase ^= 1u;
+            if (!ok) break;
+            k_slot = next_item();
+            if (!ok) break;
+            if (w.t0 < e0) issue_s(0);
+            if (w.t0 < e1) issue_s(1);
+            tc_commit_elect(CBAR(PCB_EMPTY + k_slot));
+            if (w.t0 + 1 == je) tc_commit_elect(CBAR(PCB_QEMPTY));   // the segment's last S: Q may be replaced
+#pragma unroll 1
+            for (int j = w.t0; j < je && ok; ++j) {
+                v_slot = next_item();
+                if (!ok) break;
+                if constexpr (!E4M3) {
+                    // rows of the last copied box that lie behind the sequence: cleared, since
+                    // 0 * NaN would reach every row
+                    const int valid = w.kv - j * PC_BN;
+                    const int dirty = valid < PC_BN ? (valid + p.box_rows - 1) / p.box_rows * p.box_rows : 0;
+                    if (valid < dirty) {
+                        constexpr int CH = C::SW / 16;
+                        for (int x = lane; x < (dirty - valid) * CH * C::NBLK; x += 32) {
+                            const int blk = x / ((dirty - valid) * CH), y = x % ((dirty - valid) * CH);
+                            *reinterpret_cast<uint4*>(sKV + v_slot * C::SLOT + blk * (PC_BN * C::SW) + (valid + y / CH) * C::SW + y % CH * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                        __syncwarp();
+                    }
+                }
+                const bool more = j + 1 < je;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int eg = g ? e1 : e0;
+                    if (j < eg) {
+                        ok = chunk_wait_warp(CBAR(PCB_P + g), p_phase[g], abort_flag, wlim);
+                        if (!ok) break;
+                        p_phase[g] ^= 1u;
+                        tc_fence_after();
+                        issue_pv(g, j == w.t0);
+                        if (j + 1 == eg) tc_commit_elect(CBAR(PCB_O + g));
+                    }
+                    if (g == 0 && more) {
+                        k_slot = next_item();
+                        if (!ok) break;
+                    }
+                    if (j + 1 < eg) issue_s(g);
+                }
+                if (!ok) break;
+                tc_commit_elect(CBAR(PCB_EMPTY + v_slot));
+                if (more) tc_commit_elect(CBAR(PCB_EMPTY + k_slot));
+                if (j + 2 == je) tc_commit_elect(CBAR(PCB_QEMPTY));
+            }
+        }
+        // every MMA issued completes before TMEM is released
+        tc_commit_elect(CBAR(PCB_DRAIN));
+        __syncwarp();
+        const uint64_t d0 = global_timer_ns();
+        while (!mbar_try_wait(CBAR(PCB_DRAIN), 0)) {
+            if (global_timer_ns() - d0 > wlim) {
+                atomicOr(&g_paged_status, STATUS_TIMEOUT);
+                break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == C::WARP_COPY) {
+        // ================================================================ copies: Q, and bf16 K and V
+        if (lane == 0) {
+            tma_prefetch_map(&tm_q);
+            if constexpr (!E4M3) {
+                tma_prefetch_map(&tm_k);
+                tma_prefetch_map(&tm_v);
+            }
+        }
+        uint32_t item = 0, qe_phase = 0;
+        bool ok = true, first = true;
+        const int boxes = PC_BN / p.box_rows;
+        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+            const int je = max(w.end(0), w.end(1));
+            if (je <= w.t0) continue;
+            if (!first) {
+                ok = chunk_wait_warp(CBAR(PCB_QEMPTY), qe_phase, abort_flag, wlim);
+                qe_phase ^= 1u;
+                if (!ok) break;
+            }
+            first = false;
+            if (lane == 0) {
+                const bool both = w.c.ntok1 > 0;
+                mbar_arrive_expect_tx(CBAR(PCB_QFULL), (both ? 2 : 1) * p.tpt * p.G * D * 2);
+                for (int g = 0; g < (both ? 2 : 1); ++g)
+#pragma unroll
+                    for (int c = 0; c < C::NBLK; ++c)
+                        tma_load_4d(sQ_addr + g * C::QT_BYTES + c * 128 * C::SW, &tm_q, c * C::BLK, 0, w.h, w.q0 + w.c.tok(g), CBAR(PCB_QFULL));
+            }
+            if constexpr (!E4M3) {
+                // lane i < boxes copies box i of every tile; its page is looked up one tile ahead
+                const int32_t* table = p.table + w.b * p.table_stride;
+                auto lookup = [&](int j, int* row) {
+                    const int key = j * PC_BN + lane * p.box_rows;
+                    int page = p.c.num_pages;            // outside the pool: zeros
+                    *row = 0;
+                    if (lane < boxes && j < je && key < w.kv) {
+                        const int pj = page_index(p, key);
+                        const int got = __ldg(table + pj);
+                        if (got >= 0 && got < p.c.num_pages) {
+                            page = got;
+                            *row = key - pj * p.c.page_size;
+                        } else {
+                            atomicOr(&g_paged_status, STATUS_CACHE);
+                        }
+                    }
+                    return page;
+                };
+                int row = 0, row_n = 0;
+                int page = lookup(w.t0, &row);
+                for (int j = w.t0; j < je && ok; ++j) {
+                    const int page_n = lookup(j + 1, &row_n);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int slot = static_cast<int>(item % C::NS);
+                        ok = chunk_wait_warp(CBAR(PCB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
+                        if (!ok) break;
+                        ++item;
+                        if (lane == 0) mbar_arrive_expect_tx(CBAR(PCB_FULL + slot), C::SLOT);
+                        __syncwarp();
+                        const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && kv == 0 && j == w.t0 && lane == 0;
+                        if (lane < boxes && !drop) {
+                            const uint32_t dst = sKV_addr + slot * C::SLOT + lane * p.box_rows * C::SW;
+#pragma unroll
+                            for (int c = 0; c < C::NBLK; ++c)
+                                tma_load_4d(dst + c * (PC_BN * C::SW), kv ? &tm_v : &tm_k, c * C::BLK, row, w.h, page, CBAR(PCB_FULL + slot));
+                        }
+                        __syncwarp();
+                    }
+                    page = page_n;
+                    row = row_n;
+                }
+            }
+        }
+        if (*abort_flag || !ok) {
+            // Copies in flight must land before the memory is reused; they have no one to wait for them.
+            const uint64_t d0 = global_timer_ns();
+            while (global_timer_ns() - d0 < 2000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (E4M3 && warp < 12) {
+        // ================================================================ converters: e4m3 K and V
+        if constexpr (E4M3) {
+            constexpr int CPR = D / 16;          // 16-code chunks per row
+            constexpr int X = CPR;               // chunks per thread: 128 rows * CPR / 128 threads
+            constexpr int RPX = 128 / CPR;       // rows between a thread's chunks
+            const int t = tid - 256;
+            const int r0 = t / CPR, c16 = t % CPR;
+            uint4 data[X];
+            uint32_t scale[X];
+            // the item (key tile j of segment w; K or V) whose loads are in flight
+            uint32_t item = 0;
+            bool ok = true;
+            auto fetch = [&](int x, int j, int which) {
+                const int key = j * PC_BN + x * RPX + r0;
+                data[x] = make_uint4(0u, 0u, 0u, 0u);
+                scale[x] = 127u;
+                if (key < w.kv) {
+                    const int pj = page_index(p, key);
+                    const int row = key - pj * p.c.page_size;
+                    const int page = __ldg(p.table + w.b * p.table_stride + pj);
+                    if (page >= 0 && page < p.c.num_pages) {
+                        data[x] = __ldg(reinterpret_cast<const uint4*>(p.c.data[which] + page * p.c.sp[which] + w.h * p.c.sh[which] + row * p.c.st[which]) + c16);
+                        scale[x] = __ldg(p.c.scale[which] + (static_cast<long long>(page) * p.c.Hkv + w.h) * p.c.page_size + row);
+                    } else if (which == 0 && c16 == 0) {
+                        atomicOr(&g_paged_status, STATUS_CACHE);
+                    }
+                }
+            };
+            for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+                const int je = max(w.end(0), w.end(1));
+                if (je <= w.t0) continue;
+#pragma unroll
+                for (int x = 0; x < X; ++x) fetch(x, w.t0, 0);
+                for (int j2 = 2 * w.t0; j2 < 2 * je && ok; ++j2) {   // item: tile j2 / 2, K or V
+                    const int slot = static_cast<int>(item % C::NS);
+                    ok = chunk_wait_warp(CBAR(PCB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
+                    if (!ok) break;
+                    ++item;
+                    const int nj = (j2 + 1) >> 1, nw = (j2 + 1) & 1;
+                    uint8_t* dst = sKV + slot * C::SLOT;
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        const uint4 d = data[x];
+                        const uint32_t code = scale[x];
+                        if (j2 + 1 < 2 * je) fetch(x, nj, nw);
+                        const uint32_t f = scale_factor(code) * 0x10001u;
+                        uint32_t o[8];
+                        const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[2 * e] = widen2(__byte_perm(wd[e], 0u, 0x1404), f);
+                            o[2 * e + 1] = widen2(__byte_perm(wd[e], 0u, 0x3424), f);
+                        }
+                        if (code > 134u && code != SCALE_NAN) {   // a scale above 2^7: the rest of it
+                            const uint32_t f2 = (code - 7u) << 7;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f2 * 0x10001u);
+                        }
+                        const int r = x * RPX + r0;
+                        const int col = c16 * 16;
+                        const int blk = col / C::BLK, ch = (col % C::BLK) / 8;   // 16-byte chunks ch, ch + 1 of the block's row
+                        uint8_t* line = dst + blk * (PC_BN * C::SW) + r * C::SW;
+                        const int sw = C::SW == 128 ? r & 7 : (r >> 1) & 3;
+                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                        // lanes of the second column block store their second half first: all banks at once
+                        const bool flip = blk & 1;
+                        *reinterpret_cast<uint4*>(line + (((ch + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? hi : lo;
+                        *reinterpret_cast<uint4*>(line + (((ch + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? lo : hi;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(CBAR(PCB_FULL + slot));
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+#undef CBAR
+}
+
+// Token tiles that several CTAs of paged_chunk_kernel shared.  Block c (x) looks at the border
+// between the runs of CTAs c and c + 1; the first border inside a tile puts the tile together,
+// its rows spread over blockIdx.y.  CTA c's part is slot 2c, or 2c + 1 where the tile begins in its run.
+template <int D>
+__global__ void __launch_bounds__(128) paged_chunk_combine_kernel(const PagedParams p, const int n_ctas) {
+    __shared__ long long s_scr[8];
+    int b;
+    long long at, all;
+    const long long c = blockIdx.x + 1;
+    const long long per = chunk_deal<128>(p, n_ctas, c, s_scr, false, &b, &at, &all);
+    if (c * per >= all) return;
+    ChunkWalk w;
+    w.begin(p, b, at, all);
+    if (w.t0 == 0) return;                      // the border lies between two tiles
+    const long long u0 = c * per - w.t0;        // the tile's first unit
+    const long long c0 = u0 / per, c1 = (u0 + w.c.n - 1) / per;
+    if (c != c0 + 1) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int PER = D / 32;
+    for (int r = blockIdx.y * 4 + warp; r < 256; r += gridDim.y * 4) {
+        const int g = r >> 7, rr = r & 127, tok = rr / p.G;
+        if (tok >= w.c.ntok(g) || tok >= p.tpt) continue;
+        auto slot = [&](long long cc) { return ((2 * cc + (cc == c0 ? 1 : 0)) * 2 + g) * 128 + rr; };
+        float M = -INFINITY;
+        for (long long cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldg(p.part_lse + slot(cc)));
+        float s = 0.0f, acc[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = 0.0f;
+        for (long long cc = c0; cc <= c1; ++cc) {
+            const float lc = __ldg(p.part_lse + slot(cc));
+            if (lc == -INFINITY) continue;      // nothing was stored
+            const float wgt = expf(lc - M);
+            s += wgt;
+            const float* src = p.part_out + slot(cc) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] += wgt * __ldg(src + e);
+        }
+        const bool some = !(s == 0.0f);
+        const float inv = some ? 1.0f / s : 0.0f;
+        const long long row = static_cast<long long>(w.q0) + w.c.tok(g) + tok;
+        const int hq = w.h * p.G + rr - tok * p.G;
+        __nv_bfloat16* dst = p.out + row * p.out_t + hq * p.out_h + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) dst[e] = __float2bfloat16_rn(acc[e] * inv);
+        if (lane == 0 && p.lse != nullptr) p.lse[row * p.Hq + hq] = some ? M + logf(s) : -INFINITY;
+    }
+}
