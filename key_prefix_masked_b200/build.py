@@ -17,7 +17,7 @@ LIB_NAME = "libattn_prefix.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["attn_prefix.cu", "paged.cu"]
 HEADERS = ["host_common.h", "ptx.cuh", "tmem_ops.cuh", "softmax_math.cuh", "pair_kernel.cuh", "segments.cuh",
-           "rope.cuh", "cache.cuh", "paged_simple.cuh", "paged_rows.cuh", "paged_chunk.cuh"]
+           "rope.cuh", "cache.cuh", "paged_rows.cuh", "paged_chunk.cuh", "paged_pair.cuh"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

@@ -1,6 +1,7 @@
 // paged.cu -- serving operators around the prefix-masked attention: per-head norm and
 // rotation of q and k (rope.cuh), a paged key/value cache written and read back
-// (cache.cuh), and attention of new tokens over the pages (paged_rows.cuh, paged_simple.cuh).  The C ABI is
+// (cache.cuh), and attention of new tokens over the pages (paged_rows.cuh for
+// few query rows per key head, paged_chunk.cuh and paged_pair.cuh for many).  The C ABI is
 // in include/attn_prefix.h.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -84,9 +85,9 @@ __device__ __forceinline__ int checked_page(const PagedParams& p, int b, int pj,
     return -1;
 }
 
-#include "paged_simple.cuh"
 #include "paged_rows.cuh"
 #include "paged_chunk.cuh"
+#include "paged_pair.cuh"
 
 bool take_paged_flags(unsigned* flags) {
     const unsigned zero = 0;
@@ -222,38 +223,56 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
     return launched();
 }
 
-// CTAs of the chunk kernel: one per SM, or fewer where the largest possible work needs fewer.
+// Runs of the chunk kernels: one per SM (per CTA pair at head dim 256), or fewer where the
+// largest possible work needs fewer.
 constexpr int CHUNK_MIN_UNITS = 2;
-int chunk_ctas(int B, int Hkv, int G, long long max_q, long long kv_cap) {
-    const int tokens = 2 * (128 / G);
+int chunk_runs(int B, int Hkv, int G, int D, long long max_q, long long kv_cap) {
+    const int tokens = 2 * (128 / G), all = D == 256 ? SM_COUNT / 2 : SM_COUNT;
     const long long tiles = static_cast<long long>(B) * Hkv * ((max_q + tokens - 1) / tokens);
     const long long units = tiles * ((kv_cap + PC_BN - 1) / PC_BN);
     const long long most = (units + CHUNK_MIN_UNITS - 1) / CHUNK_MIN_UNITS;
-    return static_cast<int>(most < SM_COUNT ? most : SM_COUNT);
+    return static_cast<int>(most < all ? most : all);
 }
 
 template <int D, bool E4M3>
 attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
-    using C = ChunkCfg<D, E4M3>;
-    const int n = chunk_ctas(p.B, p.c.Hkv, p.G, p.max_q, p.kv_cap);
+    constexpr bool PAIR = D == 256;
+    constexpr int BLK = D >= 64 ? 64 : 32;
+    const int n = chunk_runs(p.B, p.c.Hkv, p.G, D, p.max_q, p.kv_cap);
     p.min_units = CHUNK_MIN_UNITS;
     p.part_out = static_cast<float*>(workspace);
     p.part_lse = p.part_out + 512LL * n * D;
     p.tpt = 128 / p.G;
     p.box_rows = p.c.page_size & -p.c.page_size;   // the largest power of two that divides it
-    if (p.box_rows > PC_BN) p.box_rows = PC_BN;
-    const CUtensorMapSwizzle swz = C::SW == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const int most = PAIR ? 64 : PC_BN;
+    if (p.box_rows > most) p.box_rows = most;
+    const CUtensorMapSwizzle swz = BLK == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     CUtensorMap mq, mk, mv;
-    if (!make_map(&mq, p.q, p.T, p.c.Hkv, p.G, D, {p.q_t, p.G * p.q_h, p.q_h}, C::BLK, p.G, swz, p.tpt)) return ATTN_ERR_CUDA;
+    if (!make_map(&mq, p.q, p.T, p.c.Hkv, p.G, D, {p.q_t, p.G * p.q_h, p.q_h}, BLK, p.G, swz, p.tpt)) return ATTN_ERR_CUDA;
     mk = mv = mq;
-    if (!E4M3 && (!make_map(&mk, p.c.data[0], p.c.num_pages, p.c.Hkv, p.c.page_size, D, {p.c.sp[0] / 2, p.c.sh[0] / 2, p.c.st[0] / 2}, C::BLK, p.box_rows, swz) ||
-                  !make_map(&mv, p.c.data[1], p.c.num_pages, p.c.Hkv, p.c.page_size, D, {p.c.sp[1] / 2, p.c.sh[1] / 2, p.c.st[1] / 2}, C::BLK, p.box_rows, swz)))
+    if (!E4M3 && (!make_map(&mk, p.c.data[0], p.c.num_pages, p.c.Hkv, p.c.page_size, D, {p.c.sp[0] / 2, p.c.sh[0] / 2, p.c.st[0] / 2}, BLK, p.box_rows, swz) ||
+                  !make_map(&mv, p.c.data[1], p.c.num_pages, p.c.Hkv, p.c.page_size, D, {p.c.sp[1] / 2, p.c.sh[1] / 2, p.c.st[1] / 2}, BLK, p.box_rows, swz)))
         return ATTN_ERR_CUDA;
-    if (cudaFuncSetAttribute(paged_chunk_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
+    int grid, threads, smem;
+    void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedParams, int);
+    if constexpr (PAIR) {
+        using C = PagedPairCfg<E4M3>;
+        kern = paged_pair_kernel<E4M3>;
+        grid = 2 * n;
+        threads = C::THREADS;
+        smem = C::SMEM;
+    } else {
+        using C = ChunkCfg<D, E4M3>;
+        kern = paged_chunk_kernel<D, E4M3>;
+        grid = n;
+        threads = C::THREADS;
+        smem = C::SMEM;
+    }
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
     }
-    paged_chunk_kernel<D, E4M3><<<n, C::THREADS, C::SMEM, stream>>>(mq, mk, mv, p, n);
+    kern<<<grid, threads, smem, stream>>>(mq, mk, mv, p, n);
     if (n > 1) paged_chunk_combine_kernel<D><<<dim3(n - 1, 8), 128, 0, stream>>>(p, n);
     return launched();
 }
@@ -261,13 +280,7 @@ attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
 template <int D>
 attn_status launch_paged(const PagedParams& p, void* workspace, cudaStream_t stream) {
     if (few_rows(p.max_q, p.G)) return p.c.e4m3 ? launch_rows<D, true>(p, workspace, stream) : launch_rows<D, false>(p, workspace, stream);
-    if constexpr (D <= 128)
-        return p.c.e4m3 ? launch_chunk<D, true>(p, workspace, stream) : launch_chunk<D, false>(p, workspace, stream);
-    const long long grid = (static_cast<long long>(p.B) * p.Hq * p.max_q + 3) / 4;
-    if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
-    if (p.c.e4m3) paged_simple_kernel<D, true><<<static_cast<unsigned>(grid), 128, 0, stream>>>(p);
-    else paged_simple_kernel<D, false><<<static_cast<unsigned>(grid), 128, 0, stream>>>(p);
-    return launched();
+    return p.c.e4m3 ? launch_chunk<D, true>(p, workspace, stream) : launch_chunk<D, false>(p, workspace, stream);
 }
 
 #define ATTN_BY_HEAD_DIM(D, CALL)          \
@@ -381,9 +394,7 @@ size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page
         return 0;
     if (few_rows(max_q < T ? max_q : T, Hq / Hkv))
         return 2ull * rows_ctas(2, B, Hkv, static_cast<long long>(max_pages) * page_size) * PR_ROWS * (D + 1) * sizeof(float);
-    if (D <= 128)
-        return 512ull * chunk_ctas(B, Hkv, Hq / Hkv, max_q < T ? max_q : T, static_cast<long long>(max_pages) * page_size) * (D + 1) * sizeof(float);
-    return 0;
+    return 512ull * chunk_runs(B, Hkv, Hq / Hkv, D, max_q < T ? max_q : T, static_cast<long long>(max_pages) * page_size) * (D + 1) * sizeof(float);
 }
 
 attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_strides* q_strides,

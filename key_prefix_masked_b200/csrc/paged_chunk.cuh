@@ -57,11 +57,13 @@ enum : int {
     PCB_FULL = 9 /* [12] */, PCB_EMPTY = 21 /* [12] */, PCB_NUM = 33
 };
 
+template <bool CLUSTER = false>   // acquire at cluster scope
 __device__ __noinline__ bool chunk_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
+    auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (done()) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (done()) return true;
         if (*abort_flag) return false;
         if (global_timer_ns() - t0 > limit_ns) {
             *abort_flag = 1;
@@ -71,8 +73,9 @@ __device__ __noinline__ bool chunk_wait(uint32_t bar, uint32_t parity, volatile 
     }
 }
 // The same for a whole warp that stays converged: lane 0's answer.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool chunk_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
-    return __shfl_sync(0xffffffffu, chunk_wait(bar, parity, abort_flag, limit_ns) ? 1 : 0, 0) != 0;
+    return __shfl_sync(0xffffffffu, chunk_wait<CLUSTER>(bar, parity, abort_flag, limit_ns) ? 1 : 0, 0) != 0;
 }
 
 // Keys that query row i of a sequence with n rows and kv keys sees.
@@ -669,7 +672,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(CBAR(PCB_FULL + slot));
+                    const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && item == 1 && warp == 8;
+                    if (lane == 0 && !drop) mbar_arrive(CBAR(PCB_FULL + slot));
                 }
             }
         }

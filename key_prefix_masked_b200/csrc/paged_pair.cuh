@@ -1,0 +1,538 @@
+// paged_pair.cuh -- attention over pages for many query rows per key head at head dim 256,
+// on CTA pairs (cta_group::2).  Included by paged.cu inside namespace attn, after
+// paged_chunk.cuh, whose rows, walk and deal of the work it shares (a run belongs to a pair).
+//
+// At 256 dims a 128-row tile fills a CTA's TMEM (S twice, O), so each CTA of a pair takes one of
+// the two row tiles and half of every K and V tile (keys [64 r, +64) of K, value columns
+// [128 r, +128) of V for rank r): M = 256 MMAs issued by the leader read A from each CTA and
+// B across both, and each K/V byte brought to an SM still serves 256 rows.
+//
+// MMA order per segment: S(0), S(1), then PV(j), S(j+2), P(j) stored over S(j).  The
+// softmax of tile j runs under the MMAs of its neighbours.  A rescale of O waits for
+// PV(j-1), announced by one commit per PV.
+//
+// The pages behind a sequence: boxes that lie behind it entirely read as zeros (their page
+// coordinate is outside the pool); the rows of the last V box are loaded and stored by the
+// copying warp itself, zeros behind the sequence, and its arrival orders them before the MMA.
+
+template <bool E4M3>
+struct PagedPairCfg {
+    static constexpr int D = 256;
+    static constexpr int QT_BYTES = 128 * D * 2;
+    static constexpr int KH = 64;                       // keys of a K tile held by one CTA
+    static constexpr int KBLK = KH * 128;               // one 64-column block of them
+    static constexpr int VBLK = PC_BN * 128;            // one 64-column block of V
+    static constexpr int SLOT = 32768;                  // one CTA's half of a K or V tile
+    static constexpr int NS = 5;
+    static constexpr int CTRL = 1024;
+    static constexpr int SMEM = QT_BYTES + NS * SLOT + CTRL;
+    static constexpr uint32_t O_COL = 256;
+    // warps 0-3 softmax, 4 Q (and bf16 K, V) copies, 5 MMA (leader) and TMEM; e4m3: 6 and 7 idle, 8-11 converters
+    static constexpr int WARP_COPY = 4, WARP_MMA = 5, WARP_CONV = 8;
+    static constexpr int THREADS = E4M3 ? 384 : 192;
+};
+enum : int {
+    PPB_QFULL = 0, PPB_QEMPTY = 1, PPB_S = 2 /* [2] */, PPB_P = 4 /* [2] */, PPB_PV = 6, PPB_DRAIN = 7,
+    PPB_FULL = 8 /* [5] */, PPB_EMPTY = 13 /* [5] */, PPB_NUM = 18
+};
+
+// Arrival on a barrier of the pair's leader that orders this thread's earlier shared-memory
+// stores (after a proxy fence) before the leader's MMAs.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+}
+
+template <bool E4M3>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::THREADS, 1)
+    paged_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int n_pairs) {
+    using C = PagedPairCfg<E4M3>;
+    constexpr int D = C::D;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    // swizzled tiles need 1024-byte alignment; both CTAs see the same layout and return together
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(&g_paged_status, STATUS_LAYOUT);
+        return;
+    }
+    uint8_t* sKV = smem + C::QT_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + C::NS * C::SLOT);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + PPB_NUM);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    long long* s_scr = reinterpret_cast<long long*>(tmem_holder + 2);
+    const uint32_t bar0 = smem_u32(bars), sQ_addr = smem_u32(smem), sKV_addr = smem_u32(sKV);
+#define PPBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const bool leader = rank == 0;
+    const long long pair = blockIdx.x >> 1;
+
+    int b_first;
+    long long at, all;
+    const long long per = chunk_deal<C::THREADS>(p, n_pairs, pair, s_scr, blockIdx.x == 0, &b_first, &at, &all);
+    const long long unit0 = pair * per;
+    if (unit0 >= all) return;   // both CTAs of the pair
+    const long long run = min(per, all - unit0);
+
+    if (tid == 0) {
+        mbar_init(PPBAR(PPB_QFULL), 1);
+        mbar_init(PPBAR(PPB_QEMPTY), 1);
+        mbar_init(PPBAR(PPB_PV), 1);
+        mbar_init(PPBAR(PPB_DRAIN), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(PPBAR(PPB_S + i), 1);
+            mbar_init(PPBAR(PPB_P + i), 8);
+        }
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(PPBAR(PPB_FULL + s), E4M3 ? 8 : 2);
+            mbar_init(PPBAR(PPB_EMPTY + s), 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == C::WARP_MMA) {
+        tmem_alloc_pair(smem_u32(tmem_holder), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const unsigned long long wlim = p.wait_ns;
+    ChunkWalk w;
+
+    if (warp < 4) {
+        // ================================================================ softmax and epilogue (both CTAs)
+        const int g = rank, r = tid;
+        const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+        const uint32_t o_addr = tmem + lane_base + C::O_COL;
+        const float sl2 = p.scale_log2;
+        const bool pos_scale = sl2 > 0.0f;
+        const float mul = pos_scale ? sl2 : 1.0f;
+        const int r_tok = r / p.G, r_head = r - r_tok * p.G;
+        const uint32_t p_bar[2] = {mapa_shared(PPBAR(PPB_P), 0), mapa_shared(PPBAR(PPB_P + 1), 0)};
+        uint32_t cnt = 0;   // key tiles processed, over all segments
+        bool ok = true;
+        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+            const bool live = r_tok < w.c.ntok(g) && r_tok < p.tpt;
+            const int i = w.c.tok(g) + r_tok;
+            const int seen = live ? keys_seen(p.causal, w.kv, w.n_q, i) : 0;
+            const int all_seen = keys_seen(p.causal, w.kv, w.n_q, w.c.tok(g));
+            float m_ref = -INFINITY, l_sum = 0.0f;
+            const int je = max(w.end(0), w.end(1));
+#pragma unroll 1
+            for (int j = w.t0; j < je; ++j) {
+                ok = __all_sync(0xffffffffu, chunk_wait(PPBAR(PPB_S + (cnt & 1)), (cnt >> 1) & 1, abort_flag, wlim));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t s_addr = tmem + lane_base + (cnt & 1) * PC_BN;
+                uint32_t raw[PC_BN];
+                tmem_ld128_wait(s_addr, raw);
+                float x[PC_BN];
+                if ((j + 1) * PC_BN > all_seen) {
+                    const int lim = seen - j * PC_BN;
+#pragma unroll
+                    for (int c = 0; c < PC_BN; ++c) x[c] = c < lim ? __uint_as_float(raw[c]) * (pos_scale ? 1.0f : sl2) : -INFINITY;
+                } else if (pos_scale) {
+#pragma unroll
+                    for (int c = 0; c < PC_BN; ++c) x[c] = __uint_as_float(raw[c]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < PC_BN; ++c) x[c] = __uint_as_float(raw[c]) * sl2;
+                }
+                const float mx = row_max(x) * mul;
+                float factor = 1.0f;
+                bool rescale = false;
+                if (j == w.t0) {
+                    m_ref = mx;
+                } else if (__any_sync(0xffffffffu, mx > m_ref + PC_RESCALE_LOG2)) {
+                    const float m_new = fmaxf(m_ref, mx);
+                    factor = m_ref == -INFINITY ? 0.0f : exp2_approx(m_ref - m_new);
+                    m_ref = m_new;
+                    rescale = true;
+                }
+                const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;
+                float2 sp[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) sp[t] = make_float2(0.0f, 0.0f);
+                const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(neg_m, neg_m);
+#pragma unroll
+                for (int cc = 0; cc < PC_BN / 32; ++cc) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = fma2(make_float2(x[cc * 32 + 2 * e], x[cc * 32 + 2 * e + 1]), mul2, neg2);
+                        const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+                        sp[e & 3] = add2(sp[e & 3], make_float2(p0, p1));
+                        pk[e] = pack_bf16(p0, p1);
+                    }
+                    tmem_st16(s_addr + cc * 16, pk);
+                }
+                l_sum = l_sum * factor + (((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y)));
+                if (rescale) {
+                    // PV of the tile before: commit number cnt - 1 on its barrier, and none after it yet
+                    ok = __all_sync(0xffffffffu, chunk_wait(PPBAR(PPB_PV), (cnt - 1) & 1, abort_flag, wlim));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int oc = 0; oc < D / 32; ++oc) {
+                        uint32_t o[32];
+                        tmem_ld32_wait(o_addr + oc * 32, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+                        tmem_st32(o_addr + oc * 32, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(p_bar[cnt & 1]);
+                ++cnt;
+            }
+            if (!ok) break;
+            const bool has = je > w.t0;
+            if (has) {
+                // The last two PVs in turn: a parity wait tells one phase from the next only, and
+                // "S ready" of the last tile vouches for the PVs up to two before it.
+                ok = cnt < 2 || chunk_wait(PPBAR(PPB_PV), cnt & 1, abort_flag, wlim);
+                ok = __all_sync(0xffffffffu, ok && chunk_wait(PPBAR(PPB_PV), (cnt - 1) & 1, abort_flag, wlim));
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const bool some = !(l_sum == 0.0f);   // NaN counts
+            const float inv = some ? 1.0f / l_sum : 0.0f;
+            const float lse = some ? (m_ref + log2f(l_sum)) * 0.69314718055994530942f : -INFINITY;
+            const bool whole = w.whole();
+            const long long row = static_cast<long long>(w.q0) + i;
+            const int hq = w.h * p.G + r_head;
+            const long long part = ((2 * pair + (w.t0 == 0 ? 1 : 0)) * 2 + g) * 128 + r;
+#pragma unroll 1
+            for (int oc = 0; oc < D / 32; ++oc) {
+                uint32_t o[32];
+                if (has) {
+                    tmem_ld32_wait(o_addr + oc * 32, o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (!live) continue;
+                if (whole) {
+                    __nv_bfloat16* dst = p.out + row * p.out_t + hq * p.out_h + oc * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 v;
+                        v.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                        v.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                        v.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                        v.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                        *reinterpret_cast<uint4*>(dst + e) = v;
+                    }
+                } else if (some) {
+                    float* dst = p.part_out + part * D + oc * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(dst + e) = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                                                          __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                }
+            }
+            if (live) {
+                if (!whole) p.part_lse[part] = lse;
+                else if (p.lse != nullptr) p.lse[row * p.Hq + hq] = lse;
+            }
+            tc_fence_before();   // the reads of O above, before the next segment's first P
+        }
+    } else if (warp == C::WARP_MMA) {
+        // ================================================================ MMA issuer (leader)
+        if (leader) {
+            constexpr uint32_t IDESC_S = make_idesc_bf16(256, PC_BN, false);
+            constexpr uint32_t IDESC_PV = make_idesc_bf16(256, D, true);
+            const uint64_t q_desc0 = make_smem_desc(sQ_addr, 16, 1024, 2);
+            const uint64_t k_desc0 = make_smem_desc(sKV_addr, 16, 1024, 2);
+            const uint64_t v_desc0 = make_smem_desc(sKV_addr, C::VBLK, 1024, 2);
+            uint32_t item = 0, s_cnt = 0, p_cnt = 0, q_phase = 0;
+            bool ok = true;
+            auto next_item = [&]() -> int {
+                const int slot = static_cast<int>(item % C::NS);
+                ok = ok && chunk_wait_warp<true>(PPBAR(PPB_FULL + slot), (item / C::NS) & 1u, abort_flag, wlim);
+                ++item;
+                tc_fence_after();
+                return slot;
+            };
+            auto issue_s = [&]() {
+                const int slot = next_item();
+                if (!ok) return;
+                const uint64_t kd = k_desc0 + static_cast<uint64_t>(slot) * (C::SLOT >> 4);
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) {
+                    const int c = t >> 2, kk = t & 3;
+                    mma_ss_pair_elect(tmem + (s_cnt & 1) * PC_BN, q_desc0 + static_cast<uint64_t>(((c * 128 * 128) >> 4) + kk * 2),
+                                      kd + static_cast<uint64_t>(((c * C::KBLK) >> 4) + kk * 2), IDESC_S, t != 0 ? 1u : 0u);
+                }
+                tc_commit_pair_elect(PPBAR(PPB_EMPTY + slot), 0x3);
+                tc_commit_pair_elect(PPBAR(PPB_S + (s_cnt & 1)), 0x3);
+                ++s_cnt;
+            };
+            for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+                const int je = max(w.end(0), w.end(1));
+                if (je <= w.t0) continue;
+                ok = chunk_wait_warp(PPBAR(PPB_QFULL), q_phase, abort_flag, wlim);
+                q_phase ^= 1u;
+                if (!ok) break;
+                issue_s();
+                if (ok && w.t0 + 1 < je) issue_s();
+                if (ok && w.t0 + 2 >= je) tc_commit_pair_elect(PPBAR(PPB_QEMPTY), 0x3);   // the segment's last S
+#pragma unroll 1
+                for (int j = w.t0; j < je && ok; ++j) {
+                    const int slot = next_item();   // V
+                    ok = ok && chunk_wait_warp(PPBAR(PPB_P + (p_cnt & 1)), (p_cnt >> 1) & 1, abort_flag, wlim);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = v_desc0 + static_cast<uint64_t>(slot) * (C::SLOT >> 4);
+#pragma unroll
+                    for (int kb = 0; kb < PC_BN / 16; ++kb)
+                        mma_ts_pair_elect(tmem + C::O_COL, tmem + (p_cnt & 1) * PC_BN + kb * 8u,
+                                          vd + static_cast<uint64_t>((kb * 16 * 128) >> 4), IDESC_PV, kb == 0 && j == w.t0 ? 0u : 1u);
+                    tc_commit_pair_elect(PPBAR(PPB_EMPTY + slot), 0x3);
+                    tc_commit_pair_elect(PPBAR(PPB_PV), 0x3);
+                    ++p_cnt;
+                    if (j + 2 < je) {
+                        issue_s();
+                        if (ok && j + 3 == je) tc_commit_pair_elect(PPBAR(PPB_QEMPTY), 0x3);
+                    }
+                }
+            }
+            tc_commit_pair_elect(PPBAR(PPB_DRAIN), 0x1);
+            __syncwarp();
+            const uint64_t d0 = global_timer_ns();
+            while (!mbar_try_wait(PPBAR(PPB_DRAIN), 0)) {
+                if (global_timer_ns() - d0 > wlim) {
+                    atomicOr(&g_paged_status, STATUS_TIMEOUT);
+                    break;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == C::WARP_COPY) {
+        // ================================================================ copies (both CTAs): Q, and bf16 K and V halves
+        if (lane == 0) {
+            tma_prefetch_map(&tm_q);
+            if constexpr (!E4M3) {
+                tma_prefetch_map(&tm_k);
+                tma_prefetch_map(&tm_v);
+            }
+        }
+        // Q is read once; half of the K/V lines are kept in L2 ahead of it and of the output
+        const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last_half();
+        const uint32_t l_q = mapa_shared(PPBAR(PPB_QFULL), 0);
+        uint32_t item = 0, qe_phase = 0;
+        bool ok = true, first = true;
+        const int k_boxes = C::KH / p.box_rows, v_boxes = PC_BN / p.box_rows;   // box_rows <= 64
+        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+            const int je = max(w.end(0), w.end(1));
+            if (je <= w.t0) continue;
+            if (!first) {
+                ok = chunk_wait_warp(PPBAR(PPB_QEMPTY), qe_phase, abort_flag, wlim);
+                qe_phase ^= 1u;
+                if (!ok) break;
+            }
+            first = false;
+            if (lane == 0) {
+                if (leader) mbar_arrive_expect_tx(PPBAR(PPB_QFULL), (w.c.ntok1 > 0 ? 2 : 1) * p.tpt * p.G * D * 2);
+                if (w.c.ntok(rank) > 0)
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_4d_pair_hint(sQ_addr + c * 128 * 128, &tm_q, c * 64, 0, w.h, w.q0 + w.c.tok(rank), l_q, pol_q);
+            }
+            if constexpr (!E4M3) {
+                const int32_t* table = p.table + w.b * p.table_stride;
+                // lane i: box i of this CTA's K half / of V
+                auto lookup = [&](int j, bool k, int* row) {
+                    const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * p.box_rows;
+                    int page = p.c.num_pages;
+                    *row = 0;
+                    if (lane < (k ? k_boxes : v_boxes) && j < je && key < w.kv) {
+                        const int pj = page_index(p, key);
+                        const int got = __ldg(table + pj);
+                        if (got >= 0 && got < p.c.num_pages) {
+                            page = got;
+                            *row = key - pj * p.c.page_size;
+                        } else {
+                            atomicOr(&g_paged_status, STATUS_CACHE);
+                        }
+                    }
+                    return page;
+                };
+                int k_row, v_row, k_row_n, v_row_n;
+                int k_page = lookup(w.t0, true, &k_row), v_page = lookup(w.t0, false, &v_row);
+                int k_page_n = lookup(w.t0 + 1, true, &k_row_n), v_page_n = v_page;
+                // items in the MMA warp's order: K(t0), K(t0+1), then V(j), K(j+2)
+                auto copy = [&](bool k, int j, int page, int row) {
+                    const int slot = static_cast<int>(item % C::NS);
+                    ok = ok && chunk_wait_warp(PPBAR(PPB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
+                    if (!ok) return;
+                    ++item;
+                    const uint32_t l_full = mapa_shared(PPBAR(PPB_FULL + slot), 0);
+                    const int valid = w.kv - j * PC_BN;      // rows of the tile that exist
+                    const int cut = !k && valid < PC_BN && valid % p.box_rows != 0 ? valid / p.box_rows : -1;   // the box to fill by hand
+                    if (cut >= 0) {
+                        const int pg = __shfl_sync(0xffffffffu, page, cut), r0 = __shfl_sync(0xffffffffu, row, cut);
+                        const int n = pg < p.c.num_pages ? valid - cut * p.box_rows : 0;
+                        const uint8_t* src = p.c.data[1] + w.h * p.c.sh[1] + rank * 256;
+                        if (n > 0) src += pg * p.c.sp[1] + r0 * p.c.st[1];
+                        for (int x = lane; x < p.box_rows * 16; x += 32) {
+                            const int rr = x >> 4, c = x & 15, r = cut * p.box_rows + rr;
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (rr < n) v = __ldg(reinterpret_cast<const uint4*>(src + rr * p.c.st[1]) + c);
+                            *reinterpret_cast<uint4*>(sKV + slot * C::SLOT + (c >> 3) * C::VBLK + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        if (leader) mbar_arrive_expect_tx(PPBAR(PPB_FULL + slot), 2 * (C::SLOT - (cut >= 0 ? p.box_rows * 256 : 0)));
+                        else if (cut >= 0) mbar_arrive_cluster_release(l_full);
+                        else mbar_arrive_remote(l_full);
+                    }
+                    __syncwarp();
+                    const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && leader && k && j == w.t0 && lane == 0;
+                    const uint32_t dst = sKV_addr + slot * C::SLOT + lane * p.box_rows * 128;
+                    if (k) {
+                        if (lane < k_boxes && !drop)
+#pragma unroll
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_4d_pair_hint(dst + c * C::KBLK, &tm_k, c * 64, row, w.h, page, l_full, pol_kv);
+                    } else if (lane < v_boxes && lane != cut) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tma_load_4d_pair_hint(dst + c * C::VBLK, &tm_v, rank * 128 + c * 64, row, w.h, page, l_full, pol_kv);
+                    }
+                    __syncwarp();
+                };
+                copy(true, w.t0, k_page, k_row);
+                if (w.t0 + 1 < je) copy(true, w.t0 + 1, k_page_n, k_row_n);
+                for (int j = w.t0; j < je && ok; ++j) {
+                    k_page = lookup(j + 2, true, &k_row);
+                    v_page_n = lookup(j + 1, false, &v_row_n);
+                    copy(false, j, v_page, v_row);
+                    if (j + 2 < je) copy(true, j + 2, k_page, k_row);
+                    v_page = v_page_n;
+                    v_row = v_row_n;
+                }
+            }
+        }
+        if (*abort_flag || !ok) {
+            // copies in flight must land before the memory is reused
+            const uint64_t d0 = global_timer_ns();
+            while (global_timer_ns() - d0 < 2000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (E4M3 && warp >= C::WARP_CONV) {
+        // ================================================================ converters (both CTAs): e4m3 K and V halves
+        if constexpr (E4M3) {
+            constexpr int X = 8;                 // 16-code chunks per thread and item
+            const int t = tid - 32 * C::WARP_CONV;
+            uint4 data[X];
+            uint32_t scale[X];
+            uint32_t item = 0;
+            bool ok = true;
+            // K: 64 rows of 16 chunks; V: 128 rows of this rank's 8 chunks
+            auto fetch = [&](int x, int j, bool k) {
+                const int r = k ? x * 8 + (t >> 4) : x * 16 + (t >> 3);
+                const int key = j * PC_BN + (k ? rank * C::KH : 0) + r;
+                const int which = k ? 0 : 1;
+                data[x] = make_uint4(0u, 0u, 0u, 0u);
+                scale[x] = 127u;
+                if (key < w.kv) {
+                    const int pj = page_index(p, key);
+                    const int row = key - pj * p.c.page_size;
+                    const int page = __ldg(p.table + w.b * p.table_stride + pj);
+                    if (page >= 0 && page < p.c.num_pages) {
+                        data[x] = __ldg(reinterpret_cast<const uint4*>(p.c.data[which] + page * p.c.sp[which] + w.h * p.c.sh[which] + row * p.c.st[which]) +
+                                        (k ? t & 15 : rank * 8 + (t & 7)));
+                        scale[x] = __ldg(p.c.scale[which] + (static_cast<long long>(page) * p.c.Hkv + w.h) * p.c.page_size + row);
+                    } else if (!k && leader && (t & 7) == 0) {
+                        atomicOr(&g_paged_status, STATUS_CACHE);
+                    }
+                }
+            };
+            for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+                const int je = max(w.end(0), w.end(1));
+                if (je <= w.t0) continue;
+                // items: K(t0), K(t0+1), then V(j), K(j+2); item s of the segment's 2 (je - t0)
+                const int n = 2 * (je - w.t0);
+                auto what = [&](int s, int* j) {     // whether item s is a K tile, and its key tile
+                    if (s < 2 && s < je - w.t0) {
+                        *j = w.t0 + s;
+                        return true;
+                    }
+                    if (je - w.t0 == 1) {
+                        *j = w.t0;
+                        return false;
+                    }
+                    const int e = s - 2;             // V(0) K(2) V(1) K(3) ... V(n-3) K(n-1) V(n-2) V(n-1)
+                    if (e >= n - 4) {
+                        *j = je - (n - s);
+                        return false;
+                    }
+                    *j = w.t0 + (e >> 1) + ((e & 1) ? 2 : 0);
+                    return (e & 1) != 0;
+                };
+                int j0;
+                bool k = what(0, &j0);
+#pragma unroll
+                for (int x = 0; x < X; ++x) fetch(x, j0, k);
+                for (int s = 0; s < n && ok; ++s) {
+                    const int slot = static_cast<int>(item % C::NS);
+                    ok = chunk_wait_warp(PPBAR(PPB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
+                    if (!ok) break;
+                    ++item;
+                    int jn = 0;
+                    const bool kn = s + 1 < n ? what(s + 1, &jn) : false;
+                    uint8_t* dst = sKV + slot * C::SLOT;
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        const uint32_t wd[4] = {data[x].x, data[x].y, data[x].z, data[x].w};
+                        const uint32_t code = scale[x];
+                        if (s + 1 < n) fetch(x, jn, kn);
+                        const uint32_t f = scale_factor(code) * 0x10001u;
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[2 * e] = widen2(__byte_perm(wd[e], 0u, 0x1404), f);
+                            o[2 * e + 1] = widen2(__byte_perm(wd[e], 0u, 0x3424), f);
+                        }
+                        if (code > 134u && code != SCALE_NAN) {   // a scale above 2^7: the rest of it
+                            const uint32_t f2 = (code - 7u) << 7;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f2 * 0x10001u);
+                        }
+                        const int r = k ? x * 8 + (t >> 4) : x * 16 + (t >> 3);
+                        const int c16 = k ? t & 15 : t & 7;
+                        const int blk = c16 >> 2, ch = (c16 & 3) * 2;
+                        uint8_t* line = dst + blk * (k ? C::KBLK : C::VBLK) + r * 128;
+                        const int sw = r & 7;
+                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                        const bool flip = blk & 1;
+                        *reinterpret_cast<uint4*>(line + (((ch + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? hi : lo;
+                        *reinterpret_cast<uint4*>(line + (((ch + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? lo : hi;
+                    }
+                    k = kn;
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                    __syncwarp();
+                    const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && item == 1 && leader && warp == C::WARP_CONV;
+                    if (lane == 0 && !drop) mbar_arrive_cluster_release(mapa_shared(PPBAR(PPB_FULL + slot), 0));
+                }
+            }
+        }
+    }
+
+    // Neither CTA may release its TMEM or leave while the pair's MMAs, commits or copies may
+    // still touch the other one.
+    tc_fence_before();
+    cluster_sync();
+    if (warp == C::WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+#undef PPBAR
+}

@@ -168,7 +168,7 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
     paged_rows_kernel(const PagedParams p, const int n_ctas) {
     using C = RowsCfg<D, E4M3>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ long long s_sum[PR_WARPS];
     __shared__ long long s_first;
     __shared__ int s_b;

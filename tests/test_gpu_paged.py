@@ -289,6 +289,22 @@ def test_a_whole_serving_step(kp):
     assert kp.device_status() == kp.ATTN_OK
 
 
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_dropped_copy_times_out_and_context_survives(kp, D, e4m3):
+    """A K tile that is announced and never delivered: the bounded waits end the kernel with its flag."""
+    c = make([500], [200], 4, 2, D, 16, e4m3, seed=D)
+    kp.set_wait_limit_ns(20_000_000)
+    kp.set_debug_flags(kp.ATTN_DEBUG_DROP_COPY)
+    try:
+        call(kp, c)
+        assert kp.device_status() == kp.ATTN_ERR_TIMEOUT
+    finally:
+        kp.set_debug_flags(0)
+        kp.set_wait_limit_ns(1_000_000_000)
+    check(kp, c)
+
+
 def test_refusals(kp):
     c = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
     q = torch.zeros(5, 4, 64, dtype=torch.bfloat16, device="cuda")
