@@ -256,7 +256,8 @@ attn_status attn_qk_norm_rope(const attn_rope_operand* q, const attn_rope_operan
  *     value); every code * 2^e is a bf16 number (at e = 120 magnitudes above 240 * 2^120 are
  *     stored as that, the largest one below infinity).  A row that holds a NaN or an infinity
  *     is stored as NaN (scale byte 255), and reads back as NaN.
- * page_size: a multiple of 8.  Strides: multiples of 16 bytes, t >= D.
+ * page_size: a multiple of 8.  Strides: multiples of 16 bytes, t >= D, h a multiple of
+ * min(D, 64) elements (any layout of whole rows has that).
  * num_pages * page_size <= 2^31 - 1; element offsets are 64-bit. */
 #define ATTN_CACHE_BF16 0
 #define ATTN_CACHE_E4M3 1

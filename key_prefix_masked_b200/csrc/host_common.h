@@ -91,23 +91,27 @@ inline attn_status check_device() {
     return c == 1 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
 }
 
+// A tensor map of up to five dims, innermost first (strides in bytes, of dims 1 and up).
+inline bool encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+    return enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A [B, H, T, D] bf16 tensor at element strides s (d contiguous) as a 4-D TMA map with
 // dims (D, T, H, B); a box is box_rows rows x box_cols columns of box_outer b's of one h.
 inline bool make_map(CUtensorMap* map, const void* base, int B, int H, int T, int D, const Strides& s, int box_cols,
                      int box_rows, CUtensorMapSwizzle swz, int box_outer = 1) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(H),
-                          static_cast<cuuint64_t>(B)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(s.t) * 2ull, static_cast<cuuint64_t>(s.h) * 2ull,
-                             static_cast<cuuint64_t>(s.b) * 2ull};
-    cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u,
-                         static_cast<cuuint32_t>(box_outer)};
-    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(H),
+                                static_cast<cuuint64_t>(B)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s.t) * 2ull, static_cast<cuuint64_t>(s.h) * 2ull,
+                                   static_cast<cuuint64_t>(s.b) * 2ull};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u,
+                               static_cast<cuuint32_t>(box_outer)};
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, swz);
 }
 
 }  // namespace attn

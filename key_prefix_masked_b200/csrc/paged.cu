@@ -57,6 +57,7 @@ struct PagedParams {
     int min_units;                      // least tiles that a CTA takes
     int page_shift;                     // log2(page_size), -1 if it is no power of two
     int tpt, box_rows;                  // paged_chunk.cuh: tokens per row tile, rows per copied box
+    int head_units[2];                  // and a head's distance in column blocks (k, v)
     unsigned debug;
     unsigned long long wait_ns;
     float scale_log2;
@@ -137,6 +138,8 @@ attn_status cache_view(const attn_cache* c, CacheView* v) {
     memset(v, 0, sizeof *v);
     for (int i = 0; i < 2; ++i) {
         if ((s[i].b * size) & 15 || (s[i].h * size) & 15 || (s[i].t * size) & 15) return ATTN_ERR_INVALID_ARG;
+        if (c->Hkv == 1) s[i].h = c->D;                                       // not used
+        if (s[i].h % (c->D < 64 ? c->D : 64) != 0) return ATTN_ERR_INVALID_ARG;
         v->data[i] = static_cast<uint8_t*>(i ? c->v : c->k);
         v->scale[i] = e4m3 ? (i ? c->v_scale : c->k_scale) : nullptr;
         v->sp[i] = s[i].b * size;
@@ -249,10 +252,26 @@ attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
     const CUtensorMapSwizzle swz = BLK == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, p.q, p.T, p.c.Hkv, p.G, D, {p.q_t, p.G * p.q_h, p.q_h}, BLK, p.G, swz, p.tpt)) return ATTN_ERR_CUDA;
-    mk = mv = mq;
-    if (!E4M3 && (!make_map(&mk, p.c.data[0], p.c.num_pages, p.c.Hkv, p.c.page_size, D, {p.c.sp[0] / 2, p.c.sh[0] / 2, p.c.st[0] / 2}, BLK, p.box_rows, swz) ||
-                  !make_map(&mv, p.c.data[1], p.c.num_pages, p.c.Hkv, p.c.page_size, D, {p.c.sp[1] / 2, p.c.sh[1] / 2, p.c.st[1] / 2}, BLK, p.box_rows, swz)))
-        return ATTN_ERR_CUDA;
+    // K, V.  e4m3: rows of D codes (half of V's at head dim 256), as they lie.  bf16: a page as
+    // [8-row group][head and column block][8 rows][block], so that one box takes whole rows
+    // into shared memory group by group; heads are counted in column blocks.
+    for (int i = 0; i < 2; ++i) {
+        const CacheView& c = p.c;
+        CUtensorMap* m = i ? &mv : &mk;
+        p.head_units[i] = static_cast<int>(c.sh[i] / (2 * BLK));
+        const cuuint64_t u = static_cast<cuuint64_t>(c.Hkv - 1) * p.head_units[i] + D / BLK;
+        const cuuint64_t sp = c.sp[i], sh = c.sh[i], st = c.st[i], P = c.num_pages, page = c.page_size;
+        const cuuint32_t rows = p.box_rows, part = PAIR && i ? 2u : 1u;   // a V box of a pair: half the columns
+        if (E4M3) {
+            const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), page, static_cast<cuuint64_t>(c.Hkv), P}, str[3] = {st, sh, sp};
+            const cuuint32_t box[4] = {D / part, rows, 1u, 1u};
+            if (!encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.data[i], dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE)) return ATTN_ERR_CUDA;
+        } else {
+            const cuuint64_t dims[5] = {static_cast<cuuint64_t>(BLK), 8, u, page / 8, P}, str[4] = {st, 2 * BLK, 8 * st, sp};
+            const cuuint32_t box[5] = {static_cast<cuuint32_t>(BLK), 8u, static_cast<cuuint32_t>(D / BLK) / part, rows / 8, 1u};
+            if (!encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, c.data[i], dims, str, box, swz)) return ATTN_ERR_CUDA;
+        }
+    }
     int grid, threads, smem;
     void (*kern)(CUtensorMap, CUtensorMap, CUtensorMap, PagedParams, int);
     if constexpr (PAIR) {

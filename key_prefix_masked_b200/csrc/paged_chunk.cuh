@@ -7,22 +7,29 @@
 // 128-key tiles of K and V: while one tile's scores are in its softmax warps, the tensor
 // pipe runs the other tile's MMAs, and each K/V byte brought to shared memory serves 256 rows.
 //
-// TMEM: S_0, S_1 (128 columns each, P_g stored over S_g), O_0, O_1.  MMA order per key
-// tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1).  One thread's MMAs run in issue order, so
-// "S_g(j) ready" also means PV_g(j-1) is complete and the group may rescale O_g.
+// TMEM: S_0, S_1 (128 columns each), O_0, O_1.  MMA order per key tile j at D = 128: PV_0(j),
+// S_0(j+1), PV_1(j), S_1(j+1), P_g stored over S_g; one thread's MMAs run in issue order, so "S_g(j)
+// ready" also means PV_g(j-1) is complete and the group may rescale O_g.  At D <= 64 P_0 and P_1 have
+// columns of their own and the order is S_0(j+1), S_1(j+1), PV_0(j), PV_1(j); every PV is
+// announced on a barrier, which a group waits for before it writes P_g (or O_g) again.
 //
 // The work, (sequence, key head, token tile, key tile), is laid end to end and dealt to
 // one persistent CTA per SM in equal contiguous runs, like the few-row kernel's: ragged
 // batches and causal triangles leave no SM idle at the end, and only a run's first and last
 // token tile can be shared with another CTA; paged_chunk_combine_kernel puts those together.
 //
-// K and V: bf16 pages are copied by TMA, in boxes of the largest power of two of rows (up
-// to 128) that divides the page size, each box from its page; a box behind the
-// sequence or of a page that does not exist has its page coordinate outside the pool and reads as
-// zeros.  The rows of the last box behind the sequence are cleared in shared memory before
-// PV reads them.  e4m3 pages go through four converter warps: 16 codes a load, widened to
-// bf16 in registers (exactly, see paged_rows.cuh) and stored in the layout TMA would have
-// written, with the next tile's loads in flight meanwhile.
+// K and V are copied by TMA, in boxes of the largest power of two of rows (up to 128) that divides
+// the page size, each box from its page; a box behind the sequence or of a page that does
+// not exist has its page coordinate outside the pool and reads as zeros.  Small pages make
+// many boxes, and what one warp can issue bounds them, so a bf16 box holds all columns of its
+// rows: the tensor map splits a page into groups of 8 rows, and a tile lies in shared memory
+// as [8-row group][64-column block][8 rows][128 bytes], which the MMA descriptors address by
+// their two strides.  The rows of the last box behind the sequence are cleared in shared
+// memory before PV reads them.  e4m3 tiles land in staging slots instead, with their
+// scale bytes by cp.async; four converter warps widen them to bf16 (exactly, see paged_rows.cuh) into
+// the same layout.  (Loading the codes straight into the converters' registers, one tile
+// ahead, left them waiting for loads: 476 against 1061 TFLOP/s with the loads taken out, 2048 rows
+// on 32768 keys, 32 heads on 8, D 128.)
 //
 // Every wait is bounded; on expiry the CTA raises the timeout flag, drains and exits.
 
@@ -37,12 +44,22 @@ struct ChunkCfg {
     static constexpr int QT_BYTES = 128 * D * 2;        // one 128-row tile
     static constexpr int SLOT = PC_BN * D * 2;          // a K or V tile
     static constexpr int CTRL = 1024;
-    static constexpr int NS_FIT = (232448 - 1024 - CTRL - 2 * QT_BYTES) / SLOT;
+    static constexpr int GROUP = NBLK * 8 * SW;         // one 8-row group of a K or V tile
+    // e4m3: staged codes of a tile, and its 128 scale bytes
+    static constexpr int STG_BYTES = PC_BN * D + 128;
+    static constexpr int NSTG = E4M3 ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int NS_FIT = (232448 - 1024 - CTRL - 2 * QT_BYTES - NSTG * STG_BYTES) / SLOT;
     static constexpr int NS = NS_FIT < 12 ? NS_FIT : 12;
-    static constexpr int SMEM = 1024 + 2 * QT_BYTES + NS * SLOT + CTRL;
+    static constexpr int SMEM = 1024 + 2 * QT_BYTES + NS * SLOT + NSTG * STG_BYTES + CTRL;
+    static_assert(NS >= 3, "ring depth");
     static constexpr uint32_t LAYOUT = SW == 128 ? 2u : 4u;
     static constexpr uint32_t O_COL = 256;
-    // warps 0-7 softmax; bf16: 8 copies, 9 MMA; e4m3: 8-11 converters, 12 MMA, 13 Q copies
+    // Head dims up to 64 leave TMEM for a P buffer per group beside the scores, so S_g(j+1) is
+    // issued as soon as S_g(j) has been read out; at 128 P_g is stored over S_g, S_g(j+1) waits for
+    // PV_g(j), and P_g is announced in two halves, so that PV_g starts under the second.
+    static constexpr bool AHEAD = D <= 64;
+    static constexpr uint32_t P_COL = AHEAD ? O_COL + 128 : 0, P_STEP = AHEAD ? 64 : PC_BN;
+    // warps 0-7 softmax; bf16: 8 copies, 9 MMA; e4m3: 8-11 converters, 12 MMA, 13 copies
     static constexpr int WARP_MMA = E4M3 ? 12 : 9;
     static constexpr int WARP_COPY = E4M3 ? 13 : 8;
     static constexpr int THREADS = E4M3 ? 512 : 320;
@@ -53,17 +70,20 @@ struct ChunkCfg {
 };
 
 enum : int {
-    PCB_QFULL = 0, PCB_QEMPTY = 1, PCB_S = 2 /* [2] */, PCB_P = 4 /* [2] */, PCB_O = 6 /* [2] */, PCB_DRAIN = 8,
-    PCB_FULL = 9 /* [12] */, PCB_EMPTY = 21 /* [12] */, PCB_NUM = 33
+    PCB_QFULL = 0, PCB_QEMPTY = 1, PCB_S = 2 /* [2] */, PCB_P = 4 /* [2], then the second halves' */, PCB_O = 8 /* [2] */,
+    PCB_READ = 10 /* [2] S_g read out */, PCB_DRAIN = 12,
+    PCB_FULL = 13 /* [12] */, PCB_EMPTY = 25 /* [12] */, PCB_SFULL = 37 /* [8] */, PCB_SEMPTY = 45 /* [8] */, PCB_NUM = 53
 };
 
-template <bool CLUSTER = false>   // acquire at cluster scope
-__device__ __noinline__ bool chunk_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
-    auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (done()) return true;
+template <bool CLUSTER>   // acquire at cluster scope
+__device__ __forceinline__ bool chunk_poll(uint32_t bar, uint32_t parity) {
+    return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+}
+template <bool CLUSTER>
+__device__ __noinline__ bool chunk_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
     const uint64_t t0 = global_timer_ns();
     while (true) {
-        if (done()) return true;
+        if (chunk_poll<CLUSTER>(bar, parity)) return true;
         if (*abort_flag) return false;
         if (global_timer_ns() - t0 > limit_ns) {
             *abort_flag = 1;
@@ -72,10 +92,11 @@ __device__ __noinline__ bool chunk_wait(uint32_t bar, uint32_t parity, volatile 
         }
     }
 }
-// The same for a whole warp that stays converged: lane 0's answer.
+// Waits of a whole warp, which stays converged: true once every lane has seen the phase complete.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool chunk_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
-    return __shfl_sync(0xffffffffu, chunk_wait<CLUSTER>(bar, parity, abort_flag, limit_ns) ? 1 : 0, 0) != 0;
+    if (__all_sync(0xffffffffu, chunk_poll<CLUSTER>(bar, parity))) return true;
+    return __all_sync(0xffffffffu, chunk_wait_slow<CLUSTER>(bar, parity, abort_flag, limit_ns)) != 0;
 }
 
 // Keys that query row i of a sequence with n rows and kv keys sees.
@@ -221,6 +242,46 @@ __device__ __forceinline__ long long chunk_deal(const PagedParams& p, int n_ctas
     return per;
 }
 
+// Sixteen codes of a row as bf16 values, to two 16-byte chunks (ch, ch + 1 before the swizzle)
+// of the row's 128-byte line; lanes with `flip` store the second first, so that a quarter
+// warp touches all banks.
+__device__ __forceinline__ void store_codes(const uint4& d, uint32_t code, uint8_t* line, int ch, int sw, bool flip) {
+    const uint32_t f = scale_factor(code) * 0x10001u;
+    const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        o[2 * e] = widen2(__byte_perm(wd[e], 0u, 0x1404), f);
+        o[2 * e + 1] = widen2(__byte_perm(wd[e], 0u, 0x3424), f);
+    }
+    if (code > 134u && code != SCALE_NAN) {   // a scale above 2^7: the rest of it
+        const uint32_t f2 = ((code - 7u) << 7) * 0x10001u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f2);
+    }
+    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(line + (((ch + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? hi : lo;
+    *reinterpret_cast<uint4*>(line + (((ch + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? lo : hi;
+}
+// Page and first row of the keys from `key` on; none: num_pages (outside the pool).
+struct PageAt {
+    int page, row;
+};
+__device__ __forceinline__ PageAt page_at(const PagedParams& p, const int32_t* table, int key, bool wanted, bool report) {
+    PageAt a = {p.c.num_pages, 0};
+    if (wanted) {
+        const int pj = page_index(p, key);
+        const int got = __ldg(table + pj);
+        if (got >= 0 && got < p.c.num_pages) {
+            a.page = got;
+            a.row = key - pj * p.c.page_size;
+        } else if (report) {
+            atomicOr(&g_paged_status, STATUS_CACHE);
+        }
+    }
+    return a;
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -229,7 +290,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sKV = smem + 2 * C::QT_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + C::NS * C::SLOT);
+    uint8_t* sStg = sKV + C::NS * C::SLOT;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sStg + C::NSTG * C::STG_BYTES);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + PCB_NUM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     long long* s_scr = reinterpret_cast<long long*>(tmem_holder + 2);   // 18 words of 8 bytes
@@ -251,11 +313,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         for (int g = 0; g < 2; ++g) {
             mbar_init(CBAR(PCB_S + g), 1);
             mbar_init(CBAR(PCB_P + g), 4);
+            mbar_init(CBAR(PCB_P + 2 + g), 4);
+            mbar_init(CBAR(PCB_READ + g), 4);
             mbar_init(CBAR(PCB_O + g), 1);
         }
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(CBAR(PCB_FULL + s), E4M3 ? 4 : 1);
             mbar_init(CBAR(PCB_EMPTY + s), 1);
+        }
+        for (int s = 0; s < C::NSTG; ++s) {
+            mbar_init(CBAR(PCB_SFULL + s), 33);    // the byte count's, and every copying lane's scale bytes
+            mbar_init(CBAR(PCB_SEMPTY + s), 4);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -276,12 +344,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + static_cast<uint32_t>(g) * PC_BN;
         const uint32_t o_addr = tmem + lane_base + C::O_COL + static_cast<uint32_t>(g) * D;
+        const uint32_t p_addr = tmem + lane_base + C::P_COL + static_cast<uint32_t>(g) * C::P_STEP;
         const float sl2 = p.scale_log2;
         const bool pos_scale = sl2 > 0.0f;
         const float mul = pos_scale ? sl2 : 1.0f;
         const int r_tok = r / p.G, r_head = r - r_tok * p.G;
-        uint32_t s_phase = 0, o_phase = 0;
+        uint32_t cnt = 0, o_phase = 0;   // tiles of this group, over all segments
         bool ok = true;
+        auto arrive = [&](uint32_t bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
         for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
             const bool live = r_tok < w.c.ntok(g) && r_tok < p.tpt;
             const int i = w.c.tok(g) + r_tok;
@@ -291,9 +365,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             const int j1 = w.end(g);
 #pragma unroll 1
             for (int j = w.t0; j < j1; ++j) {
-                ok = __all_sync(0xffffffffu, chunk_wait(CBAR(PCB_S + g), s_phase, abort_flag, wlim));
+                ok = chunk_wait_warp(CBAR(PCB_S + g), cnt & 1u, abort_flag, wlim);
                 if (!ok) break;
-                s_phase ^= 1u;
                 tc_fence_after();
                 float x[C::COLS];
                 // columns [c0, c0 + COLS) of the row, masked by selection
@@ -320,37 +393,20 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     mx = fmaxf(mx, row_max(x));
                 }
                 mx *= mul;
+                if constexpr (C::AHEAD) {
+                    if constexpr (C::COLS == PC_BN) arrive(CBAR(PCB_READ + g));
+                    // PV of the tile before has read P_g and added to O_g
+                    ok = cnt == 0 || chunk_wait_warp(CBAR(PCB_O + g), (cnt - 1) & 1u, abort_flag, wlim);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 float factor = 1.0f;
-                bool rescale = false;
                 if (j == w.t0) {
                     m_ref = mx;
                 } else if (__any_sync(0xffffffffu, mx > m_ref + PC_RESCALE_LOG2)) {
                     const float m_new = fmaxf(m_ref, mx);
                     factor = m_ref == -INFINITY ? 0.0f : exp2_approx(m_ref - m_new);
                     m_ref = m_new;
-                    rescale = true;
-                }
-                const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;   // a row with no key so far: 2^-inf, not NaN
-                float2 sp[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) sp[t] = make_float2(0.0f, 0.0f);
-                const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(neg_m, neg_m);
-#pragma unroll
-                for (int cc = 0; cc < PC_BN / 32; ++cc) {
-                    constexpr int PER = C::COLS / 32;
-                    if (cc != 0 && cc % PER == 0) load(cc * 32);
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 y = fma2(make_float2(x[cc % PER * 32 + 2 * e], x[cc % PER * 32 + 2 * e + 1]), mul2, neg2);
-                        const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
-                        sp[e & 3] = add2(sp[e & 3], make_float2(p0, p1));   // the sum takes the weights unrounded
-                        pk[e] = pack_bf16(p0, p1);
-                    }
-                    tmem_st16(s_addr + cc * 16, pk);
-                }
-                l_sum = l_sum * factor + (((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y)));
-                if (rescale) {
 #pragma unroll 1
                     for (int oc = 0; oc < D / 32; ++oc) {
                         uint32_t o[32];
@@ -360,15 +416,42 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                         tmem_st32(o_addr + oc * 32, o);
                     }
                 }
+                const float neg_m = m_ref == -INFINITY ? 0.0f : -m_ref;   // a row with no key so far: 2^-inf, not NaN
+                float2 sp[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) sp[t] = make_float2(0.0f, 0.0f);
+                const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(neg_m, neg_m);
+#pragma unroll
+                for (int cc = 0; cc < PC_BN / 32; ++cc) {
+                    constexpr int PER = C::COLS / 32;
+                    if (cc != 0 && cc % PER == 0) {
+                        load(cc * 32);
+                        if constexpr (C::AHEAD) arrive(CBAR(PCB_READ + g));
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = fma2(make_float2(x[cc % PER * 32 + 2 * e], x[cc % PER * 32 + 2 * e + 1]), mul2, neg2);
+                        const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+                        sp[e & 3] = add2(sp[e & 3], make_float2(p0, p1));   // the sum takes the weights unrounded
+                        pk[e] = pack_bf16(p0, p1);
+                    }
+                    tmem_st16(p_addr + cc * 16, pk);
+                    if (!C::AHEAD && cc == 1) {                             // the first 64 keys' weights
+                        tmem_wait_st();
+                        arrive(CBAR(PCB_P + g));
+                    }
+                }
                 tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(CBAR(PCB_P + g));
+                arrive(CBAR(PCB_P + (C::AHEAD ? 0 : 2) + g));
+                l_sum = l_sum * factor + (((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y)));
+                ++cnt;
             }
             if (!ok) break;
             const bool has = j1 > w.t0;
             if (has) {
-                ok = __all_sync(0xffffffffu, chunk_wait(CBAR(PCB_O + g), o_phase, abort_flag, wlim));
+                // D <= 64: one phase per PV; 128: one per segment
+                ok = chunk_wait_warp(CBAR(PCB_O + g), C::AHEAD ? (cnt - 1) & 1u : o_phase, abort_flag, wlim);
                 if (!ok) break;
                 o_phase ^= 1u;
                 tc_fence_after();
@@ -421,11 +504,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         constexpr uint32_t IDESC_S = make_idesc_bf16(128, PC_BN, false);
         constexpr uint32_t IDESC_PV = make_idesc_bf16(128, D, true);
         const uint64_t q_desc0 = make_smem_desc(sQ_addr, 16, 8 * C::SW, C::LAYOUT);
-        const uint64_t k_desc0 = make_smem_desc(sKV_addr, 16, 8 * C::SW, C::LAYOUT);
-        const uint64_t v_desc0 = make_smem_desc(sKV_addr, PC_BN * C::SW, 8 * C::SW, C::LAYOUT);
+        const uint64_t k_desc0 = make_smem_desc(sKV_addr, 16, C::GROUP, C::LAYOUT);
+        const uint64_t v_desc0 = make_smem_desc(sKV_addr, 8 * C::SW, C::GROUP, C::LAYOUT);
         int k_slot = 0, v_slot = 0;
         uint32_t item = 0;                       // ring items consumed: K_t0, then V_j, K_{j+1}
-        uint32_t p_phase[2] = {0, 0}, q_phase = 0;
+        uint32_t p_phase[2] = {0, 0}, r_phase[2] = {0, 0}, q_phase = 0;
         bool ok = true;
         auto next_item = [&]() -> int {          // waits for the next K or V tile; its slot
             const int slot = static_cast<int>(item % C::NS);
@@ -437,20 +520,23 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         auto issue_s = [&](int g) {
             const uint64_t kd = k_desc0 + static_cast<uint64_t>(k_slot) * (C::SLOT >> 4);
             const uint64_t qd = q_desc0 + static_cast<uint64_t>(g) * (C::QT_BYTES >> 4);
+            const uint32_t d = tmem + static_cast<uint32_t>(g) * PC_BN;
+            if constexpr (C::BLK == 64) {
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) {
-                const int c = t / (C::BLK / 16), kk = t % (C::BLK / 16);
-                const uint64_t off = static_cast<uint64_t>(((c * 128 * C::SW) >> 4) + kk * 2);
-                mma_ss_elect(tmem + static_cast<uint32_t>(g) * PC_BN, qd + off, kd + off, IDESC_S, t != 0 ? 1u : 0u);
+                for (int c = 0; c < C::NBLK; ++c)
+                    mma_ss_elect_x4<2, 2>(d, qd + static_cast<uint64_t>((c * 128 * C::SW) >> 4), kd + static_cast<uint64_t>((c * 8 * C::SW) >> 4), IDESC_S, c != 0 ? 1u : 0u);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) mma_ss_elect(d, qd + 2 * t, kd + 2 * t, IDESC_S, t != 0 ? 1u : 0u);
             }
             tc_commit_elect(CBAR(PCB_S + g));
         };
-        auto issue_pv = [&](int g, bool first) {
+        auto issue_pv = [&](int g, bool first, int kb0, int kb1) {   // 16-key steps [kb0, kb1)
             const uint64_t vd = v_desc0 + static_cast<uint64_t>(v_slot) * (C::SLOT >> 4);
 #pragma unroll
-            for (int kb = 0; kb < PC_BN / 16; ++kb)
-                mma_ts_elect(tmem + C::O_COL + static_cast<uint32_t>(g) * D, tmem + static_cast<uint32_t>(g) * PC_BN + kb * 8u,
-                             vd + static_cast<uint64_t>((kb * 16 * C::SW) >> 4), IDESC_PV, kb == 0 && first ? 0u : 1u);
+            for (int kb = kb0; kb < kb1; kb += 4)
+                mma_ts_elect_x4<8, (2 * C::GROUP) / 16>(tmem + C::O_COL + static_cast<uint32_t>(g) * D, tmem + C::P_COL + static_cast<uint32_t>(g) * C::P_STEP + kb * 8u,
+                                                        vd + static_cast<uint64_t>((kb * 2 * C::GROUP) >> 4), IDESC_PV, kb == 0 && first ? 0u : 1u);
         };
         for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
             const int e0 = w.end(0), e1 = w.end(1), je = max(e0, e1);
@@ -477,7 +563,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                         constexpr int CH = C::SW / 16;
                         for (int x = lane; x < (dirty - valid) * CH * C::NBLK; x += 32) {
                             const int blk = x / ((dirty - valid) * CH), y = x % ((dirty - valid) * CH);
-                            *reinterpret_cast<uint4*>(sKV + v_slot * C::SLOT + blk * (PC_BN * C::SW) + (valid + y / CH) * C::SW + y % CH * 16) =
+                            const int r = valid + y / CH;
+                            *reinterpret_cast<uint4*>(sKV + v_slot * C::SLOT + (r >> 3) * C::GROUP + blk * (8 * C::SW) + (r & 7) * C::SW + y % CH * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
                         }
                         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -485,27 +572,46 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     }
                 }
                 const bool more = j + 1 < je;
+                if (more) k_slot = next_item();      // ahead of the waits for P
+                if (!ok) break;
+                auto arrived = [&](int bar, uint32_t phase) {
+                    ok = ok && chunk_wait_warp(CBAR(bar), phase, abort_flag, wlim);
+                    tc_fence_after();
+                    return ok;
+                };
+                if constexpr (C::AHEAD) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (j >= (g ? e1 : e0) || !arrived(PCB_READ + g, r_phase[g])) continue;
+                        r_phase[g] ^= 1u;
+                        if (j + 1 < (g ? e1 : e0)) issue_s(g);
+                    }
+                    if (!ok) break;
+                    if (more) tc_commit_elect(CBAR(PCB_EMPTY + k_slot));
+                    if (j + 2 == je) tc_commit_elect(CBAR(PCB_QEMPTY));
+                }
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const int eg = g ? e1 : e0;
                     if (j < eg) {
-                        ok = chunk_wait_warp(CBAR(PCB_P + g), p_phase[g], abort_flag, wlim);
-                        if (!ok) break;
+                        if (!arrived(PCB_P + g, p_phase[g])) break;
+                        if constexpr (C::AHEAD) {
+                            issue_pv(g, j == w.t0, 0, PC_BN / 16);
+                            tc_commit_elect(CBAR(PCB_O + g));
+                        } else {
+                            issue_pv(g, j == w.t0, 0, PC_BN / 32);
+                            if (!arrived(PCB_P + 2 + g, p_phase[g])) break;
+                            issue_pv(g, false, PC_BN / 32, PC_BN / 16);
+                            if (j + 1 == eg) tc_commit_elect(CBAR(PCB_O + g));
+                        }
                         p_phase[g] ^= 1u;
-                        tc_fence_after();
-                        issue_pv(g, j == w.t0);
-                        if (j + 1 == eg) tc_commit_elect(CBAR(PCB_O + g));
                     }
-                    if (g == 0 && more) {
-                        k_slot = next_item();
-                        if (!ok) break;
-                    }
-                    if (j + 1 < eg) issue_s(g);
+                    if (!C::AHEAD && j + 1 < eg) issue_s(g);
                 }
                 if (!ok) break;
                 tc_commit_elect(CBAR(PCB_EMPTY + v_slot));
-                if (more) tc_commit_elect(CBAR(PCB_EMPTY + k_slot));
-                if (j + 2 == je) tc_commit_elect(CBAR(PCB_QEMPTY));
+                if (!C::AHEAD && more) tc_commit_elect(CBAR(PCB_EMPTY + k_slot));
+                if (!C::AHEAD && j + 2 == je) tc_commit_elect(CBAR(PCB_QEMPTY));
             }
         }
         // every MMA issued completes before TMEM is released
@@ -520,17 +626,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         }
         __syncwarp();
     } else if (warp == C::WARP_COPY) {
-        // ================================================================ copies: Q, and bf16 K and V
+        // ================================================================ copies: Q, K, V
         if (lane == 0) {
             tma_prefetch_map(&tm_q);
-            if constexpr (!E4M3) {
-                tma_prefetch_map(&tm_k);
-                tma_prefetch_map(&tm_v);
-            }
+            tma_prefetch_map(&tm_k);
+            tma_prefetch_map(&tm_v);
         }
         uint32_t item = 0, qe_phase = 0;
         bool ok = true, first = true;
         const int boxes = PC_BN / p.box_rows;
+        constexpr int N = E4M3 ? C::NSTG : C::NS;          // the slots that are filled here
+        constexpr int FULL = E4M3 ? PCB_SFULL : PCB_FULL, EMPTY = E4M3 ? PCB_SEMPTY : PCB_EMPTY;
         for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
             const int je = max(w.end(0), w.end(1));
             if (je <= w.t0) continue;
@@ -548,49 +654,48 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     for (int c = 0; c < C::NBLK; ++c)
                         tma_load_4d(sQ_addr + g * C::QT_BYTES + c * 128 * C::SW, &tm_q, c * C::BLK, 0, w.h, w.q0 + w.c.tok(g), CBAR(PCB_QFULL));
             }
-            if constexpr (!E4M3) {
-                // lane i < boxes copies box i of every tile; its page is looked up one tile ahead
-                const int32_t* table = p.table + w.b * p.table_stride;
-                auto lookup = [&](int j, int* row) {
-                    const int key = j * PC_BN + lane * p.box_rows;
-                    int page = p.c.num_pages;            // outside the pool: zeros
-                    *row = 0;
-                    if (lane < boxes && j < je && key < w.kv) {
-                        const int pj = page_index(p, key);
-                        const int got = __ldg(table + pj);
-                        if (got >= 0 && got < p.c.num_pages) {
-                            page = got;
-                            *row = key - pj * p.c.page_size;
-                        } else {
-                            atomicOr(&g_paged_status, STATUS_CACHE);
-                        }
-                    }
-                    return page;
-                };
-                int row = 0, row_n = 0;
-                int page = lookup(w.t0, &row);
-                for (int j = w.t0; j < je && ok; ++j) {
-                    const int page_n = lookup(j + 1, &row_n);
+            // lane i < boxes copies box i of a tile (all lanes at once: one lane issuing them in
+            // turn took 20 % longer with 16-row pages); its page is looked up one tile ahead
+            const int32_t* table = p.table + w.b * p.table_stride;
+            auto lookup = [&](int j) {
+                const int key = j * PC_BN + lane * p.box_rows;
+                return page_at(p, table, key, lane < boxes && j < je && key < w.kv, true);
+            };
+            auto lookup_scale = [&](int j) {               // e4m3: lane's group of 8 rows
+                const int key = j * PC_BN + (lane & 15) * 8;
+                return page_at(p, table, key, E4M3 && j < je && key < w.kv, false);
+            };
+            PageAt a = lookup(w.t0), sa = lookup_scale(w.t0);
+            for (int j = w.t0; j < je && ok; ++j) {
+                const PageAt an = lookup(j + 1), san = lookup_scale(j + 1);
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const int slot = static_cast<int>(item % C::NS);
-                        ok = chunk_wait_warp(CBAR(PCB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
-                        if (!ok) break;
-                        ++item;
-                        if (lane == 0) mbar_arrive_expect_tx(CBAR(PCB_FULL + slot), C::SLOT);
-                        __syncwarp();
-                        const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && kv == 0 && j == w.t0 && lane == 0;
-                        if (lane < boxes && !drop) {
-                            const uint32_t dst = sKV_addr + slot * C::SLOT + lane * p.box_rows * C::SW;
-#pragma unroll
-                            for (int c = 0; c < C::NBLK; ++c)
-                                tma_load_4d(dst + c * (PC_BN * C::SW), kv ? &tm_v : &tm_k, c * C::BLK, row, w.h, page, CBAR(PCB_FULL + slot));
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int slot = static_cast<int>(item % N);
+                    ok = chunk_wait_warp(CBAR(EMPTY + slot), ((item / N) & 1u) ^ 1u, abort_flag, wlim);
+                    if (!ok) break;
+                    ++item;
+                    if (lane == 0) mbar_arrive_expect_tx(CBAR(FULL + slot), E4M3 ? PC_BN * D : C::SLOT);
+                    __syncwarp();
+                    const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && kv == 0 && j == w.t0 && lane == 0;
+                    if constexpr (E4M3) {
+                        const uint32_t dst = smem_u32(sStg) + slot * C::STG_BYTES;
+                        if (lane < boxes && !drop) tma_load_4d(dst + lane * p.box_rows * D, kv ? &tm_v : &tm_k, 0, a.row, w.h, a.page, CBAR(FULL + slot));
+                        if (lane < 16) {
+                            const bool have = sa.page < p.c.num_pages;
+                            const uint8_t* src = p.c.scale[kv];
+                            if (have) src += (static_cast<long long>(sa.page) * p.c.Hkv + w.h) * p.c.page_size + sa.row;
+                            cp_async8(dst + PC_BN * D + lane * 8, src, have);
                         }
-                        __syncwarp();
+                        cp_async_mbar_arrive_noinc(CBAR(FULL + slot));
+                    } else {
+                        if (lane < boxes && !drop)
+                            tma_load_5d(sKV_addr + slot * C::SLOT + lane * (p.box_rows / 8) * C::GROUP, kv ? &tm_v : &tm_k, 0, 0, w.h * p.head_units[kv],
+                                        a.row / 8, a.page, CBAR(FULL + slot));
                     }
-                    page = page_n;
-                    row = row_n;
+                    __syncwarp();
                 }
+                a = an;
+                sa = san;
             }
         }
         if (*abort_flag || !ok) {
@@ -608,72 +713,37 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             constexpr int RPX = 128 / CPR;       // rows between a thread's chunks
             const int t = tid - 256;
             const int r0 = t / CPR, c16 = t % CPR;
-            uint4 data[X];
-            uint32_t scale[X];
-            // the item (key tile j of segment w; K or V) whose loads are in flight
+            const int blk = c16 * 16 / C::BLK, ch = c16 * 16 % C::BLK / 8;
             uint32_t item = 0;
             bool ok = true;
-            auto fetch = [&](int x, int j, int which) {
-                const int key = j * PC_BN + x * RPX + r0;
-                data[x] = make_uint4(0u, 0u, 0u, 0u);
-                scale[x] = 127u;
-                if (key < w.kv) {
-                    const int pj = page_index(p, key);
-                    const int row = key - pj * p.c.page_size;
-                    const int page = __ldg(p.table + w.b * p.table_stride + pj);
-                    if (page >= 0 && page < p.c.num_pages) {
-                        data[x] = __ldg(reinterpret_cast<const uint4*>(p.c.data[which] + page * p.c.sp[which] + w.h * p.c.sh[which] + row * p.c.st[which]) + c16);
-                        scale[x] = __ldg(p.c.scale[which] + (static_cast<long long>(page) * p.c.Hkv + w.h) * p.c.page_size + row);
-                    } else if (which == 0 && c16 == 0) {
-                        atomicOr(&g_paged_status, STATUS_CACHE);
-                    }
-                }
-            };
             for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
                 const int je = max(w.end(0), w.end(1));
-                if (je <= w.t0) continue;
-#pragma unroll
-                for (int x = 0; x < X; ++x) fetch(x, w.t0, 0);
                 for (int j2 = 2 * w.t0; j2 < 2 * je && ok; ++j2) {   // item: tile j2 / 2, K or V
-                    const int slot = static_cast<int>(item % C::NS);
-                    ok = chunk_wait_warp(CBAR(PCB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
+                    const int slot = static_cast<int>(item % C::NS), stg = static_cast<int>(item % C::NSTG);
+                    ok = chunk_wait_warp(CBAR(PCB_SFULL + stg), (item / C::NSTG) & 1u, abort_flag, wlim) &&
+                         chunk_wait_warp(CBAR(PCB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
                     if (!ok) break;
                     ++item;
-                    const int nj = (j2 + 1) >> 1, nw = (j2 + 1) & 1;
-                    uint8_t* dst = sKV + slot * C::SLOT;
+                    const int left = w.kv - (j2 >> 1) * PC_BN;       // rows of the tile that exist
+                    const uint8_t* src = sStg + stg * C::STG_BYTES;
+                    uint8_t* dst = sKV + slot * C::SLOT + blk * (8 * C::SW);
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
-                        const uint4 d = data[x];
-                        const uint32_t code = scale[x];
-                        if (j2 + 1 < 2 * je) fetch(x, nj, nw);
-                        const uint32_t f = scale_factor(code) * 0x10001u;
-                        uint32_t o[8];
-                        const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[2 * e] = widen2(__byte_perm(wd[e], 0u, 0x1404), f);
-                            o[2 * e + 1] = widen2(__byte_perm(wd[e], 0u, 0x3424), f);
-                        }
-                        if (code > 134u && code != SCALE_NAN) {   // a scale above 2^7: the rest of it
-                            const uint32_t f2 = (code - 7u) << 7;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f2 * 0x10001u);
-                        }
                         const int r = x * RPX + r0;
-                        const int col = c16 * 16;
-                        const int blk = col / C::BLK, ch = (col % C::BLK) / 8;   // 16-byte chunks ch, ch + 1 of the block's row
-                        uint8_t* line = dst + blk * (PC_BN * C::SW) + r * C::SW;
-                        const int sw = C::SW == 128 ? r & 7 : (r >> 1) & 3;
-                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                        // lanes of the second column block store their second half first: all banks at once
-                        const bool flip = blk & 1;
-                        *reinterpret_cast<uint4*>(line + (((ch + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? hi : lo;
-                        *reinterpret_cast<uint4*>(line + (((ch + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? lo : hi;
+                        uint4 d = *reinterpret_cast<const uint4*>(src + r * D + c16 * 16);
+                        uint32_t code = src[PC_BN * D + r];
+                        if (r >= left) {                             // a page's rows behind the sequence
+                            d = make_uint4(0u, 0u, 0u, 0u);
+                            code = 127u;
+                        }
+                        store_codes(d, code, dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();
-                    const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && item == 1 && warp == 8;
-                    if (lane == 0 && !drop) mbar_arrive(CBAR(PCB_FULL + slot));
+                    if (lane == 0) {
+                        mbar_arrive(CBAR(PCB_FULL + slot));
+                        mbar_arrive(CBAR(PCB_SEMPTY + stg));
+                    }
                 }
             }
         }

@@ -20,20 +20,23 @@ struct PagedPairCfg {
     static constexpr int D = 256;
     static constexpr int QT_BYTES = 128 * D * 2;
     static constexpr int KH = 64;                       // keys of a K tile held by one CTA
-    static constexpr int KBLK = KH * 128;               // one 64-column block of them
-    static constexpr int VBLK = PC_BN * 128;            // one 64-column block of V
+    static constexpr int KGROUP = 4 * 1024;             // an 8-row group of a K half: four 64-column blocks
+    static constexpr int VGROUP = 2 * 1024;             // and of a V half: two
     static constexpr int SLOT = 32768;                  // one CTA's half of a K or V tile
-    static constexpr int NS = 5;
+    static constexpr int NS = E4M3 ? 3 : 5;
+    static constexpr int STG_BYTES = SLOT / 2 + 128;    // e4m3: staged codes of a half tile, scale bytes
+    static constexpr int NSTG = E4M3 ? 4 : 0;
     static constexpr int CTRL = 1024;
-    static constexpr int SMEM = QT_BYTES + NS * SLOT + CTRL;
+    static constexpr int SMEM = QT_BYTES + NS * SLOT + NSTG * STG_BYTES + CTRL;
+    static_assert(SMEM <= 232448, "shared memory");
     static constexpr uint32_t O_COL = 256;
-    // warps 0-3 softmax, 4 Q (and bf16 K, V) copies, 5 MMA (leader) and TMEM; e4m3: 6 and 7 idle, 8-11 converters
+    // warps 0-3 softmax, 4 copies, 5 MMA (leader) and TMEM; e4m3: 6 and 7 idle, 8-11 converters
     static constexpr int WARP_COPY = 4, WARP_MMA = 5, WARP_CONV = 8;
     static constexpr int THREADS = E4M3 ? 384 : 192;
 };
 enum : int {
     PPB_QFULL = 0, PPB_QEMPTY = 1, PPB_S = 2 /* [2] */, PPB_P = 4 /* [2] */, PPB_PV = 6, PPB_DRAIN = 7,
-    PPB_FULL = 8 /* [5] */, PPB_EMPTY = 13 /* [5] */, PPB_NUM = 18
+    PPB_FULL = 8 /* [5] */, PPB_EMPTY = 13 /* [5] */, PPB_SFULL = 18 /* [4] */, PPB_SEMPTY = 22 /* [4] */, PPB_NUM = 26
 };
 
 // Arrival on a barrier of the pair's leader that orders this thread's earlier shared-memory
@@ -55,7 +58,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         return;
     }
     uint8_t* sKV = smem + C::QT_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + C::NS * C::SLOT);
+    uint8_t* sStg = sKV + C::NS * C::SLOT;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sStg + C::NSTG * C::STG_BYTES);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + PPB_NUM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     long long* s_scr = reinterpret_cast<long long*>(tmem_holder + 2);
@@ -85,6 +89,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(PPBAR(PPB_FULL + s), E4M3 ? 8 : 2);
             mbar_init(PPBAR(PPB_EMPTY + s), 1);
+        }
+        for (int s = 0; s < C::NSTG; ++s) {
+            mbar_init(PPBAR(PPB_SFULL + s), 33);   // the byte count's, and every copying lane's scale bytes
+            mbar_init(PPBAR(PPB_SEMPTY + s), 4);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -121,7 +129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             const int je = max(w.end(0), w.end(1));
 #pragma unroll 1
             for (int j = w.t0; j < je; ++j) {
-                ok = __all_sync(0xffffffffu, chunk_wait(PPBAR(PPB_S + (cnt & 1)), (cnt >> 1) & 1, abort_flag, wlim));
+                ok = chunk_wait_warp(PPBAR(PPB_S + (cnt & 1)), (cnt >> 1) & 1, abort_flag, wlim);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lane_base + (cnt & 1) * PC_BN;
@@ -170,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 l_sum = l_sum * factor + (((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y)));
                 if (rescale) {
                     // PV of the tile before: commit number cnt - 1 on its barrier, and none after it yet
-                    ok = __all_sync(0xffffffffu, chunk_wait(PPBAR(PPB_PV), (cnt - 1) & 1, abort_flag, wlim));
+                    ok = chunk_wait_warp(PPBAR(PPB_PV), (cnt - 1) & 1, abort_flag, wlim);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -193,8 +201,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             if (has) {
                 // The last two PVs in turn: a parity wait tells one phase from the next only, and
                 // "S ready" of the last tile vouches for the PVs up to two before it.
-                ok = cnt < 2 || chunk_wait(PPBAR(PPB_PV), cnt & 1, abort_flag, wlim);
-                ok = __all_sync(0xffffffffu, ok && chunk_wait(PPBAR(PPB_PV), (cnt - 1) & 1, abort_flag, wlim));
+                ok = cnt < 2 || chunk_wait_warp(PPBAR(PPB_PV), cnt & 1, abort_flag, wlim);
+                ok = ok && chunk_wait_warp(PPBAR(PPB_PV), (cnt - 1) & 1, abort_flag, wlim);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -246,8 +254,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             constexpr uint32_t IDESC_S = make_idesc_bf16(256, PC_BN, false);
             constexpr uint32_t IDESC_PV = make_idesc_bf16(256, D, true);
             const uint64_t q_desc0 = make_smem_desc(sQ_addr, 16, 1024, 2);
-            const uint64_t k_desc0 = make_smem_desc(sKV_addr, 16, 1024, 2);
-            const uint64_t v_desc0 = make_smem_desc(sKV_addr, C::VBLK, 1024, 2);
+            const uint64_t k_desc0 = make_smem_desc(sKV_addr, 16, C::KGROUP, 2);
+            const uint64_t v_desc0 = make_smem_desc(sKV_addr, 1024, C::VGROUP, 2);
             uint32_t item = 0, s_cnt = 0, p_cnt = 0, q_phase = 0;
             bool ok = true;
             auto next_item = [&]() -> int {
@@ -262,11 +270,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 if (!ok) return;
                 const uint64_t kd = k_desc0 + static_cast<uint64_t>(slot) * (C::SLOT >> 4);
 #pragma unroll
-                for (int t = 0; t < D / 16; ++t) {
-                    const int c = t >> 2, kk = t & 3;
-                    mma_ss_pair_elect(tmem + (s_cnt & 1) * PC_BN, q_desc0 + static_cast<uint64_t>(((c * 128 * 128) >> 4) + kk * 2),
-                                      kd + static_cast<uint64_t>(((c * C::KBLK) >> 4) + kk * 2), IDESC_S, t != 0 ? 1u : 0u);
-                }
+                for (int c = 0; c < D / 64; ++c)
+                    mma_ss_pair_elect_x4<2, 2>(tmem + (s_cnt & 1) * PC_BN, q_desc0 + static_cast<uint64_t>((c * 128 * 128) >> 4),
+                                               kd + static_cast<uint64_t>((c * 1024) >> 4), IDESC_S, c != 0 ? 1u : 0u);
                 tc_commit_pair_elect(PPBAR(PPB_EMPTY + slot), 0x3);
                 tc_commit_pair_elect(PPBAR(PPB_S + (s_cnt & 1)), 0x3);
                 ++s_cnt;
@@ -288,9 +294,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     tc_fence_after();
                     const uint64_t vd = v_desc0 + static_cast<uint64_t>(slot) * (C::SLOT >> 4);
 #pragma unroll
-                    for (int kb = 0; kb < PC_BN / 16; ++kb)
-                        mma_ts_pair_elect(tmem + C::O_COL, tmem + (p_cnt & 1) * PC_BN + kb * 8u,
-                                          vd + static_cast<uint64_t>((kb * 16 * 128) >> 4), IDESC_PV, kb == 0 && j == w.t0 ? 0u : 1u);
+                    for (int kb = 0; kb < PC_BN / 16; kb += 4)
+                        mma_ts_pair_elect_x4<8, (2 * C::VGROUP) / 16>(tmem + C::O_COL, tmem + (p_cnt & 1) * PC_BN + kb * 8u,
+                                                                      vd + static_cast<uint64_t>((kb * 2 * C::VGROUP) >> 4), IDESC_PV, kb == 0 && j == w.t0 ? 0u : 1u);
                     tc_commit_pair_elect(PPBAR(PPB_EMPTY + slot), 0x3);
                     tc_commit_pair_elect(PPBAR(PPB_PV), 0x3);
                     ++p_cnt;
@@ -312,13 +318,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         }
         __syncwarp();
     } else if (warp == C::WARP_COPY) {
-        // ================================================================ copies (both CTAs): Q, and bf16 K and V halves
+        // ================================================================ copies (both CTAs): Q, and K and V halves
         if (lane == 0) {
             tma_prefetch_map(&tm_q);
-            if constexpr (!E4M3) {
-                tma_prefetch_map(&tm_k);
-                tma_prefetch_map(&tm_v);
-            }
+            tma_prefetch_map(&tm_k);
+            tma_prefetch_map(&tm_v);
         }
         // Q is read once; half of the K/V lines are kept in L2 ahead of it and of the output
         const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last_half();
@@ -342,30 +346,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     for (int c = 0; c < D / 64; ++c)
                         tma_load_4d_pair_hint(sQ_addr + c * 128 * 128, &tm_q, c * 64, 0, w.h, w.q0 + w.c.tok(rank), l_q, pol_q);
             }
-            if constexpr (!E4M3) {
-                const int32_t* table = p.table + w.b * p.table_stride;
-                // lane i: box i of this CTA's K half / of V
-                auto lookup = [&](int j, bool k, int* row) {
-                    const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * p.box_rows;
-                    int page = p.c.num_pages;
-                    *row = 0;
-                    if (lane < (k ? k_boxes : v_boxes) && j < je && key < w.kv) {
-                        const int pj = page_index(p, key);
-                        const int got = __ldg(table + pj);
-                        if (got >= 0 && got < p.c.num_pages) {
-                            page = got;
-                            *row = key - pj * p.c.page_size;
-                        } else {
-                            atomicOr(&g_paged_status, STATUS_CACHE);
-                        }
+            const int32_t* table = p.table + w.b * p.table_stride;
+            // lane i copies box i of this CTA's K half / of V; pages are looked up a tile ahead
+            auto lookup = [&](int j, bool k) {
+                const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * p.box_rows;
+                return page_at(p, table, key, lane < (k ? k_boxes : v_boxes) && j < je && key < w.kv, true);
+            };
+            auto lookup_scale = [&](int j, bool k) {       // e4m3: the lane's group of 8 rows
+                const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * 8;
+                return page_at(p, table, key, E4M3 && lane < (k ? 8 : 16) && j < je && key < w.kv, false);
+            };
+            auto copy = [&](bool k, int j, const PageAt& a, const PageAt& sa) {
+                if constexpr (E4M3) {
+                    // into staging, on this CTA's own barriers
+                    const int slot = static_cast<int>(item % C::NSTG);
+                    ok = ok && chunk_wait_warp(PPBAR(PPB_SEMPTY + slot), ((item / C::NSTG) & 1u) ^ 1u, abort_flag, wlim);
+                    if (!ok) return;
+                    ++item;
+                    if (lane == 0) mbar_arrive_expect_tx(PPBAR(PPB_SFULL + slot), C::SLOT / 2);
+                    __syncwarp();
+                    const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && leader && k && j == w.t0 && lane == 0;
+                    const uint32_t dst = smem_u32(sStg) + slot * C::STG_BYTES;
+                    if (lane < (k ? k_boxes : v_boxes) && !drop)
+                        tma_load_4d(dst + lane * p.box_rows * (k ? 256 : 128), k ? &tm_k : &tm_v, k ? 0 : rank * 128, a.row, w.h, a.page, PPBAR(PPB_SFULL + slot));
+                    if (lane < (k ? 8 : 16)) {
+                        const bool have = sa.page < p.c.num_pages;
+                        const uint8_t* src = p.c.scale[k ? 0 : 1];
+                        if (have) src += (static_cast<long long>(sa.page) * p.c.Hkv + w.h) * p.c.page_size + sa.row;
+                        cp_async8(dst + C::SLOT / 2 + lane * 8, src, have);
                     }
-                    return page;
-                };
-                int k_row, v_row, k_row_n, v_row_n;
-                int k_page = lookup(w.t0, true, &k_row), v_page = lookup(w.t0, false, &v_row);
-                int k_page_n = lookup(w.t0 + 1, true, &k_row_n), v_page_n = v_page;
-                // items in the MMA warp's order: K(t0), K(t0+1), then V(j), K(j+2)
-                auto copy = [&](bool k, int j, int page, int row) {
+                    cp_async_mbar_arrive_noinc(PPBAR(PPB_SFULL + slot));
+                    __syncwarp();
+                } else {
                     const int slot = static_cast<int>(item % C::NS);
                     ok = ok && chunk_wait_warp(PPBAR(PPB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
                     if (!ok) return;
@@ -374,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     const int valid = w.kv - j * PC_BN;      // rows of the tile that exist
                     const int cut = !k && valid < PC_BN && valid % p.box_rows != 0 ? valid / p.box_rows : -1;   // the box to fill by hand
                     if (cut >= 0) {
-                        const int pg = __shfl_sync(0xffffffffu, page, cut), r0 = __shfl_sync(0xffffffffu, row, cut);
+                        const int pg = __shfl_sync(0xffffffffu, a.page, cut), r0 = __shfl_sync(0xffffffffu, a.row, cut);
                         const int n = pg < p.c.num_pages ? valid - cut * p.box_rows : 0;
                         const uint8_t* src = p.c.data[1] + w.h * p.c.sh[1] + rank * 256;
                         if (n > 0) src += pg * p.c.sp[1] + r0 * p.c.st[1];
@@ -382,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                             const int rr = x >> 4, c = x & 15, r = cut * p.box_rows + rr;
                             uint4 v = make_uint4(0u, 0u, 0u, 0u);
                             if (rr < n) v = __ldg(reinterpret_cast<const uint4*>(src + rr * p.c.st[1]) + c);
-                            *reinterpret_cast<uint4*>(sKV + slot * C::SLOT + (c >> 3) * C::VBLK + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                            *reinterpret_cast<uint4*>(sKV + slot * C::SLOT + (r >> 3) * C::VGROUP + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
                         }
                         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                         __syncwarp();
@@ -394,29 +406,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     }
                     __syncwarp();
                     const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && leader && k && j == w.t0 && lane == 0;
-                    const uint32_t dst = sKV_addr + slot * C::SLOT + lane * p.box_rows * 128;
-                    if (k) {
-                        if (lane < k_boxes && !drop)
-#pragma unroll
-                            for (int c = 0; c < D / 64; ++c)
-                                tma_load_4d_pair_hint(dst + c * C::KBLK, &tm_k, c * 64, row, w.h, page, l_full, pol_kv);
-                    } else if (lane < v_boxes && lane != cut) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            tma_load_4d_pair_hint(dst + c * C::VBLK, &tm_v, rank * 128 + c * 64, row, w.h, page, l_full, pol_kv);
-                    }
+                    const uint32_t dst = sKV_addr + slot * C::SLOT + lane * (p.box_rows / 8) * (k ? C::KGROUP : C::VGROUP);
+                    if (lane < (k ? k_boxes : v_boxes) && lane != cut && !drop)
+                        tma_load_5d_pair_hint(dst, k ? &tm_k : &tm_v, 0, 0, w.h * p.head_units[k ? 0 : 1] + (k ? 0 : 2 * rank), a.row / 8, a.page, l_full, pol_kv);
                     __syncwarp();
-                };
-                copy(true, w.t0, k_page, k_row);
-                if (w.t0 + 1 < je) copy(true, w.t0 + 1, k_page_n, k_row_n);
-                for (int j = w.t0; j < je && ok; ++j) {
-                    k_page = lookup(j + 2, true, &k_row);
-                    v_page_n = lookup(j + 1, false, &v_row_n);
-                    copy(false, j, v_page, v_row);
-                    if (j + 2 < je) copy(true, j + 2, k_page, k_row);
-                    v_page = v_page_n;
-                    v_row = v_row_n;
                 }
+            };
+            // items in the MMA warp's order: K(t0), K(t0+1), then V(j), K(j+2)
+            PageAt ka = lookup(w.t0, true), ks = lookup_scale(w.t0, true), va = lookup(w.t0, false), vs = lookup_scale(w.t0, false);
+            PageAt kn = lookup(w.t0 + 1, true), kns = lookup_scale(w.t0 + 1, true);
+            copy(true, w.t0, ka, ks);
+            if (w.t0 + 1 < je) copy(true, w.t0 + 1, kn, kns);
+            for (int j = w.t0; j < je && ok; ++j) {
+                ka = lookup(j + 2, true);
+                ks = lookup_scale(j + 2, true);
+                const PageAt vn = lookup(j + 1, false), vns = lookup_scale(j + 1, false);
+                copy(false, j, va, vs);
+                if (j + 2 < je) copy(true, j + 2, ka, ks);
+                va = vn;
+                vs = vns;
             }
         }
         if (*abort_flag || !ok) {
@@ -431,96 +439,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         if constexpr (E4M3) {
             constexpr int X = 8;                 // 16-code chunks per thread and item
             const int t = tid - 32 * C::WARP_CONV;
-            uint4 data[X];
-            uint32_t scale[X];
             uint32_t item = 0;
             bool ok = true;
-            // K: 64 rows of 16 chunks; V: 128 rows of this rank's 8 chunks
-            auto fetch = [&](int x, int j, bool k) {
-                const int r = k ? x * 8 + (t >> 4) : x * 16 + (t >> 3);
-                const int key = j * PC_BN + (k ? rank * C::KH : 0) + r;
-                const int which = k ? 0 : 1;
-                data[x] = make_uint4(0u, 0u, 0u, 0u);
-                scale[x] = 127u;
-                if (key < w.kv) {
-                    const int pj = page_index(p, key);
-                    const int row = key - pj * p.c.page_size;
-                    const int page = __ldg(p.table + w.b * p.table_stride + pj);
-                    if (page >= 0 && page < p.c.num_pages) {
-                        data[x] = __ldg(reinterpret_cast<const uint4*>(p.c.data[which] + page * p.c.sp[which] + w.h * p.c.sh[which] + row * p.c.st[which]) +
-                                        (k ? t & 15 : rank * 8 + (t & 7)));
-                        scale[x] = __ldg(p.c.scale[which] + (static_cast<long long>(page) * p.c.Hkv + w.h) * p.c.page_size + row);
-                    } else if (!k && leader && (t & 7) == 0) {
-                        atomicOr(&g_paged_status, STATUS_CACHE);
-                    }
-                }
-            };
             for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
                 const int je = max(w.end(0), w.end(1));
-                if (je <= w.t0) continue;
-                // items: K(t0), K(t0+1), then V(j), K(j+2); item s of the segment's 2 (je - t0)
-                const int n = 2 * (je - w.t0);
-                auto what = [&](int s, int* j) {     // whether item s is a K tile, and its key tile
-                    if (s < 2 && s < je - w.t0) {
-                        *j = w.t0 + s;
-                        return true;
-                    }
-                    if (je - w.t0 == 1) {
-                        *j = w.t0;
-                        return false;
-                    }
-                    const int e = s - 2;             // V(0) K(2) V(1) K(3) ... V(n-3) K(n-1) V(n-2) V(n-1)
-                    if (e >= n - 4) {
-                        *j = je - (n - s);
-                        return false;
-                    }
-                    *j = w.t0 + (e >> 1) + ((e & 1) ? 2 : 0);
-                    return (e & 1) != 0;
-                };
-                int j0;
-                bool k = what(0, &j0);
-#pragma unroll
-                for (int x = 0; x < X; ++x) fetch(x, j0, k);
-                for (int s = 0; s < n && ok; ++s) {
-                    const int slot = static_cast<int>(item % C::NS);
-                    ok = chunk_wait_warp(PPBAR(PPB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
-                    if (!ok) break;
+                // items: K(t0), K(t0+1), then V(j), K(j+2)
+                auto convert = [&](auto is_k, int j) {
+                    constexpr bool k = decltype(is_k)::value;
+                    const int slot = static_cast<int>(item % C::NS), stg = static_cast<int>(item % C::NSTG);
+                    ok = ok && chunk_wait_warp(PPBAR(PPB_SFULL + stg), (item / C::NSTG) & 1u, abort_flag, wlim) &&
+                         chunk_wait_warp(PPBAR(PPB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
+                    if (!ok) return;
                     ++item;
-                    int jn = 0;
-                    const bool kn = s + 1 < n ? what(s + 1, &jn) : false;
-                    uint8_t* dst = sKV + slot * C::SLOT;
+                    // K: this rank's 64 rows of 16 chunks; V: 128 rows of this rank's 8 chunks
+                    constexpr int CPR = k ? 16 : 8, RPX = 128 / CPR, GROUP = k ? C::KGROUP : C::VGROUP;
+                    const int r0 = t / CPR, c16 = t % CPR, blk = c16 >> 2;
+                    const int left = w.kv - j * PC_BN - (k ? rank * C::KH : 0);   // rows that exist
+                    const uint8_t* src = sStg + stg * C::STG_BYTES;
+                    uint8_t* dst = sKV + slot * C::SLOT + blk * 1024;
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
-                        const uint32_t wd[4] = {data[x].x, data[x].y, data[x].z, data[x].w};
-                        const uint32_t code = scale[x];
-                        if (s + 1 < n) fetch(x, jn, kn);
-                        const uint32_t f = scale_factor(code) * 0x10001u;
-                        uint32_t o[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[2 * e] = widen2(__byte_perm(wd[e], 0u, 0x1404), f);
-                            o[2 * e + 1] = widen2(__byte_perm(wd[e], 0u, 0x3424), f);
+                        const int r = x * RPX + r0;
+                        uint4 d = *reinterpret_cast<const uint4*>(src + (r * CPR + c16) * 16);
+                        uint32_t code = src[C::SLOT / 2 + r];
+                        if (r >= left) {
+                            d = make_uint4(0u, 0u, 0u, 0u);
+                            code = 127u;
                         }
-                        if (code > 134u && code != SCALE_NAN) {   // a scale above 2^7: the rest of it
-                            const uint32_t f2 = (code - 7u) << 7;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f2 * 0x10001u);
-                        }
-                        const int r = k ? x * 8 + (t >> 4) : x * 16 + (t >> 3);
-                        const int c16 = k ? t & 15 : t & 7;
-                        const int blk = c16 >> 2, ch = (c16 & 3) * 2;
-                        uint8_t* line = dst + blk * (k ? C::KBLK : C::VBLK) + r * 128;
-                        const int sw = r & 7;
-                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                        const bool flip = blk & 1;
-                        *reinterpret_cast<uint4*>(line + (((ch + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? hi : lo;
-                        *reinterpret_cast<uint4*>(line + (((ch + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? lo : hi;
+                        store_codes(d, code, dst + (r >> 3) * GROUP + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
                     }
-                    k = kn;
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();
-                    const bool drop = (p.debug & ATTN_DEBUG_DROP_COPY) && item == 1 && leader && warp == C::WARP_CONV;
-                    if (lane == 0 && !drop) mbar_arrive_cluster_release(mapa_shared(PPBAR(PPB_FULL + slot), 0));
+                    if (lane == 0) {
+                        mbar_arrive_cluster_release(mapa_shared(PPBAR(PPB_FULL + slot), 0));
+                        mbar_arrive(PPBAR(PPB_SEMPTY + stg));
+                    }
+                };
+                if (w.t0 < je) convert(std::true_type{}, w.t0);
+                if (w.t0 + 1 < je) convert(std::true_type{}, w.t0 + 1);
+                for (int j = w.t0; j < je && ok; ++j) {
+                    convert(std::false_type{}, j);
+                    if (j + 2 < je) convert(std::true_type{}, j + 2);
                 }
             }
         }

@@ -98,6 +98,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* map, int x, int y, int z, int w, int v, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
+        : "memory");
+}
+// Arrives on `bar` (an arrival it counts on) once this thread's earlier cp.async are complete.
+__device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
@@ -266,6 +278,14 @@ __device__ __forceinline__ void tma_load_4d_pair_hint(uint32_t dst, const void* 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar_cluster), "l"(policy)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_5d_pair_hint(uint32_t dst, const void* map, int x, int y, int z, int w, int v,
+                                                      uint32_t bar_cluster, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar_cluster), "l"(policy)
+        : "memory");
+}
 // L2 policies: lines read under evict_last stay in L2 ahead of normal and evict_first lines.
 // The fractional form gives evict_last to half of the lines an access covers (chosen by
 // address) and leaves the priority of the other half unchanged.
@@ -348,6 +368,108 @@ __device__ __forceinline__ void tc_commit_pair_elect(uint32_t bar, uint16_t cta_
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n"
         "}\n" ::"r"(bar),
         "h"(cta_mask)
+        : "memory");
+}
+// Four MMAs of consecutive k-steps, issued under one election (operands A_STEP and B_STEP apart, in
+// the units of their descriptors or TMEM columns): accumulate is the first one's.
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_ss_elect_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, e, t;\n"
+        ".reg .b32 r;\n"
+        ".reg .b64 a<4>;\n"
+        ".reg .b64 b<4>;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.eq.b32 t, 0, 0;\n"
+        "add.s64 a1, %1, %5;\n"
+        "add.s64 b1, %2, %8;\n"
+        "add.s64 a2, %1, %6;\n"
+        "add.s64 b2, %2, %9;\n"
+        "add.s64 a3, %1, %7;\n"
+        "add.s64 b3, %2, %10;\n"
+        "elect.sync r|e, 0xffffffff;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(A_STEP), "n"(2 * A_STEP), "n"(3 * A_STEP), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+        : "memory");
+}
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_ts_elect_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, e, t;\n"
+        ".reg .b32 r;\n"
+        ".reg .b32 a<4>;\n"
+        ".reg .b64 b<4>;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.eq.b32 t, 0, 0;\n"
+        "add.u32 a1, %1, %5;\n"
+        "add.s64 b1, %2, %8;\n"
+        "add.u32 a2, %1, %6;\n"
+        "add.s64 b2, %2, %9;\n"
+        "add.u32 a3, %1, %7;\n"
+        "add.s64 b3, %2, %10;\n"
+        "elect.sync r|e, 0xffffffff;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(A_STEP), "n"(2 * A_STEP), "n"(3 * A_STEP), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+        : "memory");
+}
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_ss_pair_elect_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, e, t;\n"
+        ".reg .b32 r;\n"
+        ".reg .b64 a<4>;\n"
+        ".reg .b64 b<4>;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.eq.b32 t, 0, 0;\n"
+        "add.s64 a1, %1, %5;\n"
+        "add.s64 b1, %2, %8;\n"
+        "add.s64 a2, %1, %6;\n"
+        "add.s64 b2, %2, %9;\n"
+        "add.s64 a3, %1, %7;\n"
+        "add.s64 b3, %2, %10;\n"
+        "elect.sync r|e, 0xffffffff;\n"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(A_STEP), "n"(2 * A_STEP), "n"(3 * A_STEP), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+        : "memory");
+}
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_ts_pair_elect_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p, e, t;\n"
+        ".reg .b32 r;\n"
+        ".reg .b32 a<4>;\n"
+        ".reg .b64 b<4>;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "setp.eq.b32 t, 0, 0;\n"
+        "add.u32 a1, %1, %5;\n"
+        "add.s64 b1, %2, %8;\n"
+        "add.u32 a2, %1, %6;\n"
+        "add.s64 b2, %2, %9;\n"
+        "add.u32 a3, %1, %7;\n"
+        "add.s64 b3, %2, %10;\n"
+        "elect.sync r|e, 0xffffffff;\n"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(A_STEP), "n"(2 * A_STEP), "n"(3 * A_STEP), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
         : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {

@@ -48,6 +48,7 @@ BAD_CACHES = [
     (dict(k=0), 1), (dict(v=0), 1), (dict(k=0x10008), 1), (dict(P=0), 1), (dict(page=0), 1), (dict(H=0), 1),
     (dict(P=1 << 20, page=1 << 12), 1), (dict(fmt=1), 1), (dict(fmt=1, ks=0x10000), 1), (dict(fmt=2), 2),
     (dict(page=12), 2), (dict(D=96), 2), (dict(kst=(1024, 60, 64)), 1), (dict(vst=(1024, 64, 32)), 1),
+    (dict(kst=(4096, 72, 256)), 1),                                       # heads not a whole number of 64-column blocks apart
     (dict(fmt=1, ks=0x10000, vs=0x10000, kst=(1024, 72, 128)), 1),       # 8-byte rows in an e4m3 cache
 ]
 
