@@ -86,6 +86,37 @@ __device__ __forceinline__ int checked_page(const PagedParams& p, int b, int pj,
     return -1;
 }
 
+// Bounded waits on an mbarrier phase: false if the CTA's abort flag (where there is one) is set or
+// the time limit runs out, which sets it and the device timeout flag.
+template <bool CLUSTER>   // acquire at cluster scope
+__device__ __forceinline__ bool chunk_poll(uint32_t bar, uint32_t parity) {
+    return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+}
+template <bool CLUSTER>
+__device__ __noinline__ bool chunk_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (chunk_poll<CLUSTER>(bar, parity)) return true;
+        if (abort_flag != nullptr && *abort_flag) return false;
+        if (global_timer_ns() - t0 > limit_ns) {
+            if (abort_flag != nullptr) *abort_flag = 1;
+            atomicOr(&g_paged_status, STATUS_TIMEOUT);
+            return false;
+        }
+    }
+}
+// Waits of a whole warp, which stays converged: true once every lane has seen the phase complete.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool chunk_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
+    if (__all_sync(0xffffffffu, chunk_poll<CLUSTER>(bar, parity))) return true;
+    return __all_sync(0xffffffffu, chunk_wait_slow<CLUSTER>(bar, parity, abort_flag, limit_ns)) != 0;
+}
+
+// A combine kernel's wait for the kernel before it in the stream to be complete (it is launched
+// without one); allow_next_kernel, in that kernel, lets it be launched.
+__device__ __forceinline__ void wait_for_main_kernel() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 #include "paged_rows.cuh"
 #include "paged_chunk.cuh"
 #include "paged_pair.cuh"
@@ -210,6 +241,24 @@ int rows_ctas(int per_sm, int B, int Hkv, long long kv_cap) {
 // Few rows per key head: at most one m16 tile of them.
 bool few_rows(long long max_q, int G) { return max_q * G <= PR_ROWS; }
 
+// A combine kernel behind the main one, launched to overlap it (it waits on the device).
+attn_status launch_combine(void (*kern)(PagedParams, int), dim3 grid, int threads, cudaStream_t stream, const PagedParams& p, int n) {
+    if (grid.x == 0) return launched();
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    memset(&attr, 0, sizeof attr);
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kern, p, n);
+    return launched();
+}
+
 template <int D, bool E4M3>
 attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
     using C = RowsCfg<D, E4M3>;
@@ -221,9 +270,21 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
     }
-    paged_rows_kernel<D, E4M3><<<n, PR_THREADS, C::SMEM, stream>>>(p, n);
-    paged_rows_combine_kernel<D><<<p.B * p.c.Hkv, PR_THREADS, 0, stream>>>(p, n);
-    return launched();
+    CUtensorMap mk, mv;
+    memset(&mk, 0, sizeof mk);
+    mv = mk;
+    p.box_rows = (p.c.page_size & 15) == 0 ? 16 : 8;
+    for (int i = 0; E4M3 && i < 2; ++i) {
+        const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.c.page_size), static_cast<cuuint64_t>(p.c.Hkv),
+                                    static_cast<cuuint64_t>(p.c.num_pages)};
+        const cuuint64_t str[3] = {static_cast<cuuint64_t>(p.c.st[i]), static_cast<cuuint64_t>(p.c.sh[i]), static_cast<cuuint64_t>(p.c.sp[i])};
+        const cuuint32_t box[4] = {C::SW, static_cast<cuuint32_t>(p.box_rows), 1u, 1u};
+        if (!encode_map(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.c.data[i], dims, str, box,
+                        C::SW == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : C::SW == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B))
+            return ATTN_ERR_CUDA;
+    }
+    paged_rows_kernel<D, E4M3><<<n, PR_THREADS, C::SMEM, stream>>>(mk, mv, p, n);
+    return launch_combine(paged_rows_combine_kernel<D>, dim3(n - 1), PR_THREADS, stream, p, n);
 }
 
 // Runs of the chunk kernels: one per SM (per CTA pair at head dim 256), or fewer where the
@@ -292,8 +353,7 @@ attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
         return ATTN_ERR_CUDA;
     }
     kern<<<grid, threads, smem, stream>>>(mq, mk, mv, p, n);
-    if (n > 1) paged_chunk_combine_kernel<D><<<dim3(n - 1, 8), 128, 0, stream>>>(p, n);
-    return launched();
+    return launch_combine(paged_chunk_combine_kernel<D>, dim3(n - 1, 8), 128, stream, p, n);
 }
 
 template <int D>

@@ -75,30 +75,6 @@ enum : int {
     PCB_FULL = 13 /* [12] */, PCB_EMPTY = 25 /* [12] */, PCB_SFULL = 37 /* [8] */, PCB_SEMPTY = 45 /* [8] */, PCB_NUM = 53
 };
 
-template <bool CLUSTER>   // acquire at cluster scope
-__device__ __forceinline__ bool chunk_poll(uint32_t bar, uint32_t parity) {
-    return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-}
-template <bool CLUSTER>
-__device__ __noinline__ bool chunk_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (chunk_poll<CLUSTER>(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > limit_ns) {
-            *abort_flag = 1;
-            atomicOr(&g_paged_status, STATUS_TIMEOUT);
-            return false;
-        }
-    }
-}
-// Waits of a whole warp, which stays converged: true once every lane has seen the phase complete.
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool chunk_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit_ns) {
-    if (__all_sync(0xffffffffu, chunk_poll<CLUSTER>(bar, parity))) return true;
-    return __all_sync(0xffffffffu, chunk_wait_slow<CLUSTER>(bar, parity, abort_flag, limit_ns)) != 0;
-}
-
 // Keys that query row i of a sequence with n rows and kv keys sees.
 __device__ __forceinline__ int keys_seen(int causal, int kv, int n, int i) {
     return causal ? min(kv, max(0, kv - n + i + 1)) : kv;
@@ -299,6 +275,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
 #define CBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    allow_next_kernel();
     int b_first;
     long long at, all;
     const long long per = chunk_deal<C::THREADS>(p, n_ctas, blockIdx.x, s_scr, blockIdx.x == 0, &b_first, &at, &all);
@@ -768,6 +745,7 @@ __global__ void __launch_bounds__(128) paged_chunk_combine_kernel(const PagedPar
     long long at, all;
     const long long c = blockIdx.x + 1;
     const long long per = chunk_deal<128>(p, n_ctas, c, s_scr, false, &b, &at, &all);
+    wait_for_main_kernel();                     // every block, so that this grid never ends before that one
     if (c * per >= all) return;
     ChunkWalk w;
     w.begin(p, b, at, all);
@@ -782,18 +760,18 @@ __global__ void __launch_bounds__(128) paged_chunk_combine_kernel(const PagedPar
         if (tok >= w.c.ntok(g) || tok >= p.tpt) continue;
         auto slot = [&](long long cc) { return ((2 * cc + (cc == c0 ? 1 : 0)) * 2 + g) * 128 + rr; };
         float M = -INFINITY;
-        for (long long cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldg(p.part_lse + slot(cc)));
+        for (long long cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_lse + slot(cc)));
         float s = 0.0f, acc[PER];
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] = 0.0f;
         for (long long cc = c0; cc <= c1; ++cc) {
-            const float lc = __ldg(p.part_lse + slot(cc));
+            const float lc = __ldcg(p.part_lse + slot(cc));
             if (lc == -INFINITY) continue;      // nothing was stored
             const float wgt = expf(lc - M);
             s += wgt;
             const float* src = p.part_out + slot(cc) * D + lane * PER;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] += wgt * __ldg(src + e);
+            for (int e = 0; e < PER; ++e) acc[e] += wgt * __ldcg(src + e);
         }
         const bool some = !(s == 0.0f);
         const float inv = some ? 1.0f / s : 0.0f;

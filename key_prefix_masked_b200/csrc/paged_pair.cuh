@@ -70,6 +70,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
     const bool leader = rank == 0;
     const long long pair = blockIdx.x >> 1;
 
+    allow_next_kernel();
     int b_first;
     long long at, all;
     const long long per = chunk_deal<C::THREADS>(p, n_pairs, pair, s_scr, blockIdx.x == 0, &b_first, &at, &all);

@@ -9,16 +9,23 @@
 //   SM busy to the end (each CTA finds its run with a scan over kv_len).  A pair whose tiles
 //   fall to several CTAs is put together by paged_rows_combine_kernel, by log-sum-exp weights.
 // - Each of a CTA's four warps takes 16 of a tile's keys through a ring of shared memory of
-//   its own, filled with 16-byte cp.async (keys behind the sequence and pages that do not
-//   exist are filled with zeros), so no warp waits for another inside a run.
+//   its own, so no warp waits for another inside a run.  bf16 rows come by 16-byte cp.async
+//   (keys behind the sequence and pages that do not exist are filled with zeros).
 // - The 16 rows and 16 keys make one m16n8k16 tile: S = Q K^T (two MMAs per 16 dims), and
 //   P, already in the A layout, times V.  mma.sync is enough here: at HBM's rate the
 //   tensor work of a tile is a small part of its load time.
-// - e4m3 rows are widened to bf16 in registers on their way from shared memory: a code's
-//   bits moved to a bf16's place are the value times 2^-120, so one packed multiply by
-//   2^(120 + e) gives the row's value exactly (e the row's scale exponent).  To load 16 codes of
-//   one key at once, the head dims are taken in a permuted order, the same for Q and K; V is
-//   transposed by the byte permutes that place the codes.
+// - e4m3 rows halve the bytes, and the instructions per byte become the bound (the first
+//   form of this path, cp.async and five integer operations per pair of codes, ran 944
+//   instructions per 16-key tile and reached 2.8 TB/s).  So the tiles come by TMA, issued by one
+//   lane, and the codes go to the tensor cores as f16, which holds them exactly: one cvt
+//   per pair of K, a byte permute and a cvt per pair of V (which transposes it on the way).  To
+//   load 16 codes of one key at once, the head dims are taken in a permuted order, the same
+//   for Q and K.  Q is scaled to f16 by a power of two per row (its largest element in [2^14, 2^15),
+//   so what f16 drops is below 2^-39 of it); the key rows' scales multiply the scores; the
+//   value rows' scales 2^e multiply the weights, relative to E, the largest e seen: a weight
+//   times 2^(e-E) stays below 2^8.  Where e lies more than 12 below E in a tile, f16 would drop
+//   bits of such weights, and the tile's V is widened to bf16 instead, exactly: a code's bits moved
+//   to a bf16's place are the value times 2^-120, and one packed multiply by 2^(120+e-E) does the rest.
 // - The running maximum moves only when a score exceeds it by 2^8 (a vote per tile): the
 //   weights stay below 2^8 and the result is the same up to rounding.
 
@@ -33,30 +40,40 @@ struct RowsCfg {
     static constexpr int ROW = D * (E4M3 ? 1 : 2);      // bytes of one row
     static constexpr int CPR = ROW / 16;                // 16-byte chunks per row
     static constexpr int HALF = PR_WK * ROW;            // K or V part of a stage
-    static constexpr int STAGE = 2 * HALF + (E4M3 ? 32 : 0);   // + 16 K and 16 V scale bytes
+    static constexpr int STAGE = 2 * HALF;
+    // e4m3: the swizzle span that TMA applies to a row (128 bytes at most: column blocks at D = 256)
+    static constexpr int SW = ROW < 128 ? ROW : 128;
+    static constexpr int BLOCK = PR_WK * SW;            // a column block of 16 rows
     // about 96 KB of rings per CTA (two CTAs per SM), 192 KB where a stage is 16 KB (one)
     static constexpr int NST_RAW = 24576 / (2 * HALF);
     static constexpr int NST = NST_RAW < 3 ? 3 : NST_RAW > 8 ? 8 : NST_RAW;
     static constexpr int RING = PR_WARPS * NST * STAGE;
     static constexpr int MERGE = PR_WARPS * PR_ROWS * (D + 4) * 4;   // reuses the ring
-    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    // e4m3, behind the ring: each warp's barriers, and 16 K and 16 V scale bytes per stage
+    static constexpr int BARS = E4M3 ? PR_WARPS * NST * 8 : 0, SCALES = E4M3 ? PR_WARPS * NST * 32 : 0;
+    static constexpr int AREA = (RING > MERGE ? RING : MERGE) + 127 & ~127;
+    static constexpr int SMEM = AREA + BARS + SCALES;
     static constexpr int PER_SM = SMEM > 110 * 1024 ? 1 : 2;
 };
 
-// Byte offset of 16-byte chunk c of row r in a stage's K (w = 0) or V (w = 1) part.  The
-// chunk's place within its 128-byte line is permuted so that the reads below touch every
-// bank once: ldmatrix takes one chunk of 8 rows; an e4m3 key takes 16 bytes a lane, two rows to
-// a quarter warp; an e4m3 value takes 4 bytes of rows 2 q4 (+1, +8, +9) for q4 = 0..3.
+// Byte offset of 16-byte chunk c of row r in a stage's K or V part.  bf16: ldmatrix takes one
+// chunk of 8 rows, and the permutation puts those into different banks.  e4m3: what TMA's
+// swizzle of SW bytes makes of 16-row column blocks; the reads of V (4 bytes of rows 2 q4, q4 = 0..3)
+// then touch every bank once, those of K (16 bytes a lane, two rows to a quarter warp) twice.
 template <int D, bool E4M3>
-__device__ __forceinline__ uint32_t rows_swizzle(int w, int r, int c) {
-    constexpr int CPR = RowsCfg<D, E4M3>::CPR;
-    constexpr int RPL = CPR >= 8 ? 1 : 8 / CPR;            // rows per line
-    const int line = r * CPR / 8 + (CPR >= 8 ? c >> 3 : 0);
-    int pos = CPR >= 8 ? c & 7 : (r % RPL) * CPR + c;
-    if constexpr (!E4M3) pos ^= CPR >= 8 ? r & 7 : (r >> 1) & 3;
-    else if (w == 0) pos ^= CPR >= 8 ? (r & 1) << 2 : 0;
-    else pos ^= CPR >= 4 ? r & 6 : ((r >> 2) & 1) << 1;
-    return static_cast<uint32_t>(line * 128 + pos * 16);
+__device__ __forceinline__ uint32_t rows_swizzle(int r, int c) {
+    using C = RowsCfg<D, E4M3>;
+    constexpr int CPR = C::CPR;
+    if constexpr (E4M3) {
+        if constexpr (CPR >= 8) return static_cast<uint32_t>((c >> 3) * C::BLOCK + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        else if constexpr (CPR == 4) return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+        else return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
+    } else {
+        constexpr int RPL = CPR >= 8 ? 1 : 8 / CPR;            // rows per 128-byte line
+        const int line = r * CPR / 8 + (CPR >= 8 ? c >> 3 : 0);
+        const int pos = (CPR >= 8 ? c & 7 : (r % RPL) * CPR + c) ^ (CPR >= 8 ? r & 7 : (r >> 1) & 3);
+        return static_cast<uint32_t>(line * 128 + pos * 16);
+    }
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
@@ -88,6 +105,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (low 16 bits) to two f16 values, exactly.
+__device__ __forceinline__ uint32_t codes_f16(uint16_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
@@ -98,13 +130,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t widen2(uint32_t t, uint32_t f) {
     return mul_bf16x2((t & 0x80008000u) | ((t >> 4) & 0x07f007f0u), f);
 }
-// bf16 pattern of 2^(120 + e) cut to 2^127, for a scale code e + 127; NaN for 255.  What the
-// cut leaves (e > 7) is scale_rest.
+// bf16 pattern of 2^(120 + e) cut to 2^127, for a scale code e + 127; NaN for 255.
 __device__ __forceinline__ uint32_t scale_factor(uint32_t code) {
     return code == SCALE_NAN ? 0x7fffu : min(code + 120u, 254u) << 7;
-}
-__device__ __forceinline__ float scale_rest(uint32_t code) {
-    return __uint_as_float((code > 134u && code != SCALE_NAN ? code - 7u : 127u) << 23);
 }
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -166,7 +194,8 @@ __device__ __forceinline__ void rows_scan(const PagedParams& p, long long* s_sum
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
-    paged_rows_kernel(const PagedParams p, const int n_ctas) {
+    paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p,
+                      const int n_ctas) {
     using C = RowsCfg<D, E4M3>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ long long s_sum[PR_WARPS];
@@ -175,6 +204,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int q4 = lane & 3, r8 = lane >> 2;
 
+    allow_next_kernel();
     const RowsDeal deal = rows_deal(p, n_ctas, s_sum, blockIdx.x == 0);
     const long long all = deal.all(p.c.Hkv);
     long long unit = blockIdx.x * deal.per;
@@ -188,6 +218,18 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
     int b = s_b;
     long long rem = unit - s_first * p.c.Hkv;
     const uint32_t ring = smem_u32(smem) + warp * C::NST * C::STAGE;
+    // e4m3: this warp's barriers and scale bytes
+    const uint32_t bars = smem_u32(smem) + C::AREA + warp * C::NST * 8;
+    uint8_t* const scales = smem + C::AREA + C::BARS + warp * C::NST * 32;
+    uint32_t item = 0;       // e4m3: tiles consumed, over all segments
+    bool ok = true;          // e4m3: no wait has run out
+    if constexpr (E4M3) {
+        if (lane == 0) {
+            for (int s = 0; s < C::NST; ++s) mbar_init(bars + 8 * s, 5);   // the byte count's arrival and four scale copies'
+            fence_mbar_init();
+        }
+        __syncwarp();
+    }
 
     while (unit < unit_end) {
         int units = rows_units(p, b);
@@ -227,6 +269,28 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 qf[s][2 + e] = v.y;
             }
         }
+        float row_mul[2] = {p.scale_log2, p.scale_log2};   // what turns a row's products into log2 scores
+        if constexpr (E4M3) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t top = 0u;                         // the row's largest magnitude, as a bf16 pattern
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) top = __vmaxu2(top, __vmaxu2(qf[s][e] & 0x7fff7fffu, qf[s][2 + e] & 0x7fff7fffu));
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // amax in [2^k, 2^(k+1)): times 2^(14-k).  Rows of zeros, infinities and NaN, and exponents
+                // whose power is no normal fp32 number, are cut to what is.
+                const int up = top == 0u || top >= 0x7f80u ? 0 : min(14 + 127 - static_cast<int>(top >> 7), 126);
+                const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                row_mul[e] *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+                    for (int x = e; x < 4; x += 2)
+                        qf[s][x] = pack_f16(__uint_as_float(qf[s][x] << 16) * f, __uint_as_float(qf[s][x] & 0xffff0000u) * f);
+            }
+        }
         const int all_seen = p.causal ? max(0, kv - qr.n + 1) : kv;   // keys that every row sees
 
         // ---- loads: this warp's 16 keys of tile t; two 8-key groups, each within one page
@@ -244,6 +308,35 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             return page;
         };
         auto load = [&](int t, int page_l, int slot) {
+          if constexpr (E4M3) {
+            const uint32_t dst = ring + slot * C::STAGE, bar = bars + 8 * slot;
+            const int key0 = t * PR_TK + warp * PR_WK;
+            const int pg0 = __shfl_sync(0xffffffffu, page_l, 0), pg1 = __shfl_sync(0xffffffffu, page_l, 1);
+            const int row0 = key0 - page_index(p, key0) * p.c.page_size, row1 = key0 + 8 - page_index(p, key0 + 8) * p.c.page_size;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, C::STAGE);
+                // 16 rows lie in one page unless it ends in between: pages of 8 or an odd number of 8 rows
+                const bool one = p.box_rows == 16;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g == 1 && one) break;
+                    const int pg = g ? pg1 : pg0;
+#pragma unroll
+                    for (int b2 = 0; b2 < C::ROW / C::SW; ++b2)
+#pragma unroll
+                        for (int w = 0; w < 2; ++w)
+                            tma_load_4d(dst + w * C::HALF + b2 * C::BLOCK + g * 8 * C::SW, w ? &tm_v : &tm_k, b2 * C::SW, g ? row1 : row0, h,
+                                        pg < 0 ? p.c.num_pages : pg, bar);
+                }
+            }
+            if (lane < 4) {      // scale bytes: K and V (lane / 2) of each 8-row group (lane % 2)
+                const int pg = lane & 1 ? pg1 : pg0;
+                const uint8_t* src = p.c.scale[lane >> 1];
+                if (pg >= 0) src += (static_cast<long long>(pg) * p.c.Hkv + h) * p.c.page_size + (lane & 1 ? row1 : row0);
+                cp_async8(smem_u32(scales) + slot * 32 + 16 * (lane >> 1) + 8 * (lane & 1), src, pg >= 0);
+                cp_async_mbar_arrive_noinc(bar);
+            }
+          } else {
             const uint32_t dst = ring + slot * C::STAGE;
             const int key0 = t * PR_TK + warp * PR_WK;
 #pragma unroll
@@ -261,17 +354,11 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                         const int idx = x * 32 + lane;
                         const int r = idx / C::CPR, c = idx % C::CPR;
                         if (8 * C::CPR % 32 == 0 || idx < 8 * C::CPR)
-                            cp_async16(dst + w * C::HALF + rows_swizzle<D, E4M3>(w, 8 * g + r, c), src + (r < n ? r * p.c.st[w] + c * 16 : 0), r < n);
-                    }
-                }
-                if constexpr (E4M3) {
-                    if (lane < 2) {
-                        const uint8_t* sc = p.c.scale[lane];
-                        if (page >= 0) sc += (static_cast<long long>(page) * p.c.Hkv + h) * p.c.page_size + r0;
-                        cp_async8(dst + 2 * C::HALF + 16 * lane + 8 * g, sc, page >= 0);
+                            cp_async16(dst + w * C::HALF + rows_swizzle<D, E4M3>(8 * g + r, c), src + (r < n ? r * p.c.st[w] + c * 16 : 0), r < n);
                     }
                 }
             }
+          }
         };
         float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -284,10 +371,11 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
         for (int s = 0; s < C::NST - 1; ++s) {
             const int pg = page_next;
             page_next = page_of(tile0 + s + 1);
-            if (tile0 + s < tile1) load(tile0 + s, pg, s);
-            cp_commit();
+            if (tile0 + s < tile1) load(tile0 + s, pg, E4M3 ? static_cast<int>((item + s) % C::NST) : s);
+            if constexpr (!E4M3) cp_commit();
         }
-        int slot = 0;
+        int slot = E4M3 ? static_cast<int>(item % C::NST) : 0;
+        int e_ref = -1000;       // e4m3: E, the largest scale exponent of a value row so far
 #pragma unroll 1
         for (int t = tile0; t < tile1; ++t) {
             __syncwarp();   // every lane is done with the slot that is filled next
@@ -296,10 +384,16 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 const int pg = page_next;
                 page_next = page_of(tn + 1);
                 if (tn < tile1) load(tn, pg, slot == 0 ? C::NST - 1 : slot - 1);
-                cp_commit();
+                if constexpr (!E4M3) cp_commit();
             }
-            cp_wait<C::NST - 1>();
-            __syncwarp();
+            if constexpr (E4M3) {
+                ok = ok && chunk_wait_warp(bars + 8 * slot, (item / C::NST) & 1u, nullptr, p.wait_ns);
+                if (!ok) break;
+                ++item;
+            } else {
+                cp_wait<C::NST - 1>();
+                __syncwarp();
+            }
             const uint32_t kb = ring + slot * C::STAGE, vb = kb + C::HALF;
             const int key0 = t * PR_TK + warp * PR_WK;
             float s[2][4];
@@ -307,25 +401,31 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-            uint32_t vsc[2] = {0u, 0u};        // e4m3: factors of keys 2 q4, +1 and 2 q4 + 8, +9
-            float ks[2][2], vs[2][2];          // what the packed factors leave (1 in ordinary use)
+            float ks[2][2];          // e4m3: 2^e of keys 2 q4, +1 (and + 8)
+            int ve[2][2];            // e4m3: e of their value rows
             if constexpr (E4M3) {
-                const uint8_t* sc = smem + (kb - smem_u32(smem)) + 2 * C::HALF;
-                uint32_t kf[2];
+                const uint8_t* sc = scales + slot * 32;
+                const uint8_t* kp = smem + (kb - smem_u32(smem));
+                if (key0 + PR_WK > kv) {
+                    // value rows of a page behind the sequence hold anything, NaN codes included
+                    const int left = max(0, kv - key0);
+                    for (int x = lane; x < (PR_WK - left) * C::CPR; x += 32)
+                        *reinterpret_cast<uint4*>(smem + (vb - smem_u32(smem)) + rows_swizzle<D, true>(left + x / C::CPR, x % C::CPR)) = make_uint4(0u, 0u, 0u, 0u);
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // before TMA writes there again
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const uint32_t code = sc[8 * n + r8];
-                    kf[n] = scale_factor(code) * 0x10001u;
                     const uint32_t k2 = *reinterpret_cast<const uint16_t*>(sc + 8 * n + 2 * q4);
                     const uint32_t v2 = *reinterpret_cast<const uint16_t*>(sc + 16 + 8 * n + 2 * q4);
-                    vsc[n] = scale_factor(v2 & 255u) | scale_factor(v2 >> 8) << 16;
-                    ks[n][0] = scale_rest(k2 & 255u);
-                    ks[n][1] = scale_rest(k2 >> 8);
-                    vs[n][0] = scale_rest(v2 & 255u);
-                    vs[n][1] = scale_rest(v2 >> 8);
-                    if (key0 + PR_WK > kv) {   // scale bytes behind the sequence are anybody's
+                    ks[n][0] = scale_value(k2 & 255u);
+                    ks[n][1] = scale_value(k2 >> 8);
+                    ve[n][0] = static_cast<int>(v2 & 255u) - 127;
+                    ve[n][1] = static_cast<int>(v2 >> 8) - 127;
+                    if (key0 + PR_WK > kv) {   // so do the scale bytes
                         const int left = kv - (key0 + 8 * n + 2 * q4);
-                        vsc[n] &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                        if (left < 1) ve[n][0] = -1000;
+                        if (left < 2) ve[n][1] = -1000;
                     }
                 }
                 constexpr int RUN = D >= 64 ? 16 : 8;
@@ -336,23 +436,22 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                         const int r = 8 * n + r8;
                         uint32_t w[RUN / 4];
                         if constexpr (RUN == 16) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(smem + (kb - smem_u32(smem)) + rows_swizzle<D, true>(0, r, c * 4 + q4));
+                            const uint4 x = *reinterpret_cast<const uint4*>(kp + rows_swizzle<D, true>(r, c * 4 + q4));
                             w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
                         } else {
-                            const uint2 x = *reinterpret_cast<const uint2*>(smem + (kb - smem_u32(smem)) + rows_swizzle<D, true>(0, r, q4 >> 1) + (q4 & 1) * 8);
+                            const uint2 x = *reinterpret_cast<const uint2*>(kp + rows_swizzle<D, true>(r, q4 >> 1) + (q4 & 1) * 8);
                             w[0] = x.x; w[1] = x.y;
                         }
 #pragma unroll
                         for (int e = 0; e < RUN / 4; ++e)
-                            mma16816(s[n], qf[c * (RUN / 4) + e], widen2(__byte_perm(w[e], 0u, 0x1404), kf[n]),
-                                     widen2(__byte_perm(w[e], 0u, 0x3424), kf[n]));
+                            mma16816_f16(s[n], qf[c * (RUN / 4) + e], codes_f16(static_cast<uint16_t>(w[e])), codes_f16(static_cast<uint16_t>(w[e] >> 16)));
                     }
                 }
             } else {
 #pragma unroll
                 for (int st = 0; st < D / 16; ++st) {
                     uint32_t kf[4];   // keys 0-7 dims 0-7, 8-15; keys 8-15 dims 0-7, 8-15
-                    ldsm4(kb + rows_swizzle<D, false>(0, (lane & 7) + ((lane >> 4) << 3), st * 2 + ((lane >> 3) & 1)), kf);
+                    ldsm4(kb + rows_swizzle<D, false>((lane & 7) + ((lane >> 4) << 3), st * 2 + ((lane >> 3) & 1)), kf);
                     mma16816(s[0], qf[st], kf[0], kf[1]);
                     mma16816(s[1], qf[st], kf[2], kf[3]);
                 }
@@ -365,7 +464,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float y = s[n][e] * p.scale_log2;
+                    float y = s[n][e] * row_mul[e >> 1];
                     if constexpr (E4M3) y *= ks[n][e & 1];
                     if (masked && key0 + 8 * n + 2 * q4 + (e & 1) >= seen[e >> 1]) y = -INFINITY;
                     x[n][e] = y;
@@ -389,46 +488,115 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             }
             uint32_t pf[4];
             const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+            float wt[2][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                float w[4];
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    w[e] = exp2_approx(x[n][e] - (e < 2 ? m0 : m1));
-                    l[e >> 1] += w[e];
-                    if constexpr (E4M3) w[e] *= vs[n][e & 1];
+                    wt[n][e] = exp2_approx(x[n][e] - (e < 2 ? m0 : m1));
+                    l[e >> 1] += wt[n][e];
                 }
-                pf[2 * n] = pack_bf16(w[0], w[1]);
-                pf[2 * n + 1] = pack_bf16(w[2], w[3]);
-            }
             // ---- O += P V
             if constexpr (E4M3) {
+                // E over the tile's rows (128: a NaN row, left to its weight)
+                int top = -1000, low = 1000;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int b2 = 0; b2 < 2; ++b2) {
+                        if (ve[n][b2] < 128) top = max(top, ve[n][b2]);
+                        if (ve[n][b2] > -1000) low = min(low, ve[n][b2]);
+                    }
+                top = __reduce_max_sync(0xffffffffu, top);
+                low = __reduce_min_sync(0xffffffffu, low);
+                if (top > e_ref) {
+                    const float f = top - e_ref > 126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - (top - e_ref)) << 23);
+                    e_ref = top;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][e] *= f;
+                }
+                // 2^(e - E): of the f16 weights, or (wide) of the bf16 values
+                float vm[2][2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int b2 = 0; b2 < 2; ++b2)
+                        vm[n][b2] = ve[n][b2] == 128 ? __uint_as_float(0x7fc00000u)
+                                                     : __uint_as_float(static_cast<uint32_t>(max(127 + ve[n][b2] - e_ref, 0)) << 23);
                 const uint8_t* v = smem + (vb - smem_u32(smem));
+                const bool wide = low < e_ref - 12;
+                uint32_t vsc[2] = {0u, 0u};
 #pragma unroll
-                for (int g = 0; g < D / 32; ++g) {
-                    uint32_t w[4];   // keys 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9: dims 32 g + 4 r8 + {0..3}
+                for (int n = 0; n < 2; ++n) {
+                    if (wide) {
+                        // 2^(120 + e - E); the weights keep only a row's NaN
+                        uint32_t f2[2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = 2 * q4 + (k & 1) + 8 * (k >> 1);
-                        w[k] = *reinterpret_cast<const uint32_t*>(v + rows_swizzle<D, true>(1, r, 2 * g + (r8 >> 2)) + (r8 & 3) * 4);
+                        for (int b2 = 0; b2 < 2; ++b2) {
+                            f2[b2] = static_cast<uint32_t>(min(max(247 + ve[n][b2] - e_ref, 0), 247)) << 7;
+                            if (ve[n][b2] != 128) vm[n][b2] = 1.0f;
+                        }
+                        vsc[n] = f2[0] | f2[1] << 16;
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mma16816(o[4 * g + e], pf, widen2(__byte_perm(w[0], w[1], e << 4 | (4 + e) << 12), vsc[0]),
-                                 widen2(__byte_perm(w[2], w[3], e << 4 | (4 + e) << 12), vsc[1]));
+                    for (int e = 0; e < 4; ++e) wt[n][e] *= vm[n][e & 1];
+                    pf[2 * n] = wide ? pack_bf16(wt[n][0], wt[n][1]) : pack_f16(wt[n][0], wt[n][1]);
+                    pf[2 * n + 1] = wide ? pack_bf16(wt[n][2], wt[n][3]) : pack_f16(wt[n][2], wt[n][3]);
                 }
+                auto pv = [&](auto is_wide) {
+#pragma unroll
+                    for (int g = 0; g < D / 32; ++g) {
+                        uint32_t w[4];   // keys 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9: dims 32 g + 4 r8 + {0..3}
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = 2 * q4 + (k & 1) + 8 * (k >> 1);
+                            w[k] = *reinterpret_cast<const uint32_t*>(v + rows_swizzle<D, true>(r, 2 * g + (r8 >> 2)) + (r8 & 3) * 4);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if constexpr (decltype(is_wide)::value)
+                                mma16816(o[4 * g + e], pf, widen2(__byte_perm(w[0], w[1], e << 4 | (4 + e) << 12), vsc[0]),
+                                         widen2(__byte_perm(w[2], w[3], e << 4 | (4 + e) << 12), vsc[1]));
+                            else
+                                mma16816_f16(o[4 * g + e], pf, codes_f16(static_cast<uint16_t>(__byte_perm(w[0], w[1], e | (4 + e) << 4))),
+                                             codes_f16(static_cast<uint16_t>(__byte_perm(w[2], w[3], e | (4 + e) << 4))));
+                        }
+                    }
+                };
+                if (wide) pv(std::true_type{});
+                else pv(std::false_type{});
             } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    pf[2 * n] = pack_bf16(wt[n][0], wt[n][1]);
+                    pf[2 * n + 1] = pack_bf16(wt[n][2], wt[n][3]);
+                }
 #pragma unroll
                 for (int st = 0; st < D / 16; ++st) {
                     uint32_t vf[4];   // dims 0-7: keys 0-7, 8-15; dims 8-15: keys 0-7, 8-15
-                    ldsm4_trans(vb + rows_swizzle<D, false>(1, lane & 15, st * 2 + (lane >> 4)), vf);
+                    ldsm4_trans(vb + rows_swizzle<D, false>(lane & 15, st * 2 + (lane >> 4)), vf);
                     mma16816(o[2 * st], pf, vf[0], vf[1]);
                     mma16816(o[2 * st + 1], pf, vf[2], vf[3]);
                 }
             }
             slot = slot + 1 == C::NST ? 0 : slot + 1;
         }
-        cp_wait<0>();
+        if constexpr (!E4M3) cp_wait<0>();
+        if constexpr (E4M3) {
+            if (!ok) {   // copies that were issued must land before the memory is used otherwise
+                const uint64_t d0 = global_timer_ns();
+                while (global_timer_ns() - d0 < 2000000ull) {
+                }
+            }
+            // O is in units of 2^E
+            const float f = e_ref <= -1000 ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 + e_ref) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] *= f;
+        }
 
         // ---- the four warps' results into one: m, l and o of each warp through shared memory
 #pragma unroll
@@ -490,7 +658,12 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 if (d == 0) p.part_lse[part * PR_ROWS + r] = lse;
             }
         }
-        __syncthreads();
+        if constexpr (E4M3) {
+            asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // the merge's accesses, before TMA writes there
+            if (__syncthreads_or(!ok)) return;
+        } else {
+            __syncthreads();
+        }
         unit += tile1 - tile0;
         rem += tile1 - tile0;
         if (rem >= static_cast<long long>(units) * p.c.Hkv) {
@@ -500,40 +673,48 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
     }
 }
 
-// Puts together the pairs that several CTAs of paged_rows_kernel worked on: one block per
-// (sequence, key head).  CTA c's part is slot 2c where the pair's tiles reach its run's
-// start from an earlier CTA, 2c + 1 where the pair begins in its run.
+// Puts together the pairs that several CTAs of paged_rows_kernel worked on.  Block c looks at the
+// border between the runs of CTAs c and c + 1; the first border inside a pair does the pair.
+// CTA c's part is slot 2c where the pair's tiles reach its run's start from an earlier CTA,
+// 2c + 1 where the pair begins in its run.  Launched beside the main kernel: what precedes
+// the wait runs under it.
 template <int D>
 __global__ void __launch_bounds__(PR_THREADS) paged_rows_combine_kernel(const PagedParams p, const int n_ctas) {
     __shared__ long long s_sum[PR_WARPS];
     __shared__ long long s_first;
-    __shared__ int s_units;
-    const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x - b * p.c.Hkv;
+    __shared__ int s_units, s_b;
     const int tid = threadIdx.x;
-    if (tid == 0) s_units = 0;
     const RowsDeal deal = rows_deal(p, n_ctas, s_sum, false);
-    rows_scan(p, s_sum, [&](int bb, long long, long long) { return bb == b; },
-              [&](int, long long lo, int n) {
+    const long long border = (blockIdx.x + 1) * deal.per;
+    if (tid == 0) s_units = 0;
+    rows_scan(p, s_sum, [&](int, long long lo, long long hi) { return lo * p.c.Hkv <= border && border < hi * p.c.Hkv; },
+              [&](int b, long long lo, int n) {
+                  s_b = b;
                   s_first = lo;
                   s_units = n;
               });
-    const int units = s_units;
-    if (units == 0) return;
-    const long long u0 = s_first * p.c.Hkv + static_cast<long long>(h) * units;
+    wait_for_main_kernel();   // every block, so that this grid never ends before that one
+    const int units = s_units, b = s_b;
+    if (units == 0) return;   // no unit behind the border
+    const long long rem = border - s_first * p.c.Hkv;
+    const int h = static_cast<int>(rem / units);
+    const long long u0 = border - (rem - static_cast<long long>(h) * units);
     const long long c0 = u0 / deal.per, c1 = (u0 + units - 1) / deal.per;
-    if (c0 == c1) return;   // one CTA had it whole
+    if (u0 == border || c0 != blockIdx.x) return;
     const QueryRange qr = query_range(p, b, false);
     const int rows = min(qr.n, p.max_q) * p.G;
     auto slot = [&](long long c) { return 2 * c + (c == c0 ? 1 : 0); };
     for (int idx = tid; idx < rows * (D / 4); idx += PR_THREADS) {
         const int r = idx / (D / 4), d = idx % (D / 4) * 4;
         float M = -INFINITY;
-        for (long long c = c0; c <= c1; ++c) M = fmaxf(M, __ldg(p.part_lse + slot(c) * PR_ROWS + r));
+#pragma unroll 4
+        for (long long c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_lse + slot(c) * PR_ROWS + r));
         float s = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
         for (long long c = c0; c <= c1; ++c) {
-            const float lc = __ldg(p.part_lse + slot(c) * PR_ROWS + r);
+            const float lc = __ldcg(p.part_lse + slot(c) * PR_ROWS + r);
             const float w = lc == -INFINITY ? 0.0f : expf(lc - M);
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p.part_out + (slot(c) * PR_ROWS + r) * D + d));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_out + (slot(c) * PR_ROWS + r) * D + d));
             s += w;
             acc[0] += w * v.x;
             acc[1] += w * v.y;

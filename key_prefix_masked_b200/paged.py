@@ -28,28 +28,46 @@ _OPERAND = struct.Struct("3P2i6q")      # attn_rope_operand
 _STRIDES = struct.Struct("3q")          # attn_strides
 
 
+_functions = {}
+# The current stream's handle by device index.  The public accessor builds a Stream object
+# on every call (2 us); this one is what generated torch code uses.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(name, device, *args):
     """The library's function `name` on the device's current stream, with that device current."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, stream)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib(), name)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream)
-    _check(st, name)
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _check(st, name)
+
+
+def _new(shape, strides, dtype, device):
+    """An uninitialised tensor (empty_strided skips a microsecond of torch.empty's argument handling)."""
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
 def _strides4(t, name):
     """(page or batch, head, row) strides of a [*, H, T, D] view; a dim of size 1 gets a stride that
     is never used but passes the checks."""
-    if t.stride(3) != 1 and t.shape[3] != 1:
-        raise ValueError(f"{name}: the head dim must be contiguous (stride 1)")
     B, H, T, D = t.shape
-    b, h, s, _ = t.stride()
-    s = D if T == 1 else s
-    h = T * D if H == 1 else h
-    b = H * T * D if B == 1 else b
+    b, h, s, d = t.stride()
+    if d != 1 and D != 1:
+        raise ValueError(f"{name}: the head dim must be contiguous (stride 1)")
+    if T == 1:
+        s = D
+    if H == 1:
+        h = T * D
+    if B == 1:
+        b = H * T * D
     if s == 0:
         raise ValueError(f"{name}: rows may not be broadcast")
     return b, h, s
@@ -57,12 +75,14 @@ def _strides4(t, name):
 
 def _strides3(t, name):
     """(0, head, token) strides of a [T, H, D] view."""
-    if t.stride(2) != 1 and t.shape[2] != 1:
-        raise ValueError(f"{name}: the head dim must be contiguous (stride 1)")
     T, H, D = t.shape
-    s, h, _ = t.stride()
-    s = H * D if T == 1 else s
-    h = D if H == 1 else h
+    s, h, d = t.stride()
+    if d != 1 and D != 1:
+        raise ValueError(f"{name}: the head dim must be contiguous (stride 1)")
+    if T == 1:
+        s = H * D
+    if H == 1:
+        h = D
     if s == 0:
         raise ValueError(f"{name}: rows may not be broadcast")
     return 0, h, s
@@ -74,7 +94,7 @@ def _bf16(t, dim, name):
 
 
 def _int32(t, shape, name, device):
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
 
 
@@ -123,23 +143,27 @@ def rope_inv_freq(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_c
     return f.to(device), attn_factor
 
 
-def _operand(x, y, weight, name):
-    if weight is not None:
-        if (weight.dtype not in (torch.bfloat16, torch.float32) or weight.device != x.device
-                or tuple(weight.shape) != (x.shape[-1],) or not weight.is_contiguous()):
-            raise ValueError(f"{name}_weight must be a contiguous bf16 or fp32 tensor [D] on {x.device}")
-    st = _strides4 if x.dim() == 4 else _strides3
-    return _OPERAND.pack(x.data_ptr(), y.data_ptr(), 0 if weight is None else weight.data_ptr(), x.shape[-3 if x.dim() == 4 else -2],
-                         0 if weight is None else weight.dtype == torch.float32, *st(x, name), *st(y, name + "_out"))
-
-
-def _rope_out(x, out, name):
+def _operand(x, out, weight, name):
+    """(output, packed attn_rope_operand) of one operand; makes the output where none is given."""
+    shape, dev = x.shape, x.device
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise ValueError(f"{name}_out must be a bf16 tensor of {name}'s shape on {x.device}")
-    _not_overlapping(out, name + "_out")
-    return out
+        *lead, n, D = shape
+        strides = (n * D, D, 1) if len(shape) == 3 else (lead[1] * n * D, n * D, D, 1)
+        out = _new(shape, strides, torch.bfloat16, dev)
+    else:
+        if out.shape != shape or out.dtype != torch.bfloat16 or out.device != dev:
+            raise ValueError(f"{name}_out must be a bf16 tensor of {name}'s shape on {dev}")
+        _not_overlapping(out, name + "_out")
+    w = 0
+    fp32 = False
+    if weight is not None:
+        fp32 = weight.dtype == torch.float32
+        if (not (fp32 or weight.dtype == torch.bfloat16) or weight.device != dev or weight.shape != shape[-1:]
+                or not weight.is_contiguous()):
+            raise ValueError(f"{name}_weight must be a contiguous bf16 or fp32 tensor [D] on {dev}")
+        w = weight.data_ptr()
+    st = _strides4 if len(shape) == 4 else _strides3
+    return out, _OPERAND.pack(x.data_ptr(), out.data_ptr(), w, shape[1], fp32, *st(x, name), *st(out, name + "_out"))
 
 
 def attn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -166,12 +190,10 @@ def attn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, e
             raise ValueError("k must have q's tokens, head dim and device")
     if q.numel() == 0 or (k is not None and k.numel() == 0):
         raise ValueError("q and k may not be empty")
-    q_out = _rope_out(q, q_out, "q")
-    op_q = _operand(q, q_out, q_weight, "q")
+    q_out, op_q = _operand(q, q_out, q_weight, "q")
     op_k = None
     if k is not None:
-        k_out = _rope_out(k, k_out, "k")
-        op_k = _operand(k, k_out, k_weight, "k")
+        k_out, op_k = _operand(k, k_out, k_weight, "k")
     _call("attn_qk_norm_rope", q.device, op_q, op_k, positions.data_ptr() if R else None,
           inv_freq.data_ptr() if R else None, B, T, D, R, bool(interleaved), eps, attn_factor)
     return q_out, k_out if k is not None else None
@@ -246,7 +268,8 @@ def attn_cache_read(k_cache, v_cache, block_table, kv_len, Tk=None, k_scale=None
         if k_out is not None or v_out is not None:
             raise ValueError("k_out and v_out are given together")
         shape = (B, H, n * page if Tk is None else int(Tk), D)
-        k_out, v_out = (torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) for _ in range(2))
+        strides = (H * shape[2] * D, shape[2] * D, D, 1)
+        k_out, v_out = (_new(shape, strides, torch.bfloat16, k_cache.device) for _ in range(2))
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if (t.dim() != 4 or t.shape[:2] != (B, H) or t.shape[3] != D or t.dtype != torch.bfloat16
                 or t.device != k_cache.device or t.shape != k_out.shape or Tk not in (None, t.shape[2])):
@@ -286,23 +309,26 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q
     elif T != B:
         raise ValueError("without q_start, q must have one row per sequence")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = _new((T, Hq, D), (Hq * D, D, 1), torch.bfloat16, dev)
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev:
         raise ValueError("out must be a bf16 tensor of q's shape on q's device")
     else:
         _not_overlapping(out, "out")
     if lse is not None:
-        if tuple(lse.shape) != (T, Hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+        if lse.shape != (T, Hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 tensor [T, Hq] on q's device")
     elif need_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = _new((T, Hq), (Hq, 1), torch.float32, dev)
     if T == 0:
         return out, lse
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    scale = D ** -0.5 if scale is None else scale
     max_q = 1 if q_start is None else T if max_q is None else int(max_q)
-    need = lib().attn_paged_workspace_bytes(B, T, Hq, Hkv, D, page, n, max_q)
+    bytes_of = _functions.get("attn_paged_workspace_bytes")
+    if bytes_of is None:
+        bytes_of = _functions["attn_paged_workspace_bytes"] = lib().attn_paged_workspace_bytes
+    need = bytes_of(B, T, Hq, Hkv, D, page, n, max_q)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _new((need,), (1,), torch.uint8, dev)
     elif need and (workspace.device != dev or not workspace.is_contiguous()
                    or workspace.numel() * workspace.element_size() < need):
         raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {need} bytes")
