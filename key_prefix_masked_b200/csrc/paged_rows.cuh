@@ -111,10 +111,16 @@ __device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint32_t (&a)[
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 codes (low 16 bits) to two f16 values, exactly.
-__device__ __forceinline__ uint32_t codes_f16(uint16_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+// The two e4m3 codes in the low or the high half of w as two f16 values, exactly.
+__device__ __forceinline__ uint32_t codes_f16_lo(uint32_t w) {
+    uint32_t d;
+    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(d) : "r"(w));
+    return d;
+}
+__device__ __forceinline__ uint32_t codes_f16_hi(uint32_t w) {
+    uint32_t d;
+    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, hi;\n}\n" : "=r"(d) : "r"(w));
+    return d;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -221,6 +227,16 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
     // e4m3: this warp's barriers and scale bytes
     const uint32_t bars = smem_u32(smem) + C::AREA + warp * C::NST * 8;
     uint8_t* const scales = smem + C::AREA + C::BARS + warp * C::NST * 32;
+    // e4m3: where this lane's 16 (8) bytes of keys r8 and r8 + 8 begin in a K tile, and its 4 bytes of rows
+    // 2 q4, + 1, + 8, + 9 in a V tile.  The swizzle only flips address bits, so further chunks
+    // of the row are an exclusive or away.
+    uint32_t k_off[2], v_off[4];
+    if constexpr (E4M3) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) k_off[n] = D >= 64 ? rows_swizzle<D, true>(8 * n + r8, q4) : rows_swizzle<D, true>(8 * n + r8, q4 >> 1) + (q4 & 1) * 8;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v_off[k] = rows_swizzle<D, true>(2 * q4 + (k & 1) + 8 * (k >> 1), r8 >> 2) + (r8 & 3) * 4;
+    }
     uint32_t item = 0;       // e4m3: tiles consumed, over all segments
     bool ok = true;          // e4m3: no wait has run out
     if constexpr (E4M3) {
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             const int key = t * PR_TK + warp * PR_WK + (lane & 1) * 8;
             int page = -1;
             if (t < tile1 && key < kv) {
-                page = __ldg(table + key / p.c.page_size);
+                page = __ldg(table + page_index(p, key));
                 if (page < 0 || page >= p.c.num_pages) {
                     if (lane < 2) atomicOr(&g_paged_status, STATUS_CACHE);
                     page = -1;
@@ -375,7 +391,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             if constexpr (!E4M3) cp_commit();
         }
         int slot = E4M3 ? static_cast<int>(item % C::NST) : 0;
-        int e_ref = -1000;       // e4m3: E, the largest scale exponent of a value row so far
+        int e_ref = -1000;       // e4m3: E + 127, the largest scale code of a value row so far
 #pragma unroll 1
         for (int t = tile0; t < tile1; ++t) {
             __syncwarp();   // every lane is done with the slot that is filled next
@@ -402,49 +418,42 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
             float ks[2][2];          // e4m3: 2^e of keys 2 q4, +1 (and + 8)
-            int ve[2][2];            // e4m3: e of their value rows
+            uint32_t vc = 0u;        // e4m3: the scale codes of their value rows, a byte each
+            bool odd_codes = false;  // a scale code of NaN in the tile
             if constexpr (E4M3) {
                 const uint8_t* sc = scales + slot * 32;
-                const uint8_t* kp = smem + (kb - smem_u32(smem));
+                const uint32_t kc = *reinterpret_cast<const uint16_t*>(sc + 2 * q4) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sc + 8 + 2 * q4)) << 16;
+                vc = *reinterpret_cast<const uint16_t*>(sc + 16 + 2 * q4) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sc + 24 + 2 * q4)) << 16;
                 if (key0 + PR_WK > kv) {
-                    // value rows of a page behind the sequence hold anything, NaN codes included
+                    // rows of a page behind the sequence hold anything: value codes of NaN, scale bytes
                     const int left = max(0, kv - key0);
                     for (int x = lane; x < (PR_WK - left) * C::CPR; x += 32)
                         *reinterpret_cast<uint4*>(smem + (vb - smem_u32(smem)) + rows_swizzle<D, true>(left + x / C::CPR, x % C::CPR)) = make_uint4(0u, 0u, 0u, 0u);
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // before TMA writes there again
                     __syncwarp();
-                }
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint32_t k2 = *reinterpret_cast<const uint16_t*>(sc + 8 * n + 2 * q4);
-                    const uint32_t v2 = *reinterpret_cast<const uint16_t*>(sc + 16 + 8 * n + 2 * q4);
-                    ks[n][0] = scale_value(k2 & 255u);
-                    ks[n][1] = scale_value(k2 >> 8);
-                    ve[n][0] = static_cast<int>(v2 & 255u) - 127;
-                    ve[n][1] = static_cast<int>(v2 >> 8) - 127;
-                    if (key0 + PR_WK > kv) {   // so do the scale bytes
-                        const int left = kv - (key0 + 8 * n + 2 * q4);
-                        if (left < 1) ve[n][0] = -1000;
-                        if (left < 2) ve[n][1] = -1000;
-                    }
+                    for (int b2 = 0; b2 < 4; ++b2)
+                        if (2 * q4 + (b2 & 1) + 8 * (b2 >> 1) >= left) vc &= ~(255u << 8 * b2);
+                }
+                odd_codes = __any_sync(0xffffffffu, __vcmpeq4(kc, 0xffffffffu) | __vcmpeq4(vc, 0xffffffffu));
+#pragma unroll
+                for (int b2 = 0; b2 < 4; ++b2) {
+                    const uint32_t code = (kc >> 8 * b2) & 255u;
+                    ks[b2 >> 1][b2 & 1] = odd_codes ? scale_value(code) : __uint_as_float(code << 23);
                 }
                 constexpr int RUN = D >= 64 ? 16 : 8;
 #pragma unroll
                 for (int c = 0; c < D / (RUN * 4); ++c) {
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        const int r = 8 * n + r8;
                         uint32_t w[RUN / 4];
-                        if constexpr (RUN == 16) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(kp + rows_swizzle<D, true>(r, c * 4 + q4));
-                            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-                        } else {
-                            const uint2 x = *reinterpret_cast<const uint2*>(kp + rows_swizzle<D, true>(r, q4 >> 1) + (q4 & 1) * 8);
-                            w[0] = x.x; w[1] = x.y;
-                        }
+                        const uint32_t at = kb + (D == 256 ? (c >> 1) * C::BLOCK : 0) + (k_off[n] ^ ((D == 256 ? c & 1 : c) << 6));
+                        if constexpr (RUN == 16)
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+                        else
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
 #pragma unroll
-                        for (int e = 0; e < RUN / 4; ++e)
-                            mma16816_f16(s[n], qf[c * (RUN / 4) + e], codes_f16(static_cast<uint16_t>(w[e])), codes_f16(static_cast<uint16_t>(w[e] >> 16)));
+                        for (int e = 0; e < RUN / 4; ++e) mma16816_f16(s[n], qf[c * (RUN / 4) + e], codes_f16_lo(w[e]), codes_f16_hi(w[e]));
                     }
                 }
             } else {
@@ -498,50 +507,48 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 }
             // ---- O += P V
             if constexpr (E4M3) {
-                // E over the tile's rows (128: a NaN row, left to its weight)
-                int top = -1000, low = 1000;
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int b2 = 0; b2 < 2; ++b2) {
-                        if (ve[n][b2] < 128) top = max(top, ve[n][b2]);
-                        if (ve[n][b2] > -1000) low = min(low, ve[n][b2]);
-                    }
-                top = __reduce_max_sync(0xffffffffu, top);
-                low = __reduce_min_sync(0xffffffffu, low);
-                if (top > e_ref) {
-                    const float f = top - e_ref > 126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - (top - e_ref)) << 23);
-                    e_ref = top;
+                // E over the tile's rows.  Codes of NaN do not count (their weights become NaN), nor do rows
+                // that are not there (code 0 above).
+                uint32_t c4 = vc;
+                if (odd_codes) c4 &= ~__vcmpeq4(vc, 0xffffffffu);
+                uint32_t top = __vmaxu4(c4, c4 >> 16);
+                top = __reduce_max_sync(0xffffffffu, max(top & 255u, (top >> 8) & 255u));
+                if (static_cast<int>(top) > e_ref) {
+                    const int up = static_cast<int>(top) - e_ref;
+                    const float f = up > 126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                    e_ref = static_cast<int>(top);
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[i][e] *= f;
                 }
-                // 2^(e - E): of the f16 weights, or (wide) of the bf16 values
-                float vm[2][2];
+                // 2^(e - E) multiplies the f16 weights, or (wide) the bf16 values
+                bool far = false;
+                int de[4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int b2 = 0; b2 < 2; ++b2)
-                        vm[n][b2] = ve[n][b2] == 128 ? __uint_as_float(0x7fc00000u)
-                                                     : __uint_as_float(static_cast<uint32_t>(max(127 + ve[n][b2] - e_ref, 0)) << 23);
-                const uint8_t* v = smem + (vb - smem_u32(smem));
-                const bool wide = low < e_ref - 12;
+                for (int b2 = 0; b2 < 4; ++b2) {
+                    de[b2] = static_cast<int>((c4 >> 8 * b2) & 255u) - e_ref;
+                    far |= de[b2] < -12;
+                }
+                // (rows that are not there ask for the wide form too: a sequence's last tile)
+                const bool wide = __any_sync(0xffffffffu, far);
                 uint32_t vsc[2] = {0u, 0u};
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
+                    float vm[2];
                     if (wide) {
-                        // 2^(120 + e - E); the weights keep only a row's NaN
-                        uint32_t f2[2];
-#pragma unroll
-                        for (int b2 = 0; b2 < 2; ++b2) {
-                            f2[b2] = static_cast<uint32_t>(min(max(247 + ve[n][b2] - e_ref, 0), 247)) << 7;
-                            if (ve[n][b2] != 128) vm[n][b2] = 1.0f;
-                        }
-                        vsc[n] = f2[0] | f2[1] << 16;
+                        vm[0] = vm[1] = 1.0f;
+                        vsc[n] = static_cast<uint32_t>(max(247 + de[2 * n], 0)) << 7 | static_cast<uint32_t>(max(247 + de[2 * n + 1], 0)) << 23;
+                    } else {
+                        vm[0] = __uint_as_float(static_cast<uint32_t>(127 + de[2 * n]) << 23);
+                        vm[1] = __uint_as_float(static_cast<uint32_t>(127 + de[2 * n + 1]) << 23);
+                    }
+                    if (odd_codes) {
+                        if (((vc >> 16 * n) & 255u) == SCALE_NAN) vm[0] = __uint_as_float(0x7fc00000u);
+                        if (((vc >> (16 * n + 8)) & 255u) == SCALE_NAN) vm[1] = __uint_as_float(0x7fc00000u);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) wt[n][e] *= vm[n][e & 1];
+                    for (int e = 0; e < 4; ++e) wt[n][e] *= vm[e & 1];
                     pf[2 * n] = wide ? pack_bf16(wt[n][0], wt[n][1]) : pack_f16(wt[n][0], wt[n][1]);
                     pf[2 * n + 1] = wide ? pack_bf16(wt[n][2], wt[n][3]) : pack_f16(wt[n][2], wt[n][3]);
                 }
@@ -550,18 +557,16 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                     for (int g = 0; g < D / 32; ++g) {
                         uint32_t w[4];   // keys 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9: dims 32 g + 4 r8 + {0..3}
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int r = 2 * q4 + (k & 1) + 8 * (k >> 1);
-                            w[k] = *reinterpret_cast<const uint32_t*>(v + rows_swizzle<D, true>(r, 2 * g + (r8 >> 2)) + (r8 & 3) * 4);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[k]) : "r"(vb + (D == 256 ? (g >> 2) * C::BLOCK : 0) + (v_off[k] ^ ((D == 256 ? g & 3 : g) << 5))));
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if constexpr (decltype(is_wide)::value)
                                 mma16816(o[4 * g + e], pf, widen2(__byte_perm(w[0], w[1], e << 4 | (4 + e) << 12), vsc[0]),
                                          widen2(__byte_perm(w[2], w[3], e << 4 | (4 + e) << 12), vsc[1]));
                             else
-                                mma16816_f16(o[4 * g + e], pf, codes_f16(static_cast<uint16_t>(__byte_perm(w[0], w[1], e | (4 + e) << 4))),
-                                             codes_f16(static_cast<uint16_t>(__byte_perm(w[2], w[3], e | (4 + e) << 4))));
+                                mma16816_f16(o[4 * g + e], pf, codes_f16_lo(__byte_perm(w[0], w[1], e | (4 + e) << 4)),
+                                             codes_f16_lo(__byte_perm(w[2], w[3], e | (4 + e) << 4)));
                         }
                     }
                 };
@@ -591,7 +596,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 }
             }
             // O is in units of 2^E
-            const float f = e_ref <= -1000 ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 + e_ref) << 23);
+            const float f = e_ref <= -1000 ? 1.0f : __uint_as_float(static_cast<uint32_t>(e_ref) << 23);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
 #pragma unroll
