@@ -55,6 +55,7 @@ struct PagedParams {
     float* part_lse;
     int B, T, Hq, G, max_q, kv_cap, causal;
     int min_units;                      // least tiles that a CTA takes
+    int tile_keys;                      // paged_rows.cuh: keys per tile
     int page_shift;                     // log2(page_size), -1 if it is no power of two
     int tpt, box_rows;                  // paged_chunk.cuh: tokens per row tile, rows per copied box
     int head_units[2];                  // and a head's distance in column blocks (k, v)
@@ -233,8 +234,8 @@ constexpr int SM_COUNT = 148;   // B200
 // CTAs of the few-row kernel: every resident slot, or fewer where the largest possible work
 // (every sequence of kv_cap keys) needs fewer.
 constexpr int ROWS_MIN_UNITS = 2;
-int rows_ctas(int per_sm, int B, int Hkv, long long kv_cap) {
-    const long long units = static_cast<long long>(B) * Hkv * ((kv_cap + PR_TK - 1) / PR_TK);
+int rows_ctas(int per_sm, int tile_keys, int B, int Hkv, long long kv_cap) {
+    const long long units = static_cast<long long>(B) * Hkv * ((kv_cap + tile_keys - 1) / tile_keys);
     const long long most = (units + ROWS_MIN_UNITS - 1) / ROWS_MIN_UNITS;
     return static_cast<int>(most < SM_COUNT * per_sm ? most : SM_COUNT * per_sm);
 }
@@ -262,8 +263,9 @@ attn_status launch_combine(void (*kern)(PagedParams, int), dim3 grid, int thread
 template <int D, bool E4M3>
 attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
     using C = RowsCfg<D, E4M3>;
-    const int n = rows_ctas(C::PER_SM, p.B, p.c.Hkv, p.kv_cap);
+    const int n = rows_ctas(C::PER_SM, C::TK, p.B, p.c.Hkv, p.kv_cap);
     p.min_units = ROWS_MIN_UNITS;
+    p.tile_keys = C::TK;
     p.part_out = static_cast<float*>(workspace);
     p.part_lse = p.part_out + 2LL * n * PR_ROWS * D;
     if (cudaFuncSetAttribute(paged_rows_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
@@ -273,7 +275,8 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
     CUtensorMap mk, mv;
     memset(&mk, 0, sizeof mk);
     mv = mk;
-    p.box_rows = (p.c.page_size & 15) == 0 ? 16 : 8;
+    p.box_rows = p.c.page_size & -p.c.page_size;
+    if (p.box_rows > C::WK) p.box_rows = C::WK;
     for (int i = 0; E4M3 && i < 2; ++i) {
         const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.c.page_size), static_cast<cuuint64_t>(p.c.Hkv),
                                     static_cast<cuuint64_t>(p.c.num_pages)};
@@ -472,7 +475,7 @@ size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page
     if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || D <= 0 || page_size <= 0 || max_pages <= 0 || max_q <= 0)
         return 0;
     if (few_rows(max_q < T ? max_q : T, Hq / Hkv))
-        return 2ull * rows_ctas(2, B, Hkv, static_cast<long long>(max_pages) * page_size) * PR_ROWS * (D + 1) * sizeof(float);
+        return 2ull * rows_ctas(2, RowsCfg<32, false>::TK, B, Hkv, static_cast<long long>(max_pages) * page_size) * PR_ROWS * (D + 1) * sizeof(float);
     return 512ull * chunk_runs(B, Hkv, Hq / Hkv, D, max_q < T ? max_q : T, static_cast<long long>(max_pages) * page_size) * (D + 1) * sizeof(float);
 }
 

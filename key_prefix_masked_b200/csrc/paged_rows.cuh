@@ -31,26 +31,27 @@
 
 constexpr int PR_THREADS = 128;
 constexpr int PR_WARPS = 4;
-constexpr int PR_WK = 16;                  // keys per warp and tile
-constexpr int PR_TK = PR_WARPS * PR_WK;    // keys per tile
 constexpr int PR_ROWS = 16;                // query rows per CTA
 
 template <int D, bool E4M3>
 struct RowsCfg {
+    // Keys per warp and tile: what a tile costs besides its keys (waits, copies, votes) is most of an
+    // e4m3 tile of 16 keys (528 instructions at D = 128).
+    static constexpr int WK = !E4M3 || D == 256 ? 16 : D == 128 ? 32 : 64, TK = PR_WARPS * WK, NT = WK / 8;
     static constexpr int ROW = D * (E4M3 ? 1 : 2);      // bytes of one row
     static constexpr int CPR = ROW / 16;                // 16-byte chunks per row
-    static constexpr int HALF = PR_WK * ROW;            // K or V part of a stage
+    static constexpr int HALF = WK * ROW;            // K or V part of a stage
     static constexpr int STAGE = 2 * HALF;
     // e4m3: the swizzle span that TMA applies to a row (128 bytes at most: column blocks at D = 256)
     static constexpr int SW = ROW < 128 ? ROW : 128;
-    static constexpr int BLOCK = PR_WK * SW;            // a column block of 16 rows
+    static constexpr int BLOCK = WK * SW;               // a column block of a tile
     // about 96 KB of rings per CTA (two CTAs per SM), 192 KB where a stage is 16 KB (one)
     static constexpr int NST_RAW = 24576 / (2 * HALF);
     static constexpr int NST = NST_RAW < 3 ? 3 : NST_RAW > 8 ? 8 : NST_RAW;
     static constexpr int RING = PR_WARPS * NST * STAGE;
     static constexpr int MERGE = PR_WARPS * PR_ROWS * (D + 4) * 4;   // reuses the ring
-    // e4m3, behind the ring: each warp's barriers, and 16 K and 16 V scale bytes per stage
-    static constexpr int BARS = E4M3 ? PR_WARPS * NST * 8 : 0, SCALES = E4M3 ? PR_WARPS * NST * 32 : 0;
+    // e4m3, behind the ring: each warp's barriers, and the K and V scale bytes of each stage
+    static constexpr int BARS = E4M3 ? PR_WARPS * NST * 8 : 0, SCALES = E4M3 ? PR_WARPS * NST * 2 * WK : 0;
     static constexpr int AREA = (RING > MERGE ? RING : MERGE) + 127 & ~127;
     static constexpr int SMEM = AREA + BARS + SCALES;
     static constexpr int PER_SM = SMEM > 110 * 1024 ? 1 : 2;
@@ -58,7 +59,7 @@ struct RowsCfg {
 
 // Byte offset of 16-byte chunk c of row r in a stage's K or V part.  bf16: ldmatrix takes one
 // chunk of 8 rows, and the permutation puts those into different banks.  e4m3: what TMA's
-// swizzle of SW bytes makes of 16-row column blocks; the reads of V (4 bytes of rows 2 q4, q4 = 0..3)
+// swizzle of SW bytes makes of column blocks; the reads of V (4 bytes of rows 2 q4, q4 = 0..3)
 // then touch every bank once, those of K (16 bytes a lane, two rows to a quarter warp) twice.
 template <int D, bool E4M3>
 __device__ __forceinline__ uint32_t rows_swizzle(int r, int c) {
@@ -152,7 +153,7 @@ __device__ __forceinline__ int rows_units(const PagedParams& p, int b, bool repo
     const int n = query_range(p, b, report).n;
     const int kv = paged_kv_len(p.kv_len, b, p.kv_cap, report);
     if (n == 0) return 0;
-    return max(1, (kv + PR_TK - 1) / PR_TK);
+    return max(1, (kv + p.tile_keys - 1) / p.tile_keys);
 }
 
 // The deal: `total` units per key head over the batch, `per` of all heads' units to a CTA.
@@ -226,22 +227,22 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
     const uint32_t ring = smem_u32(smem) + warp * C::NST * C::STAGE;
     // e4m3: this warp's barriers and scale bytes
     const uint32_t bars = smem_u32(smem) + C::AREA + warp * C::NST * 8;
-    uint8_t* const scales = smem + C::AREA + C::BARS + warp * C::NST * 32;
-    // e4m3: where this lane's 16 (8) bytes of keys r8 and r8 + 8 begin in a K tile, and its 4 bytes of rows
-    // 2 q4, + 1, + 8, + 9 in a V tile.  The swizzle only flips address bits, so further chunks
+    uint8_t* const scales = smem + C::AREA + C::BARS + warp * C::NST * 2 * C::WK;
+    // e4m3: where this lane's 16 (8) bytes of keys r8, r8 + 8, ... begin in a K tile, and its 4 bytes of
+    // rows 2 q4, + 1, + 8, + 9, ... in a V tile.  The swizzle only flips address bits, so further chunks
     // of the row are an exclusive or away.
-    uint32_t k_off[2], v_off[4];
+    uint32_t k_off[C::NT], v_off[C::NT * 2];
     if constexpr (E4M3) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) k_off[n] = D >= 64 ? rows_swizzle<D, true>(8 * n + r8, q4) : rows_swizzle<D, true>(8 * n + r8, q4 >> 1) + (q4 & 1) * 8;
+        for (int n = 0; n < C::NT; ++n) k_off[n] = D >= 64 ? rows_swizzle<D, true>(8 * n + r8, q4) : rows_swizzle<D, true>(8 * n + r8, q4 >> 1) + (q4 & 1) * 8;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v_off[k] = rows_swizzle<D, true>(2 * q4 + (k & 1) + 8 * (k >> 1), r8 >> 2) + (r8 & 3) * 4;
+        for (int k = 0; k < 2 * C::NT; ++k) v_off[k] = rows_swizzle<D, true>(2 * q4 + (k & 1) + 8 * (k >> 1), r8 >> 2) + (r8 & 3) * 4;
     }
     uint32_t item = 0;       // e4m3: tiles consumed, over all segments
     bool ok = true;          // e4m3: no wait has run out
     if constexpr (E4M3) {
         if (lane == 0) {
-            for (int s = 0; s < C::NST; ++s) mbar_init(bars + 8 * s, 5);   // the byte count's arrival and four scale copies'
+            for (int s = 0; s < C::NST; ++s) mbar_init(bars + 8 * s, 1 + C::WK / 4);   // the byte count's arrival and the scale copies'
             fence_mbar_init();
         }
         __syncwarp();
@@ -311,13 +312,13 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
 
         // ---- loads: this warp's 16 keys of tile t; two 8-key groups, each within one page
         const int32_t* table = p.table + b * p.table_stride;
-        auto page_of = [&](int t) {   // lanes 0, 1: the page of the group, -1: none
-            const int key = t * PR_TK + warp * PR_WK + (lane & 1) * 8;
+        auto page_of = [&](int t) {   // lane g < WK / 8: the page of the 8-key group, -1: none
+            const int key = t * C::TK + warp * C::WK + (lane & (C::WK / 8 - 1)) * 8;
             int page = -1;
             if (t < tile1 && key < kv) {
                 page = __ldg(table + page_index(p, key));
                 if (page < 0 || page >= p.c.num_pages) {
-                    if (lane < 2) atomicOr(&g_paged_status, STATUS_CACHE);
+                    if (lane < C::WK / 8) atomicOr(&g_paged_status, STATUS_CACHE);
                     page = -1;
                 }
             }
@@ -326,35 +327,30 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
         auto load = [&](int t, int page_l, int slot) {
           if constexpr (E4M3) {
             const uint32_t dst = ring + slot * C::STAGE, bar = bars + 8 * slot;
-            const int key0 = t * PR_TK + warp * PR_WK;
-            const int pg0 = __shfl_sync(0xffffffffu, page_l, 0), pg1 = __shfl_sync(0xffffffffu, page_l, 1);
-            const int row0 = key0 - page_index(p, key0) * p.c.page_size, row1 = key0 + 8 - page_index(p, key0 + 8) * p.c.page_size;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, C::STAGE);
-                // 16 rows lie in one page unless it ends in between: pages of 8 or an odd number of 8 rows
-                const bool one = p.box_rows == 16;
+            const int key0 = t * C::TK + warp * C::WK;
+            const int g_l = lane & (C::WK / 8 - 1);        // this lane's 8-row group
+            const int row_l = key0 + 8 * g_l - page_index(p, key0 + 8 * g_l) * p.c.page_size;
+            // box g (box_rows rows, all in one page) by the lane that looked its first group up
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::STAGE);
+            __syncwarp();
+            if (lane < C::WK / 8 && (lane * 8 & (p.box_rows - 1)) == 0) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (g == 1 && one) break;
-                    const int pg = g ? pg1 : pg0;
+                for (int b2 = 0; b2 < C::ROW / C::SW; ++b2)
 #pragma unroll
-                    for (int b2 = 0; b2 < C::ROW / C::SW; ++b2)
-#pragma unroll
-                        for (int w = 0; w < 2; ++w)
-                            tma_load_4d(dst + w * C::HALF + b2 * C::BLOCK + g * 8 * C::SW, w ? &tm_v : &tm_k, b2 * C::SW, g ? row1 : row0, h,
-                                        pg < 0 ? p.c.num_pages : pg, bar);
-                }
+                    for (int w = 0; w < 2; ++w)
+                        tma_load_4d(dst + w * C::HALF + b2 * C::BLOCK + lane * 8 * C::SW, w ? &tm_v : &tm_k, b2 * C::SW, row_l, h,
+                                    page_l < 0 ? p.c.num_pages : page_l, bar);
             }
-            if (lane < 4) {      // scale bytes: K and V (lane / 2) of each 8-row group (lane % 2)
-                const int pg = lane & 1 ? pg1 : pg0;
-                const uint8_t* src = p.c.scale[lane >> 1];
-                if (pg >= 0) src += (static_cast<long long>(pg) * p.c.Hkv + h) * p.c.page_size + (lane & 1 ? row1 : row0);
-                cp_async8(smem_u32(scales) + slot * 32 + 16 * (lane >> 1) + 8 * (lane & 1), src, pg >= 0);
+            if (lane < C::WK / 4) {      // scale bytes: K, then V, of each 8-row group
+                const int w = lane / (C::WK / 8);
+                const uint8_t* src = p.c.scale[w];
+                if (page_l >= 0) src += (static_cast<long long>(page_l) * p.c.Hkv + h) * p.c.page_size + row_l;
+                cp_async8(smem_u32(scales) + slot * 2 * C::WK + 8 * lane, src, page_l >= 0);
                 cp_async_mbar_arrive_noinc(bar);
             }
           } else {
             const uint32_t dst = ring + slot * C::STAGE;
-            const int key0 = t * PR_TK + warp * PR_WK;
+            const int key0 = t * C::TK + warp * C::WK;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const int page = __shfl_sync(0xffffffffu, page_l, g);
@@ -411,41 +407,52 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 __syncwarp();
             }
             const uint32_t kb = ring + slot * C::STAGE, vb = kb + C::HALF;
-            const int key0 = t * PR_TK + warp * PR_WK;
-            float s[2][4];
+            const int key0 = t * C::TK + warp * C::WK;
+            float s[C::NT][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < C::NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-            float ks[2][2];          // e4m3: 2^e of keys 2 q4, +1 (and + 8)
-            uint32_t vc = 0u;        // e4m3: the scale codes of their value rows, a byte each
+            float ks[C::NT][2];      // e4m3: 2^e of keys 8 n + 2 q4, + 1
+            uint32_t vc[C::NT / 2];  // e4m3: the scale codes of the value rows, a byte each: tiles 2 i, 2 i + 1
             bool odd_codes = false;  // a scale code of NaN in the tile
             if constexpr (E4M3) {
-                const uint8_t* sc = scales + slot * 32;
-                const uint32_t kc = *reinterpret_cast<const uint16_t*>(sc + 2 * q4) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sc + 8 + 2 * q4)) << 16;
-                vc = *reinterpret_cast<const uint16_t*>(sc + 16 + 2 * q4) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sc + 24 + 2 * q4)) << 16;
-                if (key0 + PR_WK > kv) {
+                const uint8_t* sc = scales + slot * 2 * C::WK + 2 * q4;
+                uint32_t kc[C::NT / 2];
+                bool odd = false;
+#pragma unroll
+                for (int i = 0; i < C::NT / 2; ++i) {
+                    kc[i] = *reinterpret_cast<const uint16_t*>(sc + 16 * i) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sc + 16 * i + 8)) << 16;
+                    vc[i] = *reinterpret_cast<const uint16_t*>(sc + C::WK + 16 * i) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sc + C::WK + 16 * i + 8)) << 16;
+                }
+                if (key0 + C::WK > kv) {
                     // rows of a page behind the sequence hold anything: value codes of NaN, scale bytes
                     const int left = max(0, kv - key0);
-                    for (int x = lane; x < (PR_WK - left) * C::CPR; x += 32)
+                    for (int x = lane; x < (C::WK - left) * C::CPR; x += 32)
                         *reinterpret_cast<uint4*>(smem + (vb - smem_u32(smem)) + rows_swizzle<D, true>(left + x / C::CPR, x % C::CPR)) = make_uint4(0u, 0u, 0u, 0u);
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // before TMA writes there again
                     __syncwarp();
 #pragma unroll
-                    for (int b2 = 0; b2 < 4; ++b2)
-                        if (2 * q4 + (b2 & 1) + 8 * (b2 >> 1) >= left) vc &= ~(255u << 8 * b2);
-                }
-                odd_codes = __any_sync(0xffffffffu, __vcmpeq4(kc, 0xffffffffu) | __vcmpeq4(vc, 0xffffffffu));
+                    for (int i = 0; i < C::NT / 2; ++i)
 #pragma unroll
-                for (int b2 = 0; b2 < 4; ++b2) {
-                    const uint32_t code = (kc >> 8 * b2) & 255u;
-                    ks[b2 >> 1][b2 & 1] = odd_codes ? scale_value(code) : __uint_as_float(code << 23);
+                        for (int b2 = 0; b2 < 4; ++b2)
+                            if (16 * i + 2 * q4 + (b2 & 1) + 8 * (b2 >> 1) >= left) vc[i] &= ~(255u << 8 * b2);
                 }
+#pragma unroll
+                for (int i = 0; i < C::NT / 2; ++i) odd |= (__vcmpeq4(kc[i], 0xffffffffu) | __vcmpeq4(vc[i], 0xffffffffu)) != 0u;
+                odd_codes = __any_sync(0xffffffffu, odd);
+#pragma unroll
+                for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                    for (int b2 = 0; b2 < 2; ++b2) {
+                        const uint32_t code = (kc[n >> 1] >> (16 * (n & 1) + 8 * b2)) & 255u;
+                        ks[n][b2] = odd_codes ? scale_value(code) : __uint_as_float(code << 23);
+                    }
                 constexpr int RUN = D >= 64 ? 16 : 8;
 #pragma unroll
                 for (int c = 0; c < D / (RUN * 4); ++c) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int n = 0; n < C::NT; ++n) {
                         uint32_t w[RUN / 4];
                         const uint32_t at = kb + (D == 256 ? (c >> 1) * C::BLOCK : 0) + (k_off[n] ^ ((D == 256 ? c & 1 : c) << 6));
                         if constexpr (RUN == 16)
@@ -466,11 +473,11 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 }
             }
             // ---- scores in the log2 domain, masked by selection
-            float x[2][4];
-            const bool masked = key0 + PR_WK > all_seen;   // uniform
+            float x[C::NT][4];
+            const bool masked = key0 + C::WK > all_seen;   // uniform
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < C::NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float y = s[n][e] * row_mul[e >> 1];
@@ -495,11 +502,11 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                     }
                 }
             }
-            uint32_t pf[4];
+            uint32_t pf[C::NT / 2][4];   // A fragments of 16 keys each
             const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
-            float wt[2][4];
+            float wt[C::NT][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < C::NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     wt[n][e] = exp2_approx(x[n][e] - (e < 2 ? m0 : m1));
@@ -509,9 +516,13 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             if constexpr (E4M3) {
                 // E over the tile's rows.  Codes of NaN do not count (their weights become NaN), nor do rows
                 // that are not there (code 0 above).
-                uint32_t c4 = vc;
-                if (odd_codes) c4 &= ~__vcmpeq4(vc, 0xffffffffu);
-                uint32_t top = __vmaxu4(c4, c4 >> 16);
+                uint32_t c4[C::NT / 2], top = 0u;
+#pragma unroll
+                for (int i = 0; i < C::NT / 2; ++i) {
+                    c4[i] = odd_codes ? vc[i] & ~__vcmpeq4(vc[i], 0xffffffffu) : vc[i];
+                    top = __vmaxu4(top, c4[i]);
+                }
+                top = __vmaxu4(top, top >> 16);
                 top = __reduce_max_sync(0xffffffffu, max(top & 255u, (top >> 8) & 255u));
                 if (static_cast<int>(top) > e_ref) {
                     const int up = static_cast<int>(top) - e_ref;
@@ -524,49 +535,59 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 }
                 // 2^(e - E) multiplies the f16 weights, or (wide) the bf16 values
                 bool far = false;
-                int de[4];
+                int de[C::NT][2];
 #pragma unroll
-                for (int b2 = 0; b2 < 4; ++b2) {
-                    de[b2] = static_cast<int>((c4 >> 8 * b2) & 255u) - e_ref;
-                    far |= de[b2] < -12;
-                }
+                for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                    for (int b2 = 0; b2 < 2; ++b2) {
+                        de[n][b2] = static_cast<int>((c4[n >> 1] >> (16 * (n & 1) + 8 * b2)) & 255u) - e_ref;
+                        far |= de[n][b2] < -12;
+                    }
                 // (rows that are not there ask for the wide form too: a sequence's last tile)
                 const bool wide = __any_sync(0xffffffffu, far);
-                uint32_t vsc[2] = {0u, 0u};
+                uint32_t vsc[C::NT];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < C::NT; ++n) {
                     float vm[2];
+                    vsc[n] = 0u;
                     if (wide) {
                         vm[0] = vm[1] = 1.0f;
-                        vsc[n] = static_cast<uint32_t>(max(247 + de[2 * n], 0)) << 7 | static_cast<uint32_t>(max(247 + de[2 * n + 1], 0)) << 23;
+                        vsc[n] = static_cast<uint32_t>(max(247 + de[n][0], 0)) << 7 | static_cast<uint32_t>(max(247 + de[n][1], 0)) << 23;
                     } else {
-                        vm[0] = __uint_as_float(static_cast<uint32_t>(127 + de[2 * n]) << 23);
-                        vm[1] = __uint_as_float(static_cast<uint32_t>(127 + de[2 * n + 1]) << 23);
+                        vm[0] = __uint_as_float(static_cast<uint32_t>(127 + de[n][0]) << 23);
+                        vm[1] = __uint_as_float(static_cast<uint32_t>(127 + de[n][1]) << 23);
                     }
                     if (odd_codes) {
-                        if (((vc >> 16 * n) & 255u) == SCALE_NAN) vm[0] = __uint_as_float(0x7fc00000u);
-                        if (((vc >> (16 * n + 8)) & 255u) == SCALE_NAN) vm[1] = __uint_as_float(0x7fc00000u);
+#pragma unroll
+                        for (int b2 = 0; b2 < 2; ++b2)
+                            if (((vc[n >> 1] >> (16 * (n & 1) + 8 * b2)) & 255u) == SCALE_NAN) vm[b2] = __uint_as_float(0x7fc00000u);
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) wt[n][e] *= vm[e & 1];
-                    pf[2 * n] = wide ? pack_bf16(wt[n][0], wt[n][1]) : pack_f16(wt[n][0], wt[n][1]);
-                    pf[2 * n + 1] = wide ? pack_bf16(wt[n][2], wt[n][3]) : pack_f16(wt[n][2], wt[n][3]);
+                    uint32_t(&pw)[4] = pf[n >> 1];
+                    pw[2 * (n & 1)] = wide ? pack_bf16(wt[n][0], wt[n][1]) : pack_f16(wt[n][0], wt[n][1]);
+                    pw[2 * (n & 1) + 1] = wide ? pack_bf16(wt[n][2], wt[n][3]) : pack_f16(wt[n][2], wt[n][3]);
                 }
                 auto pv = [&](auto is_wide) {
 #pragma unroll
                     for (int g = 0; g < D / 32; ++g) {
-                        uint32_t w[4];   // keys 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9: dims 32 g + 4 r8 + {0..3}
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[k]) : "r"(vb + (D == 256 ? (g >> 2) * C::BLOCK : 0) + (v_off[k] ^ ((D == 256 ? g & 3 : g) << 5))));
+                        for (int i = 0; i < C::NT / 2; ++i) {
+                            uint32_t w[4];   // keys 16 i + 2 q4, + 1, + 8, + 9: dims 32 g + 4 r8 + {0..3}
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if constexpr (decltype(is_wide)::value)
-                                mma16816(o[4 * g + e], pf, widen2(__byte_perm(w[0], w[1], e << 4 | (4 + e) << 12), vsc[0]),
-                                         widen2(__byte_perm(w[2], w[3], e << 4 | (4 + e) << 12), vsc[1]));
-                            else
-                                mma16816_f16(o[4 * g + e], pf, codes_f16_lo(__byte_perm(w[0], w[1], e | (4 + e) << 4)),
-                                             codes_f16_lo(__byte_perm(w[2], w[3], e | (4 + e) << 4)));
+                            for (int k = 0; k < 4; ++k)
+                                asm volatile("ld.shared.b32 %0, [%1];"
+                                             : "=r"(w[k])
+                                             : "r"(vb + (D == 256 ? (g >> 2) * C::BLOCK : 0) + (v_off[4 * i + k] ^ ((D == 256 ? g & 3 : g) << 5))));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if constexpr (decltype(is_wide)::value)
+                                    mma16816(o[4 * g + e], pf[i], widen2(__byte_perm(w[0], w[1], e << 4 | (4 + e) << 12), vsc[2 * i]),
+                                             widen2(__byte_perm(w[2], w[3], e << 4 | (4 + e) << 12), vsc[2 * i + 1]));
+                                else
+                                    mma16816_f16(o[4 * g + e], pf[i], codes_f16_lo(__byte_perm(w[0], w[1], e | (4 + e) << 4)),
+                                                 codes_f16_lo(__byte_perm(w[2], w[3], e | (4 + e) << 4)));
+                            }
                         }
                     }
                 };
@@ -575,15 +596,15 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             } else {
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    pf[2 * n] = pack_bf16(wt[n][0], wt[n][1]);
-                    pf[2 * n + 1] = pack_bf16(wt[n][2], wt[n][3]);
+                    pf[0][2 * n] = pack_bf16(wt[n][0], wt[n][1]);
+                    pf[0][2 * n + 1] = pack_bf16(wt[n][2], wt[n][3]);
                 }
 #pragma unroll
                 for (int st = 0; st < D / 16; ++st) {
                     uint32_t vf[4];   // dims 0-7: keys 0-7, 8-15; dims 8-15: keys 0-7, 8-15
                     ldsm4_trans(vb + rows_swizzle<D, false>(lane & 15, st * 2 + (lane >> 4)), vf);
-                    mma16816(o[2 * st], pf, vf[0], vf[1]);
-                    mma16816(o[2 * st + 1], pf, vf[2], vf[3]);
+                    mma16816(o[2 * st], pf[0], vf[0], vf[1]);
+                    mma16816(o[2 * st + 1], pf[0], vf[2], vf[3]);
                 }
             }
             slot = slot + 1 == C::NST ? 0 : slot + 1;
