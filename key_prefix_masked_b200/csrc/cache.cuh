@@ -10,12 +10,12 @@
 // the top binade of e4m3 fully, but a floating-point code gains no precision from that, and
 // each reader would round once more.
 //
-// Both kernels are copies: HBM bounds them.  A lane moves 8 elements (16 bytes of bf16, 8
-// bytes of codes) and has several rows in flight.
+// Both kernels are copies: HBM bounds them.  A lane moves 8 elements (16 bytes of bf16; 16
+// codes, 32 bytes of bf16, where codes are read) and has several rows in flight.
 
 constexpr int CACHE_THREADS = 256;
-constexpr int CACHE_WRITE_U = 2;      // rows in flight per thread
-constexpr int CACHE_READ_U = 4;       // (K and V each)
+constexpr int CACHE_WRITE_U = 4;      // rows in flight per thread
+constexpr int CACHE_READ_U = 2;       // (K and V each)
 constexpr int SCALE_EXP_MIN = -117, SCALE_EXP_MAX = 120;
 constexpr int SCALE_NAN = 255;
 
@@ -40,14 +40,15 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
     const int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7fu) > 96u ? 1 : 0);
     return static_cast<uint32_t>(min(max(e, SCALE_EXP_MIN), SCALE_EXP_MAX) + 127);
 }
-// Eight bf16 values (four words) to eight e4m3 codes of magnitude <= top; inv = 2^-e.
-__device__ __forceinline__ uint2 quantise8(const uint4& x, float inv, float top) {
+// Eight bf16 values (four words) to eight e4m3 codes; inv = 2^-e.  `last`: e = 120, where codes
+// end at 240 (below that exponent none exceeds 448).
+__device__ __forceinline__ uint2 quantise8(const uint4& x, float inv, bool last) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = make_float2(fminf(fmaxf(__uint_as_float(w[i] << 16) * inv, -top), top),
-                                     fminf(fmaxf(__uint_as_float(w[i] & 0xffff0000u) * inv, -top), top));
+        float2 f = mul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), make_float2(inv, inv));
+        if (last) f = make_float2(fminf(fmaxf(f.x, -240.0f), 240.0f), fminf(fmaxf(f.y, -240.0f), 240.0f));
         h[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
     }
     return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
@@ -68,61 +69,66 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
 struct CacheWriteParams {
     CacheView c;
     const __nv_bfloat16* src[2];
-    long long st[2], sh[2];   // element strides of the new rows: token, head
+    long long st[2], sh[2];     // element strides of the new rows: token, head
     const int32_t* slots;
-    long long rows;           // T * 2 * Hkv: (token, k or v, head), head fastest
+    int page_shift;             // log2(page_size), -1 if it is no power of two
+    int parts, rows_per_part;   // warps per token, and of its 2 Hkv rows (k heads, v heads) each
+    long long tasks;            // tokens * parts
 };
 
+// A warp takes a token's rows (or a part of them), so the slot is looked up and taken apart once.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheWriteParams p) {
     constexpr int LPR = D / 8;
-    constexpr int RPI = CACHE_THREADS / LPR;
-    const int lane = threadIdx.x % LPR;
-    const long long r0 = static_cast<long long>(blockIdx.x) * (RPI * CACHE_WRITE_U) + threadIdx.x / LPR;
-    const int per_token = 2 * p.c.Hkv;
-    uint4 x[CACHE_WRITE_U];
-    int slot[CACHE_WRITE_U], kv[CACHE_WRITE_U], head[CACHE_WRITE_U];
+    constexpr int RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, l = lane % LPR;
+    const long long task = static_cast<long long>(blockIdx.x) * (CACHE_THREADS / 32) + (threadIdx.x >> 5);
+    if (task >= p.tasks) return;
+    const long long t = task / p.parts;
+    const int begin = static_cast<int>(task - t * p.parts) * p.rows_per_part, end = min(2 * p.c.Hkv, begin + p.rows_per_part);
+    const int slot = __ldg(p.slots + t);
+    if (slot < 0) return;
+    if (slot >= p.c.num_pages * p.c.page_size) {
+        if (lane == 0) atomicOr(&g_paged_status, STATUS_CACHE);
+        return;
+    }
+    const int page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.c.page_size, row = slot - page * p.c.page_size;
+#pragma unroll 1
+    for (int r0 = begin + lane / LPR; r0 - lane / LPR < end; r0 += CACHE_WRITE_U * RPW) {
+        uint4 x[CACHE_WRITE_U];
 #pragma unroll
-    for (int u = 0; u < CACHE_WRITE_U; ++u) {
-        const long long r = r0 + u * RPI;
-        x[u] = make_uint4(0u, 0u, 0u, 0u);
-        slot[u] = -1;
-        if (r < p.rows) {
-            const long long t = r / per_token;
-            const int rest = static_cast<int>(r - t * per_token);
-            kv[u] = rest >= p.c.Hkv;
-            head[u] = kv[u] ? rest - p.c.Hkv : rest;
-            x[u] = __ldg(reinterpret_cast<const uint4*>(p.src[kv[u]] + t * p.st[kv[u]] + head[u] * p.sh[kv[u]]) + lane);
-            slot[u] = __ldg(p.slots + t);
-            if (slot[u] >= p.c.num_pages * p.c.page_size) {
-                if (lane == 0) atomicOr(&g_paged_status, STATUS_CACHE);
-                slot[u] = -1;
+        for (int u = 0; u < CACHE_WRITE_U; ++u) {
+            const int r = r0 + u * RPW;
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < end) {
+                const int w = r >= p.c.Hkv;
+                x[u] = __ldg(reinterpret_cast<const uint4*>(p.src[w] + t * p.st[w] + (w ? r - p.c.Hkv : r) * p.sh[w]) + l);
             }
         }
-    }
 #pragma unroll
-    for (int u = 0; u < CACHE_WRITE_U; ++u) {
-        uint32_t code = 0u;
-        if constexpr (E4M3) {
-            // largest magnitude of the row, as bf16 patterns (ordered like the numbers, NaN on top)
-            uint32_t m = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
-                                  __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
+        for (int u = 0; u < CACHE_WRITE_U; ++u) {
+            const int r = r0 + u * RPW;
+            uint32_t code = 0u;
+            if constexpr (E4M3) {
+                // largest magnitude of the row, as bf16 patterns (ordered like the numbers, NaN on top)
+                uint32_t m = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu),
+                                      __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
 #pragma unroll
-            for (int k = LPR / 2; k > 0; k >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, k));
-            code = scale_code(max(m & 0xffffu, m >> 16));
-        }
-        if (slot[u] < 0) continue;
-        const int page = slot[u] / p.c.page_size, row = slot[u] - page * p.c.page_size;
-        uint8_t* dst = p.c.data[kv[u]] + page * p.c.sp[kv[u]] + head[u] * p.c.sh[kv[u]] + row * p.c.st[kv[u]];
-        if constexpr (E4M3) {
-            uint2 q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN
-            if (code != SCALE_NAN) q = quantise8(x[u], __uint_as_float((254u - code) << 23), code == SCALE_EXP_MAX + 127 ? 240.0f : 448.0f);
-            reinterpret_cast<uint2*>(dst)[lane] = q;
-            if (lane == 0)
-                p.c.scale[kv[u]][(static_cast<long long>(page) * p.c.Hkv + head[u]) * p.c.page_size + row] =
-                    static_cast<uint8_t>(code);
-        } else {
-            reinterpret_cast<uint4*>(dst)[lane] = x[u];
+                for (int k = LPR / 2; k > 0; k >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, k));
+                code = scale_code(max(m & 0xffffu, m >> 16));
+            }
+            if (r >= end) continue;
+            const int w = r >= p.c.Hkv, head = w ? r - p.c.Hkv : r;
+            uint8_t* dst = p.c.data[w] + page * p.c.sp[w] + head * p.c.sh[w] + row * p.c.st[w];
+            if constexpr (E4M3) {
+                uint2 q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN
+                if (code != SCALE_NAN) q = quantise8(x[u], __uint_as_float((254u - code) << 23), code == SCALE_EXP_MAX + 127);
+                reinterpret_cast<uint2*>(dst)[l] = q;
+                if (l == 0)
+                    p.c.scale[w][(static_cast<long long>(page) * p.c.Hkv + head) * p.c.page_size + row] = static_cast<uint8_t>(code);
+            } else {
+                reinterpret_cast<uint4*>(dst)[l] = x[u];
+            }
         }
     }
 }
@@ -135,12 +141,14 @@ struct CacheReadParams {
     long long table_stride;
     const int32_t* kv_len;
     int max_pages, Tk, n_rb;         // row blocks per (b, h)
+    int page_shift;                  // log2(page_size), -1 if it is no power of two
 };
 
 // One block: rows [rb * RPI * U, ...) of element b, head h, K and V.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheReadParams p) {
-    constexpr int LPR = D / 8;
+    constexpr int PER = E4M3 ? 16 : 8;        // elements per lane: 16 bytes loaded
+    constexpr int LPR = D / PER;
     constexpr int RPI = CACHE_THREADS / LPR;
     const int lane = threadIdx.x % LPR;
     const int rb = static_cast<int>(blockIdx.x % p.n_rb);
@@ -149,19 +157,19 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
     const int kv = paged_kv_len(p.kv_len, b, static_cast<int>(min(static_cast<long long>(p.Tk),
                                 static_cast<long long>(p.max_pages) * p.c.page_size)), rb == 0 && h == 0);
     const long long j0 = static_cast<long long>(rb) * (RPI * CACHE_READ_U) + threadIdx.x / LPR;
-    using Raw = typename std::conditional<E4M3, uint2, uint4>::type;
-    Raw x[CACHE_READ_U][2];
-    float sc[CACHE_READ_U][2];
+    uint4 x[CACHE_READ_U][2];
+    uint32_t sc[CACHE_READ_U][2];
 #pragma unroll
     for (int u = 0; u < CACHE_READ_U; ++u) {
         const long long j = j0 + u * RPI;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            x[u][w] = Raw{};
-            sc[u][w] = 0.0f;
+            x[u][w] = make_uint4(0u, 0u, 0u, 0u);
+            sc[u][w] = 0u;
         }
         if (j >= kv) continue;
-        const int pj = static_cast<int>(j) / p.c.page_size, row = static_cast<int>(j) - pj * p.c.page_size;
+        const int pj = p.page_shift >= 0 ? static_cast<int>(j) >> p.page_shift : static_cast<int>(j) / p.c.page_size;
+        const int row = static_cast<int>(j) - pj * p.c.page_size;
         const int page = __ldg(p.table + b * p.table_stride + pj);
         if (page < 0 || page >= p.c.num_pages) {
             if (lane == 0) atomicOr(&g_paged_status, STATUS_CACHE);
@@ -169,9 +177,8 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
         }
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            x[u][w] = __ldg(reinterpret_cast<const Raw*>(p.c.data[w] + page * p.c.sp[w] + h * p.c.sh[w] + row * p.c.st[w]) + lane);
-            if constexpr (E4M3)
-                sc[u][w] = scale_value(__ldg(p.c.scale[w] + (static_cast<long long>(page) * p.c.Hkv + h) * p.c.page_size + row));
+            x[u][w] = __ldg(reinterpret_cast<const uint4*>(p.c.data[w] + page * p.c.sp[w] + h * p.c.sh[w] + row * p.c.st[w]) + lane);
+            if constexpr (E4M3) sc[u][w] = __ldg(p.c.scale[w] + (static_cast<long long>(page) * p.c.Hkv + h) * p.c.page_size + row);
         }
     }
 #pragma unroll
@@ -180,10 +187,14 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_read_kernel(const CacheRe
         if (j >= kv) continue;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            uint4 o;
-            if constexpr (E4M3) o = dequantise8(x[u][w], sc[u][w]);
-            else o = x[u][w];
-            reinterpret_cast<uint4*>(p.dst[w] + b * p.sb[w] + h * p.sh[w] + j * p.st[w])[lane] = o;
+            uint4* dst = reinterpret_cast<uint4*>(p.dst[w] + b * p.sb[w] + h * p.sh[w] + j * p.st[w]);
+            if constexpr (E4M3) {
+                const float f = scale_value(sc[u][w]);
+                dst[2 * lane] = dequantise8(make_uint2(x[u][w].x, x[u][w].y), f);
+                dst[2 * lane + 1] = dequantise8(make_uint2(x[u][w].z, x[u][w].w), f);
+            } else {
+                dst[lane] = x[u][w];
+            }
         }
     }
 }

@@ -152,12 +152,19 @@ bool token_strides_of(const attn_strides* s, int H, int D, Strides* out) {
     *out = {0, static_cast<long long>(s->h), static_cast<long long>(s->t)};
     return true;
 }
+// log2 of a page size that is a power of two, -1 otherwise
+int page_shift(int page_size) {
+    if ((page_size & (page_size - 1)) != 0) return -1;
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
 bool head_dim_ok(int D) { return D == 32 || D == 64 || D == 128 || D == 256; }
 
 attn_status cache_view(const attn_cache* c, CacheView* v) {
     if (c == nullptr || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return ATTN_ERR_INVALID_ARG;
     if (c->num_pages <= 0 || c->page_size <= 0 || c->Hkv <= 0) return ATTN_ERR_INVALID_ARG;
-    if (static_cast<long long>(c->num_pages) * c->page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(c->num_pages) * c->page_size > 0x7fffffffLL || c->Hkv > 65535) return ATTN_ERR_INVALID_ARG;
     if (c->format != ATTN_CACHE_BF16 && c->format != ATTN_CACHE_E4M3) return ATTN_ERR_UNSUPPORTED;
     if (!head_dim_ok(c->D) || (c->page_size & 7)) return ATTN_ERR_UNSUPPORTED;
     const bool e4m3 = c->format == ATTN_CACHE_E4M3;
@@ -186,30 +193,45 @@ attn_status cache_view(const attn_cache* c, CacheView* v) {
     return ATTN_OK;
 }
 
+constexpr int SM_COUNT = 148;   // B200
+
 attn_status launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
 template <int D>
 attn_status launch_rope(const RopeParams& prm, int mode, long long tokens, cudaStream_t stream) {
-    constexpr int RPI = ROPE_THREADS / (D / 8);
+    constexpr int RPW = 256 / D;   // rows per step of a warp
     RopeParams p = prm;
-    const int rows = p.op[0].H + p.op[1].H;
-    // Few tokens: their heads are spread over blocks until there are about four blocks per SM.
-    const int steps = (rows + RPI - 1) / RPI;
-    long long ny = tokens >= 592 ? 1 : 592 / tokens;
-    if (ny > steps) ny = steps;
-    if (ny > 65535) ny = 65535;
-    p.rows_per_y = static_cast<int>((steps + ny - 1) / ny) * RPI;
-    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>((rows + p.rows_per_y - 1) / p.rows_per_y));
-    if (mode == ROPE_INTERLEAVED) qk_norm_rope_kernel<D, ROPE_INTERLEAVED><<<grid, ROPE_THREADS, 0, stream>>>(p);
-    else if (mode == ROPE_HALF) qk_norm_rope_kernel<D, ROPE_HALF><<<grid, ROPE_THREADS, 0, stream>>>(p);
-    else qk_norm_rope_kernel<D, ROPE_HALF_SCALAR><<<grid, ROPE_THREADS, 0, stream>>>(p);
+    // Few tokens: their heads are spread over warps until there are eight per SM; many: a warp
+    // takes a token's heads, but at most 16 steps of them (the sines cost about as much as six).
+    const int steps = (p.op[0].H + p.op[1].H + RPW - 1) / RPW;
+    long long parts = (8LL * SM_COUNT + tokens - 1) / tokens;
+    if (parts < (steps + 15) / 16) parts = (steps + 15) / 16;
+    if (parts > steps) parts = steps;
+    p.rows_per_part = static_cast<int>((steps + parts - 1) / parts) * RPW;
+    p.parts = (p.op[0].H + p.op[1].H + p.rows_per_part - 1) / p.rows_per_part;
+    p.tasks = tokens * p.parts;
+    const long long grid = (p.tasks + ROPE_THREADS / 32 - 1) / (ROPE_THREADS / 32);
+    if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    const unsigned g = static_cast<unsigned>(grid);
+    if (mode == ROPE_INTERLEAVED) qk_norm_rope_kernel<D, ROPE_INTERLEAVED><<<g, ROPE_THREADS, 0, stream>>>(p);
+    else if (mode == ROPE_HALF) qk_norm_rope_kernel<D, ROPE_HALF><<<g, ROPE_THREADS, 0, stream>>>(p);
+    else qk_norm_rope_kernel<D, ROPE_HALF_SCALAR><<<g, ROPE_THREADS, 0, stream>>>(p);
     return launched();
 }
 
 template <int D>
-attn_status launch_write(const CacheWriteParams& p, cudaStream_t stream) {
-    constexpr int ROWS = CACHE_THREADS / (D / 8) * CACHE_WRITE_U;
-    const long long grid = (p.rows + ROWS - 1) / ROWS;
+attn_status launch_write(const CacheWriteParams& prm, long long tokens, cudaStream_t stream) {
+    constexpr int RPW = 256 / D;   // rows per step of a warp
+    CacheWriteParams p = prm;
+    p.page_shift = page_shift(p.c.page_size);
+    // few tokens: their rows are spread over warps until there are eight per SM
+    const int steps = (2 * p.c.Hkv + RPW - 1) / RPW;
+    long long parts = (8LL * SM_COUNT + tokens - 1) / tokens;
+    if (parts > steps) parts = steps;
+    p.rows_per_part = static_cast<int>((steps + parts - 1) / parts) * RPW;
+    p.parts = (2 * p.c.Hkv + p.rows_per_part - 1) / p.rows_per_part;
+    p.tasks = tokens * p.parts;
+    const long long grid = (p.tasks + CACHE_THREADS / 32 - 1) / (CACHE_THREADS / 32);
     if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     if (p.c.e4m3) cache_write_kernel<D, true><<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
     else cache_write_kernel<D, false><<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
@@ -218,8 +240,9 @@ attn_status launch_write(const CacheWriteParams& p, cudaStream_t stream) {
 
 template <int D>
 attn_status launch_read(const CacheReadParams& prm, int B, cudaStream_t stream) {
-    constexpr int ROWS = CACHE_THREADS / (D / 8) * CACHE_READ_U;
+    const int ROWS = CACHE_THREADS / (D / (prm.c.e4m3 ? 16 : 8)) * CACHE_READ_U;
     CacheReadParams p = prm;
+    p.page_shift = page_shift(p.c.page_size);
     const long long n_rb = (static_cast<long long>(p.Tk) + ROWS - 1) / ROWS;
     const long long grid = n_rb * B * p.c.Hkv;
     if (grid > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
@@ -228,8 +251,6 @@ attn_status launch_read(const CacheReadParams& prm, int B, cudaStream_t stream) 
     else cache_read_kernel<D, false><<<static_cast<unsigned>(grid), CACHE_THREADS, 0, stream>>>(p);
     return launched();
 }
-
-constexpr int SM_COUNT = 148;   // B200
 
 // CTAs of the few-row kernel: every resident slot, or fewer where the largest possible work
 // (every sequence of kv_cap keys) needs fewer.
@@ -433,8 +454,7 @@ attn_status attn_cache_write(const attn_cache* cache, const void* k, const void*
         p.sh[i] = s[i].h;
     }
     p.slots = slots;
-    p.rows = 2LL * T * cache->Hkv;
-#define CALL(DD) launch_write<DD>(p, stream)
+#define CALL(DD) launch_write<DD>(p, T, stream)
     ATTN_BY_HEAD_DIM(cache->D, CALL)
 #undef CALL
 }
@@ -521,9 +541,7 @@ attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_st
     p.max_q = rows_q;
     p.kv_cap = static_cast<int>(cap);
     p.causal = causal != 0;
-    p.page_shift = -1;
-    if ((cache->page_size & (cache->page_size - 1)) == 0)
-        for (p.page_shift = 0; (1 << p.page_shift) < cache->page_size;) ++p.page_shift;
+    p.page_shift = page_shift(cache->page_size);
     p.debug = g_debug.load(std::memory_order_relaxed);
     p.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     p.scale_log2 = scale * 1.44269504088896340736f;
