@@ -704,16 +704,27 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     const int left = w.kv - (j2 >> 1) * PC_BN;       // rows of the tile that exist
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * (8 * C::SW);
+                    // All of a thread's codes first: a load behind a store to shared memory would wait for it.
+                    uint4 d[X];
+                    uint32_t code[X];
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int r = x * RPX + r0;
-                        uint4 d = *reinterpret_cast<const uint4*>(src + r * D + c16 * 16);
-                        uint32_t code = src[PC_BN * D + r];
-                        if (r >= left) {                             // a page's rows behind the sequence
-                            d = make_uint4(0u, 0u, 0u, 0u);
-                            code = 127u;
-                        }
-                        store_codes(d, code, dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1);
+                        d[x] = *reinterpret_cast<const uint4*>(src + r * D + c16 * 16);
+                        code[x] = src[PC_BN * D + r];
+                    }
+                    if (left < PC_BN) {                              // a page's rows behind the sequence
+#pragma unroll
+                        for (int x = 0; x < X; ++x)
+                            if (x * RPX + r0 >= left) {
+                                d[x] = make_uint4(0u, 0u, 0u, 0u);
+                                code[x] = 127u;
+                            }
+                    }
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        const int r = x * RPX + r0;
+                        store_codes(d[x], code[x], dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();

@@ -458,16 +458,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     const int left = w.kv - j * PC_BN - (k ? rank * C::KH : 0);   // rows that exist
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * 1024;
+                    uint4 d[X];                          // all loads first, as in paged_chunk.cuh
+                    uint32_t code[X];
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int r = x * RPX + r0;
-                        uint4 d = *reinterpret_cast<const uint4*>(src + (r * CPR + c16) * 16);
-                        uint32_t code = src[C::SLOT / 2 + r];
-                        if (r >= left) {
-                            d = make_uint4(0u, 0u, 0u, 0u);
-                            code = 127u;
-                        }
-                        store_codes(d, code, dst + (r >> 3) * GROUP + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
+                        d[x] = *reinterpret_cast<const uint4*>(src + (r * CPR + c16) * 16);
+                        code[x] = src[C::SLOT / 2 + r];
+                    }
+                    if (left < 128 / (k ? 2 : 1)) {
+#pragma unroll
+                        for (int x = 0; x < X; ++x)
+                            if (x * RPX + r0 >= left) {
+                                d[x] = make_uint4(0u, 0u, 0u, 0u);
+                                code[x] = 127u;
+                            }
+                    }
+#pragma unroll
+                    for (int x = 0; x < X; ++x) {
+                        const int r = x * RPX + r0;
+                        store_codes(d[x], code[x], dst + (r >> 3) * GROUP + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();
