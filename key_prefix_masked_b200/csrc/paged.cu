@@ -41,6 +41,13 @@ __device__ __forceinline__ int paged_kv_len(const int32_t* kv_len, int b, int ca
 #include "rope.cuh"
 #include "cache.cuh"
 
+// What the combine kernels need of a run that begins inside a (sequence, key head, token tile):
+// n units, t0 of them in earlier runs of `per` units.  n = 0: the run begins at a border, or there is none.
+struct SharedAt {
+    int b, h, qt, t0, n, pad;
+    long long per;
+};
+
 struct PagedParams {
     CacheView c;
     const __nv_bfloat16* q;
@@ -53,6 +60,7 @@ struct PagedParams {
     const int32_t* q_start;             // null: one row per sequence
     float* part_out;                    // partial results of sequences shared by several CTAs
     float* part_lse;
+    SharedAt* shared;                   // by run
     int B, T, Hq, G, max_q, kv_cap, causal;
     int min_units;                      // least tiles that a CTA takes
     int tile_keys;                      // paged_rows.cuh: keys per tile
@@ -264,7 +272,7 @@ int rows_ctas(int per_sm, int tile_keys, int B, int Hkv, long long kv_cap) {
 bool few_rows(long long max_q, int G) { return max_q * G <= PR_ROWS; }
 
 // A combine kernel behind the main one, launched to overlap it (it waits on the device).
-attn_status launch_combine(void (*kern)(PagedParams, int), dim3 grid, int threads, cudaStream_t stream, const PagedParams& p, int n) {
+attn_status launch_combine(void (*kern)(PagedParams), dim3 grid, int threads, cudaStream_t stream, const PagedParams& p) {
     if (grid.x == 0) return launched();
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -277,7 +285,7 @@ attn_status launch_combine(void (*kern)(PagedParams, int), dim3 grid, int thread
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kern, p, n);
+    cudaLaunchKernelEx(&cfg, kern, p);
     return launched();
 }
 
@@ -289,6 +297,7 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
     p.tile_keys = C::TK;
     p.part_out = static_cast<float*>(workspace);
     p.part_lse = p.part_out + 2LL * n * PR_ROWS * D;
+    p.shared = reinterpret_cast<SharedAt*>(p.part_lse + 2LL * n * PR_ROWS);
     if (cudaFuncSetAttribute(paged_rows_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
@@ -308,7 +317,7 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
             return ATTN_ERR_CUDA;
     }
     paged_rows_kernel<D, E4M3><<<n, PR_THREADS, C::SMEM, stream>>>(mk, mv, p, n);
-    return launch_combine(paged_rows_combine_kernel<D>, dim3(n - 1), PR_THREADS, stream, p, n);
+    return launch_combine(paged_rows_combine_kernel<D>, dim3(n - 1), PR_THREADS, stream, p);
 }
 
 // Runs of the chunk kernels: one per SM (per CTA pair at head dim 256), or fewer where the
@@ -330,6 +339,7 @@ attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
     p.min_units = CHUNK_MIN_UNITS;
     p.part_out = static_cast<float*>(workspace);
     p.part_lse = p.part_out + 512LL * n * D;
+    p.shared = reinterpret_cast<SharedAt*>(p.part_lse + 512LL * n);
     p.tpt = 128 / p.G;
     p.box_rows = p.c.page_size & -p.c.page_size;   // the largest power of two that divides it
     const int most = PAIR ? 64 : PC_BN;
@@ -377,7 +387,7 @@ attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
         return ATTN_ERR_CUDA;
     }
     kern<<<grid, threads, smem, stream>>>(mq, mk, mv, p, n);
-    return launch_combine(paged_chunk_combine_kernel<D>, dim3(n - 1, 8), 128, stream, p, n);
+    return launch_combine(paged_chunk_combine_kernel<D>, dim3(n - 1, 8), 256, stream, p);
 }
 
 template <int D>
@@ -494,9 +504,11 @@ attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table,
 size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size, int max_pages, int max_q) {
     if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || D <= 0 || page_size <= 0 || max_pages <= 0 || max_q <= 0)
         return 0;
-    if (few_rows(max_q < T ? max_q : T, Hq / Hkv))
-        return 2ull * rows_ctas(2, RowsCfg<32, false>::TK, B, Hkv, static_cast<long long>(max_pages) * page_size) * PR_ROWS * (D + 1) * sizeof(float);
-    return 512ull * chunk_runs(B, Hkv, Hq / Hkv, D, max_q < T ? max_q : T, static_cast<long long>(max_pages) * page_size) * (D + 1) * sizeof(float);
+    const long long q = max_q < T ? max_q : T, cap = static_cast<long long>(max_pages) * page_size;
+    // per run: two parts of rows x (D + 1) floats, and a SharedAt (both multiples of 8 bytes)
+    if (few_rows(q, Hq / Hkv))
+        return rows_ctas(2, RowsCfg<32, false>::TK, B, Hkv, cap) * (2ull * PR_ROWS * (D + 1) * sizeof(float) + sizeof(SharedAt));
+    return chunk_runs(B, Hkv, Hq / Hkv, D, q, cap) * (512ull * (D + 1) * sizeof(float) + sizeof(SharedAt));
 }
 
 attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_strides* q_strides,

@@ -280,7 +280,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     long long at, all;
     const long long per = chunk_deal<C::THREADS>(p, n_ctas, blockIdx.x, s_scr, blockIdx.x == 0, &b_first, &at, &all);
     const long long unit0 = blockIdx.x * per;
-    if (unit0 >= all) return;
+    if (unit0 >= all) {
+        if (tid == 0) p.shared[blockIdx.x].n = 0;
+        return;
+    }
     const long long run = min(per, all - unit0);
 
     if (tid == 0) {
@@ -612,6 +615,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         uint32_t item = 0, qe_phase = 0;
         bool ok = true, first = true;
         const int boxes = PC_BN / p.box_rows;
+        w.begin(p, b_first, at, run);
+        if (lane == 0) p.shared[blockIdx.x] = {w.b, w.h, w.qt, w.t0, w.t0 > 0 ? w.c.n : 0, 0, per};
         constexpr int N = E4M3 ? C::NSTG : C::NS;          // the slots that are filled here
         constexpr int FULL = E4M3 ? PCB_SFULL : PCB_FULL, EMPTY = E4M3 ? PCB_SEMPTY : PCB_EMPTY;
         for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
@@ -747,50 +752,64 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
 }
 
 // Token tiles that several CTAs of paged_chunk_kernel shared.  Block c (x) looks at the border
-// between the runs of CTAs c and c + 1; the first border inside a tile puts the tile together,
-// its rows spread over blockIdx.y.  CTA c's part is slot 2c, or 2c + 1 where the tile begins in its run.
+// between the runs of CTAs c and c + 1; the first border inside a tile puts the tile together, its
+// rows spread over blockIdx.y, one warp a row.  CTA c's part is slot 2c, or 2c + 1 where the
+// tile begins in its run.
 template <int D>
-__global__ void __launch_bounds__(128) paged_chunk_combine_kernel(const PagedParams p, const int n_ctas) {
-    __shared__ long long s_scr[8];
-    int b;
-    long long at, all;
-    const long long c = blockIdx.x + 1;
-    const long long per = chunk_deal<128>(p, n_ctas, c, s_scr, false, &b, &at, &all);
+__global__ void __launch_bounds__(256) paged_chunk_combine_kernel(const PagedParams p) {
     wait_for_main_kernel();                     // every block, so that this grid never ends before that one
-    if (c * per >= all) return;
-    ChunkWalk w;
-    w.begin(p, b, at, all);
-    if (w.t0 == 0) return;                      // the border lies between two tiles
-    const long long u0 = c * per - w.t0;        // the tile's first unit
-    const long long c0 = u0 / per, c1 = (u0 + w.c.n - 1) / per;
-    if (c != c0 + 1) return;
+    const SharedAt s = p.shared[blockIdx.x + 1];
+    if (s.n == 0) return;                       // the border lies between two tiles
+    const long long u0 = (blockIdx.x + 1) * s.per - s.t0;   // the tile's first unit
+    const long long c0 = u0 / s.per, c1 = (u0 + s.n - 1) / s.per;
+    if (c0 != blockIdx.x) return;
+    const QueryRange qr = query_range(p, s.b, false);
+    const int n_live = min(qr.n, p.max_q), tok0 = s.qt * 2 * p.tpt;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int PER = D / 32;
-    for (int r = blockIdx.y * 4 + warp; r < 256; r += gridDim.y * 4) {
+    constexpr int V = D >= 128 ? 4 : D / 32, NV = D / (32 * V);   // floats per load, loads per lane
+    for (int r = blockIdx.y * 8 + warp; r < 256; r += gridDim.y * 8) {
         const int g = r >> 7, rr = r & 127, tok = rr / p.G;
-        if (tok >= w.c.ntok(g) || tok >= p.tpt) continue;
+        const int i = tok0 + g * p.tpt + tok;
+        if (tok >= p.tpt || i >= n_live) continue;
         auto slot = [&](long long cc) { return ((2 * cc + (cc == c0 ? 1 : 0)) * 2 + g) * 128 + rr; };
         float M = -INFINITY;
+#pragma unroll 4
         for (long long cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_lse + slot(cc)));
-        float s = 0.0f, acc[PER];
+        float sum = 0.0f, acc[NV * V];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = 0.0f;
+        for (int e = 0; e < NV * V; ++e) acc[e] = 0.0f;
+#pragma unroll 2
         for (long long cc = c0; cc <= c1; ++cc) {
             const float lc = __ldcg(p.part_lse + slot(cc));
             if (lc == -INFINITY) continue;      // nothing was stored
             const float wgt = expf(lc - M);
-            s += wgt;
-            const float* src = p.part_out + slot(cc) * D + lane * PER;
+            sum += wgt;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] += wgt * __ldcg(src + e);
+            for (int n = 0; n < NV; ++n) {
+                const float* src = p.part_out + slot(cc) * D + n * 32 * V + lane * V;
+                float v[V];
+                if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(src));
+                else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(src));
+                else v[0] = __ldcg(src);
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[n * V + e] += wgt * v[e];
+            }
         }
-        const bool some = !(s == 0.0f);
-        const float inv = some ? 1.0f / s : 0.0f;
-        const long long row = static_cast<long long>(w.q0) + w.c.tok(g) + tok;
-        const int hq = w.h * p.G + rr - tok * p.G;
-        __nv_bfloat16* dst = p.out + row * p.out_t + hq * p.out_h + lane * PER;
+        const bool some = !(sum == 0.0f);
+        const float inv = some ? 1.0f / sum : 0.0f;
+        const long long row = static_cast<long long>(qr.t0) + i;
+        const int hq = s.h * p.G + rr - tok * p.G;
+        __nv_bfloat16* dst = p.out + row * p.out_t + hq * p.out_h;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) dst[e] = __float2bfloat16_rn(acc[e] * inv);
-        if (lane == 0 && p.lse != nullptr) p.lse[row * p.Hq + hq] = some ? M + logf(s) : -INFINITY;
+        for (int n = 0; n < NV; ++n) {
+            __nv_bfloat16* d = dst + n * 32 * V + lane * V;
+            if constexpr (V == 4)
+                *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(acc[n * V] * inv, acc[n * V + 1] * inv), pack_bf16(acc[n * V + 2] * inv, acc[n * V + 3] * inv));
+            else if constexpr (V == 2)
+                *reinterpret_cast<uint32_t*>(d) = pack_bf16(acc[0] * inv, acc[1] * inv);
+            else
+                *d = __float2bfloat16_rn(acc[0] * inv);
+        }
+        if (lane == 0 && p.lse != nullptr) p.lse[row * p.Hq + hq] = some ? M + logf(sum) : -INFINITY;
     }
 }

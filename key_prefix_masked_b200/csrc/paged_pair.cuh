@@ -75,7 +75,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
     long long at, all;
     const long long per = chunk_deal<C::THREADS>(p, n_pairs, pair, s_scr, blockIdx.x == 0, &b_first, &at, &all);
     const long long unit0 = pair * per;
-    if (unit0 >= all) return;   // both CTAs of the pair
+    if (unit0 >= all) {         // both CTAs of the pair
+        if (leader && tid == 0) p.shared[pair].n = 0;
+        return;
+    }
     const long long run = min(per, all - unit0);
 
     if (tid == 0) {
@@ -330,6 +333,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         const uint32_t l_q = mapa_shared(PPBAR(PPB_QFULL), 0);
         uint32_t item = 0, qe_phase = 0;
         bool ok = true, first = true;
+        w.begin(p, b_first, at, run);
+        if (leader && lane == 0) p.shared[pair] = {w.b, w.h, w.qt, w.t0, w.t0 > 0 ? w.c.n : 0, 0, per};
         const int k_boxes = C::KH / p.box_rows, v_boxes = PC_BN / p.box_rows;   // box_rows <= 64
         for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
             const int je = max(w.end(0), w.end(1));

@@ -216,7 +216,10 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
     const long long all = deal.all(p.c.Hkv);
     long long unit = blockIdx.x * deal.per;
     const long long unit_end = min(all, unit + deal.per);
-    if (unit >= all) return;
+    if (unit >= all) {
+        if (tid == 0) p.shared[blockIdx.x].n = 0;
+        return;
+    }
     rows_scan(p, s_sum, [&](int, long long lo, long long hi) { return lo * p.c.Hkv <= unit && unit < hi * p.c.Hkv; },
               [&](int b, long long lo, int) {
                   s_b = b;
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
         const int h = static_cast<int>(rem / units);
         const int tile0 = static_cast<int>(rem - static_cast<long long>(h) * units);
         const int tile1 = static_cast<int>(min(static_cast<long long>(units), tile0 + (unit_end - unit)));
+        if (tid == 0 && unit == blockIdx.x * deal.per) p.shared[blockIdx.x] = {b, h, 0, tile0, tile0 > 0 ? units : 0, 0, deal.per};
         const QueryRange qr = query_range(p, b, false);
         const int kv = paged_kv_len(p.kv_len, b, p.kv_cap, false);
         const int rows = min(qr.n, p.max_q) * p.G;
@@ -702,31 +706,16 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
 // Puts together the pairs that several CTAs of paged_rows_kernel worked on.  Block c looks at the
 // border between the runs of CTAs c and c + 1; the first border inside a pair does the pair.
 // CTA c's part is slot 2c where the pair's tiles reach its run's start from an earlier CTA,
-// 2c + 1 where the pair begins in its run.  Launched beside the main kernel: what precedes
-// the wait runs under it.
+// 2c + 1 where the pair begins in its run.
 template <int D>
-__global__ void __launch_bounds__(PR_THREADS) paged_rows_combine_kernel(const PagedParams p, const int n_ctas) {
-    __shared__ long long s_sum[PR_WARPS];
-    __shared__ long long s_first;
-    __shared__ int s_units, s_b;
+__global__ void __launch_bounds__(PR_THREADS) paged_rows_combine_kernel(const PagedParams p) {
     const int tid = threadIdx.x;
-    const RowsDeal deal = rows_deal(p, n_ctas, s_sum, false);
-    const long long border = (blockIdx.x + 1) * deal.per;
-    if (tid == 0) s_units = 0;
-    rows_scan(p, s_sum, [&](int, long long lo, long long hi) { return lo * p.c.Hkv <= border && border < hi * p.c.Hkv; },
-              [&](int b, long long lo, int n) {
-                  s_b = b;
-                  s_first = lo;
-                  s_units = n;
-              });
     wait_for_main_kernel();   // every block, so that this grid never ends before that one
-    const int units = s_units, b = s_b;
-    if (units == 0) return;   // no unit behind the border
-    const long long rem = border - s_first * p.c.Hkv;
-    const int h = static_cast<int>(rem / units);
-    const long long u0 = border - (rem - static_cast<long long>(h) * units);
-    const long long c0 = u0 / deal.per, c1 = (u0 + units - 1) / deal.per;
-    if (u0 == border || c0 != blockIdx.x) return;
+    const SharedAt s = p.shared[blockIdx.x + 1];
+    if (s.n == 0) return;
+    const int b = s.b, h = s.h;
+    const long long u0 = (blockIdx.x + 1) * s.per - s.t0, c0 = u0 / s.per, c1 = (u0 + s.n - 1) / s.per;
+    if (c0 != blockIdx.x) return;
     const QueryRange qr = query_range(p, b, false);
     const int rows = min(qr.n, p.max_q) * p.G;
     auto slot = [&](long long c) { return 2 * c + (c == c0 ? 1 : 0); };
@@ -735,23 +724,23 @@ __global__ void __launch_bounds__(PR_THREADS) paged_rows_combine_kernel(const Pa
         float M = -INFINITY;
 #pragma unroll 4
         for (long long c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part_lse + slot(c) * PR_ROWS + r));
-        float s = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (long long c = c0; c <= c1; ++c) {
             const float lc = __ldcg(p.part_lse + slot(c) * PR_ROWS + r);
             const float w = lc == -INFINITY ? 0.0f : expf(lc - M);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_out + (slot(c) * PR_ROWS + r) * D + d));
-            s += w;
+            sum += w;
             acc[0] += w * v.x;
             acc[1] += w * v.y;
             acc[2] += w * v.z;
             acc[3] += w * v.w;
         }
-        const bool some = s != 0.0f;
-        const float inv = some ? 1.0f / s : 0.0f;
+        const bool some = sum != 0.0f;
+        const float inv = some ? 1.0f / sum : 0.0f;
         const int i = r / p.G, hq = h * p.G + r - i * p.G;
         *reinterpret_cast<uint2*>(p.out + (qr.t0 + i) * p.out_t + hq * p.out_h + d) =
             make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-        if (d == 0 && p.lse != nullptr) p.lse[static_cast<long long>(qr.t0 + i) * p.Hq + hq] = some ? M + logf(s) : -INFINITY;
+        if (d == 0 && p.lse != nullptr) p.lse[static_cast<long long>(qr.t0 + i) * p.Hq + hq] = some ? M + logf(sum) : -INFINITY;
     }
 }
