@@ -65,7 +65,7 @@ struct PagedParams {
     int min_units;                      // least tiles that a CTA takes
     int tile_keys;                      // paged_rows.cuh: keys per tile
     int page_shift;                     // log2(page_size), -1 if it is no power of two
-    int tpt, box_rows;                  // paged_chunk.cuh: tokens per row tile, rows per copied box
+    int tpt, box_rows, box_shift;       // paged_chunk.cuh: tokens per row tile, rows per copied box and their log2
     int head_units[2];                  // and a head's distance in column blocks (k, v)
     unsigned debug;
     unsigned long long wait_ns;
@@ -344,6 +344,7 @@ attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
     p.box_rows = p.c.page_size & -p.c.page_size;   // the largest power of two that divides it
     const int most = PAIR ? 64 : PC_BN;
     if (p.box_rows > most) p.box_rows = most;
+    p.box_shift = page_shift(p.box_rows);
     const CUtensorMapSwizzle swz = BLK == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, p.q, p.T, p.c.Hkv, p.G, D, {p.q_t, p.G * p.q_h, p.q_h}, BLK, p.G, swz, p.tpt)) return ATTN_ERR_CUDA;

@@ -239,23 +239,25 @@ __device__ __forceinline__ void store_codes(const uint4& d, uint32_t code, uint8
     *reinterpret_cast<uint4*>(line + (((ch + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? hi : lo;
     *reinterpret_cast<uint4*>(line + (((ch + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? lo : hi;
 }
-// Page and first row of the keys from `key` on; none: num_pages (outside the pool).
+// The block table's entry for the keys from `key` on, asked for a tile ahead; nothing looks at
+// it (and so waits for the load) before at().
+struct PageAsk {
+    int entry, key;
+    bool wanted;
+};
+__device__ __forceinline__ PageAsk page_ask(const PagedParams& p, const int32_t* table, int key, bool wanted) {
+    PageAsk a = {0, key, wanted};
+    if (wanted) a.entry = __ldg(table + page_index(p, key));
+    return a;
+}
+// Its page and row; none: page num_pages (outside the pool), row 0.
 struct PageAt {
     int page, row;
 };
-__device__ __forceinline__ PageAt page_at(const PagedParams& p, const int32_t* table, int key, bool wanted, bool report) {
-    PageAt a = {p.c.num_pages, 0};
-    if (wanted) {
-        const int pj = page_index(p, key);
-        const int got = __ldg(table + pj);
-        if (got >= 0 && got < p.c.num_pages) {
-            a.page = got;
-            a.row = key - pj * p.c.page_size;
-        } else if (report) {
-            atomicOr(&g_paged_status, STATUS_CACHE);
-        }
-    }
-    return a;
+__device__ __forceinline__ PageAt page_at(const PagedParams& p, const PageAsk& a, bool report) {
+    const bool have = a.wanted && a.entry >= 0 && a.entry < p.c.num_pages;
+    if (report && a.wanted && !have) atomicOr(&g_paged_status, STATUS_CACHE);
+    return {have ? a.entry : p.c.num_pages, have ? a.key - page_index(p, a.key) * p.c.page_size : 0};
 }
 
 template <int D, bool E4M3>
@@ -641,15 +643,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             const int32_t* table = p.table + w.b * p.table_stride;
             auto lookup = [&](int j) {
                 const int key = j * PC_BN + lane * p.box_rows;
-                return page_at(p, table, key, lane < boxes && j < je && key < w.kv, true);
+                return page_ask(p, table, key, lane < boxes && j < je && key < w.kv);
             };
             auto lookup_scale = [&](int j) {               // e4m3: lane's group of 8 rows
                 const int key = j * PC_BN + (lane & 15) * 8;
-                return page_at(p, table, key, E4M3 && j < je && key < w.kv, false);
+                return page_ask(p, table, key, E4M3 && j < je && key < w.kv);
             };
-            PageAt a = lookup(w.t0), sa = lookup_scale(w.t0);
+            PageAsk ask = lookup(w.t0), scale_ask = lookup_scale(w.t0);
             for (int j = w.t0; j < je && ok; ++j) {
-                const PageAt an = lookup(j + 1), san = lookup_scale(j + 1);
+                const PageAt a = page_at(p, ask, true), sa = page_at(p, scale_ask, false);
+                ask = lookup(j + 1);
+                scale_ask = lookup_scale(j + 1);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const int slot = static_cast<int>(item % N);
@@ -676,8 +680,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     }
                     __syncwarp();
                 }
-                a = an;
-                sa = san;
             }
         }
         if (*abort_flag || !ok) {

@@ -335,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         bool ok = true, first = true;
         w.begin(p, b_first, at, run);
         if (leader && lane == 0) p.shared[pair] = {w.b, w.h, w.qt, w.t0, w.t0 > 0 ? w.c.n : 0, 0, per};
-        const int k_boxes = C::KH / p.box_rows, v_boxes = PC_BN / p.box_rows;   // box_rows <= 64
+        const int k_boxes = C::KH >> p.box_shift, v_boxes = PC_BN >> p.box_shift;   // box_rows <= 64
         for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
             const int je = max(w.end(0), w.end(1));
             if (je <= w.t0) continue;
@@ -356,13 +356,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             // lane i copies box i of this CTA's K half / of V; pages are looked up a tile ahead
             auto lookup = [&](int j, bool k) {
                 const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * p.box_rows;
-                return page_at(p, table, key, lane < (k ? k_boxes : v_boxes) && j < je && key < w.kv, true);
+                return page_ask(p, table, key, lane < (k ? k_boxes : v_boxes) && j < je && key < w.kv);
             };
             auto lookup_scale = [&](int j, bool k) {       // e4m3: the lane's group of 8 rows
                 const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * 8;
-                return page_at(p, table, key, E4M3 && lane < (k ? 8 : 16) && j < je && key < w.kv, false);
+                return page_ask(p, table, key, E4M3 && lane < (k ? 8 : 16) && j < je && key < w.kv);
             };
-            auto copy = [&](bool k, int j, const PageAt& a, const PageAt& sa) {
+            auto copy = [&](bool k, int j, const PageAsk& ask, const PageAsk& scale_ask) {
+                const PageAt a = page_at(p, ask, true), sa = page_at(p, scale_ask, false);
                 if constexpr (E4M3) {
                     // into staging, on this CTA's own barriers
                     const int slot = static_cast<int>(item % C::NSTG);
@@ -390,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     ++item;
                     const uint32_t l_full = mapa_shared(PPBAR(PPB_FULL + slot), 0);
                     const int valid = w.kv - j * PC_BN;      // rows of the tile that exist
-                    const int cut = !k && valid < PC_BN && valid % p.box_rows != 0 ? valid / p.box_rows : -1;   // the box to fill by hand
+                    const int cut = !k && valid < PC_BN && (valid & (p.box_rows - 1)) != 0 ? valid >> p.box_shift : -1;   // the box to fill by hand
                     if (cut >= 0) {
                         const int pg = __shfl_sync(0xffffffffu, a.page, cut), r0 = __shfl_sync(0xffffffffu, a.row, cut);
                         const int n = pg < p.c.num_pages ? valid - cut * p.box_rows : 0;
@@ -419,16 +420,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 }
             };
             // items in the MMA warp's order: K(t0), K(t0+1), then V(j), K(j+2)
-            PageAt ka = lookup(w.t0, true), ks = lookup_scale(w.t0, true), va = lookup(w.t0, false), vs = lookup_scale(w.t0, false);
-            PageAt kn = lookup(w.t0 + 1, true), kns = lookup_scale(w.t0 + 1, true);
+            PageAsk ka = lookup(w.t0, true), ks = lookup_scale(w.t0, true), va = lookup(w.t0, false), vs = lookup_scale(w.t0, false);
+            PageAsk kn = lookup(w.t0 + 1, true), kns = lookup_scale(w.t0 + 1, true);
             copy(true, w.t0, ka, ks);
+            ka = lookup(w.t0 + 2, true);
+            ks = lookup_scale(w.t0 + 2, true);
             if (w.t0 + 1 < je) copy(true, w.t0 + 1, kn, kns);
             for (int j = w.t0; j < je && ok; ++j) {
-                ka = lookup(j + 2, true);
-                ks = lookup_scale(j + 2, true);
-                const PageAt vn = lookup(j + 1, false), vns = lookup_scale(j + 1, false);
+                kn = lookup(j + 3, true);
+                kns = lookup_scale(j + 3, true);
+                const PageAsk vn = lookup(j + 1, false), vns = lookup_scale(j + 1, false);
                 copy(false, j, va, vs);
                 if (j + 2 < je) copy(true, j + 2, ka, ks);
+                ka = kn;
+                ks = kns;
                 va = vn;
                 vs = vns;
             }
