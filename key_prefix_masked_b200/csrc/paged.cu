@@ -41,11 +41,17 @@ __device__ __forceinline__ int paged_kv_len(const int32_t* kv_len, int b, int ca
 #include "rope.cuh"
 #include "cache.cuh"
 
-// What the combine kernels need of a run that begins inside a (sequence, key head, token tile):
+// What the few-row combine kernel needs of a run that begins inside a (sequence, key head):
 // n units, t0 of them in earlier runs of `per` units.  n = 0: the run begins at a border, or there is none.
 struct SharedAt {
-    int b, h, qt, t0, n, pad;
+    int b, h, t0, n;
     long long per;
+};
+
+// What the chunk kernels' combine needs of a pair that several runs worked on: `parts` slots by
+// number (0: none) and slots 2C + s0 .. 2C + s1, of those runs whose first record says has_s (paged_chunk.cuh).
+struct SharedPair {
+    int b, h, qt, parts, part[2], s0, s1, has_s;
 };
 
 struct PagedParams {
@@ -60,7 +66,8 @@ struct PagedParams {
     const int32_t* q_start;             // null: one row per sequence
     float* part_out;                    // partial results of sequences shared by several CTAs
     float* part_lse;
-    SharedAt* shared;                   // by run
+    SharedAt* shared_at;                // by run (paged_rows.cuh)
+    SharedPair* shared;                 // two by run (paged_chunk.cuh)
     int B, T, Hq, G, max_q, kv_cap, causal;
     int min_units;                      // least tiles that a CTA takes
     int tile_keys;                      // paged_rows.cuh: keys per tile
@@ -272,7 +279,8 @@ int rows_ctas(int per_sm, int tile_keys, int B, int Hkv, long long kv_cap) {
 bool few_rows(long long max_q, int G) { return max_q * G <= PR_ROWS; }
 
 // A combine kernel behind the main one, launched to overlap it (it waits on the device).
-attn_status launch_combine(void (*kern)(PagedParams), dim3 grid, int threads, cudaStream_t stream, const PagedParams& p) {
+template <typename... Args>
+attn_status launch_combine(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t stream, const Args&... args) {
     if (grid.x == 0) return launched();
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -285,7 +293,7 @@ attn_status launch_combine(void (*kern)(PagedParams), dim3 grid, int threads, cu
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kern, p);
+    cudaLaunchKernelEx(&cfg, kern, args...);
     return launched();
 }
 
@@ -297,7 +305,7 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
     p.tile_keys = C::TK;
     p.part_out = static_cast<float*>(workspace);
     p.part_lse = p.part_out + 2LL * n * PR_ROWS * D;
-    p.shared = reinterpret_cast<SharedAt*>(p.part_lse + 2LL * n * PR_ROWS);
+    p.shared_at = reinterpret_cast<SharedAt*>(p.part_lse + 2LL * n * PR_ROWS);
     if (cudaFuncSetAttribute(paged_rows_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
@@ -338,8 +346,8 @@ attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
     const int n = chunk_runs(p.B, p.c.Hkv, p.G, D, p.max_q, p.kv_cap);
     p.min_units = CHUNK_MIN_UNITS;
     p.part_out = static_cast<float*>(workspace);
-    p.part_lse = p.part_out + 512LL * n * D;
-    p.shared = reinterpret_cast<SharedAt*>(p.part_lse + 512LL * n);
+    p.part_lse = p.part_out + 1024LL * n * D;
+    p.shared = reinterpret_cast<SharedPair*>(p.part_lse + 1024LL * n);
     p.tpt = 128 / p.G;
     p.box_rows = p.c.page_size & -p.c.page_size;   // the largest power of two that divides it
     const int most = PAIR ? 64 : PC_BN;
@@ -388,7 +396,7 @@ attn_status launch_chunk(PagedParams p, void* workspace, cudaStream_t stream) {
         return ATTN_ERR_CUDA;
     }
     kern<<<grid, threads, smem, stream>>>(mq, mk, mv, p, n);
-    return launch_combine(paged_chunk_combine_kernel<D>, dim3(n - 1, 8), 256, stream, p);
+    return launch_combine(paged_chunk_combine_kernel<D>, dim3(2 * n, 16), 256, stream, p, n);
 }
 
 template <int D>
@@ -506,10 +514,10 @@ size_t attn_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page
     if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || D <= 0 || page_size <= 0 || max_pages <= 0 || max_q <= 0)
         return 0;
     const long long q = max_q < T ? max_q : T, cap = static_cast<long long>(max_pages) * page_size;
-    // per run: two parts of rows x (D + 1) floats, and a SharedAt (both multiples of 8 bytes)
+    // per run: its parts (two of 16 rows, four of 256) of D + 1 floats a row, and the records
     if (few_rows(q, Hq / Hkv))
         return rows_ctas(2, RowsCfg<32, false>::TK, B, Hkv, cap) * (2ull * PR_ROWS * (D + 1) * sizeof(float) + sizeof(SharedAt));
-    return chunk_runs(B, Hkv, Hq / Hkv, D, q, cap) * (512ull * (D + 1) * sizeof(float) + sizeof(SharedAt));
+    return chunk_runs(B, Hkv, Hq / Hkv, D, q, cap) * (1024ull * (D + 1) * sizeof(float) + 2 * sizeof(SharedPair));
 }
 
 attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_strides* q_strides,

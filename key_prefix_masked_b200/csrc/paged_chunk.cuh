@@ -13,10 +13,16 @@
 // columns of their own and the order is S_0(j+1), S_1(j+1), PV_0(j), PV_1(j); every PV is
 // announced on a barrier, which a group waits for before it writes P_g (or O_g) again.
 //
-// The work, (sequence, key head, token tile, key tile), is laid end to end and dealt to
-// one persistent CTA per SM in equal contiguous runs, like the few-row kernel's: ragged
-// batches and causal triangles leave no SM idle at the end, and only a run's first and last
-// token tile can be shared with another CTA; paged_chunk_combine_kernel puts those together.
+// The work is (sequence, key head, token tile) pairs of n key tiles each, dealt to one persistent
+// CTA per SM so that every run has the same number of key tiles: run c takes pairs c, c + C,
+// c + 2C, ... up to its share; what its pairs have beyond that goes to a pool, in order, which
+// the runs whose pairs fall short share out.  So ragged batches and causal triangles leave
+// no SM idle, while nearly every pair starts at its first key tile when its neighbours, the other
+// token tiles of the same head, do: they read the same K and V at the same time, from L2.
+// (Cutting the pairs laid end to end into equal runs balances as well, but each run then
+// reads another place of the keys: 1185 against 1670 TFLOP/s at 2368 and 9472 rows on
+// 65536 keys, D 256, from L2 misses and the power they cost.)  Pairs worked on by several
+// CTAs are put together by paged_chunk_combine_kernel.
 //
 // K and V are copied by TMA, in boxes of the largest power of two of rows (up to 128) that divides
 // the page size, each box from its page; a box behind the sequence or of a page that does
@@ -43,14 +49,14 @@ struct ChunkCfg {
     static constexpr int NBLK = D / BLK;
     static constexpr int QT_BYTES = 128 * D * 2;        // one 128-row tile
     static constexpr int SLOT = PC_BN * D * 2;          // a K or V tile
-    static constexpr int CTRL = 1024;
+    static constexpr int CTRL = 2048;                   // barriers, TMEM address, abort flag, the deal
     static constexpr int GROUP = NBLK * 8 * SW;         // one 8-row group of a K or V tile
     // e4m3: staged codes of a tile, and its 128 scale bytes
     static constexpr int STG_BYTES = PC_BN * D + 128;
     static constexpr int NSTG = E4M3 ? (D == 128 ? 4 : 8) : 0;
-    static constexpr int NS_FIT = (232448 - 1024 - CTRL - 2 * QT_BYTES - NSTG * STG_BYTES) / SLOT;
+    static constexpr int NS_FIT = (232448 - CTRL - 2 * QT_BYTES - NSTG * STG_BYTES) / SLOT;
     static constexpr int NS = NS_FIT < 12 ? NS_FIT : 12;
-    static constexpr int SMEM = 1024 + 2 * QT_BYTES + NS * SLOT + NSTG * STG_BYTES + CTRL;
+    static constexpr int SMEM = 2 * QT_BYTES + NS * SLOT + NSTG * STG_BYTES + CTRL;
     static_assert(NS >= 3, "ring depth");
     static constexpr uint32_t LAYOUT = SW == 128 ? 2u : 4u;
     static constexpr uint32_t O_COL = 256;
@@ -72,7 +78,8 @@ struct ChunkCfg {
 enum : int {
     PCB_QFULL = 0, PCB_QEMPTY = 1, PCB_S = 2 /* [2] */, PCB_P = 4 /* [2], then the second halves' */, PCB_O = 8 /* [2] */,
     PCB_READ = 10 /* [2] S_g read out */, PCB_DRAIN = 12,
-    PCB_FULL = 13 /* [12] */, PCB_EMPTY = 25 /* [12] */, PCB_SFULL = 37 /* [8] */, PCB_SEMPTY = 45 /* [8] */, PCB_NUM = 53
+    PCB_FULL = 13 /* [12] */, PCB_EMPTY = 25 /* [12] */, PCB_SFULL = 37 /* [8] */, PCB_SEMPTY = 45 /* [8] */,
+    PCB_GFULL = 53 /* [4] segments */, PCB_GEMPTY = 57 /* [4] */, PCB_NUM = 61
 };
 
 // Keys that query row i of a sequence with n rows and kv keys sees.
@@ -100,122 +107,307 @@ __device__ __forceinline__ ChunkPair chunk_pair(const PagedParams& p, int n_q, i
     return c;
 }
 __device__ __forceinline__ int chunk_qtiles(const PagedParams& p, int n_live) { return (n_live + 2 * p.tpt - 1) / (2 * p.tpt); }
-// Units of sequence b for one key head.
-__device__ __forceinline__ long long chunk_units(const PagedParams& p, int b, bool report) {
-    const int n = query_range(p, b, report).n;
-    const int kv = paged_kv_len(p.kv_len, b, p.kv_cap, report);
-    const int live = min(n, p.max_q), nq = chunk_qtiles(p, live);
-    if (!p.causal) return static_cast<long long>(nq) * max(1, (kv + PC_BN - 1) / PC_BN);
-    long long sum = 0;
-    for (int qt = 0; qt < nq; ++qt)   // what the tile's last row sees
-        sum += max(1, (keys_seen(1, kv, n, min((qt + 1) * 2 * p.tpt, live) - 1) + PC_BN - 1) / PC_BN);
-    return sum;
-}
 
-// Walks a CTA's run of units.  Every role of the CTA walks the same segments.
-struct ChunkWalk {
-    int b, h, qt, t0, t1;            // key tiles [t0, t1) of the pair
-    int n_q, n_live, kv, q0;         // the sequence's rows (all, computed), keys, first row
-    long long left;                  // units of the run from t0 on
-    ChunkPair c;
-
-    __device__ __forceinline__ void sequence(const PagedParams& p) {
-        const QueryRange r = query_range(p, b, false);
-        n_q = r.n;
-        n_live = min(r.n, p.max_q);
-        q0 = r.t0;
-        kv = paged_kv_len(p.kv_len, b, p.kv_cap, false);
+// A pair by its number, counted over sequences, key heads and token tiles (fastest).  Used by a
+// converged warp: the lanes look at 32 sequences at a time.
+struct PairSeek {
+    int b, nq;                       // sequence and its token tiles
+    int n_q, n_live, kv, q0;         // its rows (all, computed), keys, first row
+    long long base;                  // pairs of the sequences before it
+    __device__ __forceinline__ void first() {
+        b = 0;
+        nq = 0;
+        base = 0;
     }
-    __device__ __forceinline__ void segment(const PagedParams& p) {
-        c = chunk_pair(p, n_q, n_live, kv, qt);
-        t1 = static_cast<int>(min(static_cast<long long>(c.n), t0 + left));
-    }
-    // At sequence b, `at` units into it, with `left` units to walk.
-    __device__ __forceinline__ void begin(const PagedParams& p, int b_, long long at, long long left_) {
-        b = b_;
-        left = left_;
-        sequence(p);
-        const long long units = chunk_units(p, b, false);
-        h = static_cast<int>(at / units);
-        at -= h * units;
-        qt = 0;
-        c = chunk_pair(p, n_q, n_live, kv, 0);
-        while (at >= c.n) {
-            at -= c.n;
-            c = chunk_pair(p, n_q, n_live, kv, ++qt);
+    // Forward to pair idx (there is one).
+    __device__ __forceinline__ void to(const PagedParams& p, long long idx) {
+        if (idx - base < static_cast<long long>(nq) * p.c.Hkv) return;
+        const int lane = threadIdx.x & 31;
+        while (b < p.B) {            // (base counts the pairs before sequence b)
+            const int mine = b + lane;
+            int m_n = 0, m_q0 = 0, m_kv = 0, m_nq = 0;
+            if (mine < p.B) {
+                const QueryRange r = query_range(p, mine, false);
+                m_n = r.n;
+                m_q0 = r.t0;
+                m_kv = paged_kv_len(p.kv_len, mine, p.kv_cap, false);
+                m_nq = chunk_qtiles(p, min(r.n, p.max_q));
+            }
+            const long long pairs = static_cast<long long>(m_nq) * p.c.Hkv;
+            long long incl = pairs;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += t;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + incl - pairs <= idx && idx < base + incl);
+            if (hit != 0u) {
+                const int l = __ffs(hit) - 1;
+                b += l;
+                base += __shfl_sync(0xffffffffu, incl - pairs, l);
+                nq = __shfl_sync(0xffffffffu, m_nq, l);
+                n_q = __shfl_sync(0xffffffffu, m_n, l);
+                q0 = __shfl_sync(0xffffffffu, m_q0, l);
+                kv = __shfl_sync(0xffffffffu, m_kv, l);
+                n_live = min(n_q, p.max_q);
+                return;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+            b += 32;
         }
-        t0 = static_cast<int>(at);
-        segment(p);
     }
-    __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == c.n; }
-    __device__ __forceinline__ void next(const PagedParams& p) {
-        left -= t1 - t0;
-        if (left <= 0) return;
-        t0 = 0;   // a segment that ends inside its pair ends the run
-        if (++qt == chunk_qtiles(p, n_live)) {
-            qt = 0;
-            if (++h == p.c.Hkv) {
-                h = 0;
-                do {
-                    ++b;
-                    sequence(p);
-                } while (n_live == 0);   // a later one has rows: left > 0
+};
+
+// The deal (in shared memory): C runs of T units (key tiles); run c's pairs exceed T by E[c+1] - E[c]
+// units, which are [E[c], E[c+1]) of the pool, and fall short of it by D[c+1] - D[c]: it takes
+// [D[c], D[c+1]) of the pool, as far as there is one.  (2^32 units would run for hours.)
+constexpr int PC_MAX_RUNS = 148;
+struct ChunkDeal {
+    uint32_t E[PC_MAX_RUNS + 1], D[PC_MAX_RUNS + 1];
+    uint32_t scan[2][8];
+    uint32_t T, total;
+};
+// Block-wide, at least PC_MAX_RUNS threads.  scratch: shared memory for `cap` sequences at a time,
+// {pairs before it, rows, keys, token tiles}.
+__device__ __forceinline__ void chunk_deal(const PagedParams& p, int C, ChunkDeal* s, int4* scratch, int cap) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t load = 0, before = 0;   // key tiles of run tid's pairs; pairs of the sequences before this batch
+    for (int b0 = 0; b0 < p.B; b0 += cap) {
+        const int nb = min(cap, p.B - b0);
+        for (int i = tid; i < nb; i += blockDim.x) {
+            const bool report = blockIdx.x == 0;   // one block reports ranges out of bounds
+            const int n = query_range(p, b0 + i, report).n;
+            scratch[i] = make_int4(0, n, paged_kv_len(p.kv_len, b0 + i, p.kv_cap, report), chunk_qtiles(p, min(n, p.max_q)));
+        }
+        __syncthreads();
+        if (warp == 0) {
+            uint32_t carry = 0;
+            for (int i0 = 0; i0 < nb; i0 += 32) {
+                const uint32_t v = i0 + lane < nb ? static_cast<uint32_t>(scratch[i0 + lane].w) * p.c.Hkv : 0u;
+                uint32_t incl = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += t;
+                }
+                if (i0 + lane < nb) scratch[i0 + lane].x = static_cast<int>(carry + incl - v);
+                carry += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            if (lane == 0) s->total = carry;
+        }
+        __syncthreads();
+        const uint32_t pairs = s->total;
+        if (tid < C) {
+            int i = 0;
+            for (uint32_t l = (static_cast<uint32_t>(tid) + C - before % C) % C; l < pairs; l += C) {
+                while (l >= static_cast<uint32_t>(scratch[i].x) + static_cast<uint32_t>(scratch[i].w) * p.c.Hkv) ++i;
+                const int4 q = scratch[i];
+                load += chunk_pair(p, q.y, min(q.y, p.max_q), q.z, static_cast<int>((l - static_cast<uint32_t>(q.x)) % static_cast<uint32_t>(q.w))).n;
             }
         }
-        segment(p);
+        before += pairs;
+        __syncthreads();
+    }
+    uint32_t sum = load;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0 && warp < 5) s->scan[0][warp] = sum;
+    __syncthreads();
+    uint32_t total = 0;
+    for (int w = 0; w < 5; ++w) total += s->scan[0][w];
+    const uint32_t T = max(static_cast<uint32_t>(p.min_units), (total + C - 1) / C);
+    __syncthreads();
+    const uint32_t ex = load > T ? load - T : 0u, de = tid < C && load < T ? T - load : 0u;
+    uint32_t ie = ex, id = de;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t e = __shfl_up_sync(0xffffffffu, ie, o), d = __shfl_up_sync(0xffffffffu, id, o);
+        if (lane >= o) {
+            ie += e;
+            id += d;
+        }
+    }
+    if (lane == 31 && warp < 5) {
+        s->scan[0][warp] = ie;
+        s->scan[1][warp] = id;
+    }
+    __syncthreads();
+    for (int w = 0; w < warp && w < 5; ++w) {
+        ie += s->scan[0][w];
+        id += s->scan[1][w];
+    }
+    if (tid < C) {
+        s->E[tid + 1] = ie;
+        s->D[tid + 1] = id;
+    }
+    if (tid == 0) {
+        s->E[0] = s->D[0] = 0u;
+        s->T = T;
+        s->total = total;
+    }
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // TMA writes where the scratch was
+    __syncthreads();
+}
+// The last run r with table[r] <= x (and so table[r + 1] > x, for x below table[C]).
+__device__ __forceinline__ int deal_find(const uint32_t* table, int C, uint32_t x) {
+    int lo = 0, hi = C - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (table[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Walks a run's segments: key tiles [t0, t1) of a pair.
+struct ChunkWalk {
+    PairSeek k;
+    int h, qt, t0, t1;
+    ChunkPair c;
+    int run, C, source;              // whose list of pairs this is: the run's own, or one in the pool
+    long long idx;                   // pair
+    uint32_t left;                   // units to take from this list from t0 on
+    uint32_t pool, pool_end;         // next pool unit, and the end of the run's share
+    bool own, tail;                  // own list; the first piece of a pair that its own run began
+
+    __device__ __forceinline__ void pair(const PagedParams& p) {
+        k.to(p, idx);
+        const int i = static_cast<int>(idx - k.base);
+        h = i / k.nq;
+        qt = i - h * k.nq;
+        c = chunk_pair(p, k.n_q, k.n_live, k.kv, qt);
+    }
+    __device__ __forceinline__ void cut() { t1 = static_cast<int>(min(static_cast<uint32_t>(c.n), t0 + left)); }
+    __device__ __forceinline__ void begin(const PagedParams& p, const ChunkDeal* s, int run_, int C_) {
+        run = source = run_;
+        C = C_;
+        own = true;
+        tail = false;
+        pool = s->D[run];
+        pool_end = min(s->D[run + 1], s->E[C]);
+        left = s->T - (s->D[run + 1] - s->D[run]);   // its own pairs' units, at most T
+        t0 = t1 = 0;
+        idx = run;
+        k.first();
+        if (left > 0) {
+            pair(p);
+            cut();
+        } else {
+            from_pool(p, s);
+        }
+    }
+    __device__ __forceinline__ void from_pool(const PagedParams& p, const ChunkDeal* s) {
+        own = false;
+        left = 0;
+        if (pool >= pool_end) return;
+        source = deal_find(s->E, C, pool);
+        // skip runs without excess that share the table value
+        uint32_t off = s->T + (pool - s->E[source]);   // units into that run's list
+        idx = source;
+        k.first();
+        pair(p);
+        while (off >= static_cast<uint32_t>(c.n)) {
+            off -= c.n;
+            idx += C;
+            pair(p);
+        }
+        t0 = static_cast<int>(off);
+        tail = t0 > 0 && pool == s->E[source];
+        left = min(pool_end, s->E[source + 1]) - pool;
+        pool += left;
+        cut();
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next(const PagedParams& p, const ChunkDeal* s) {
+        left -= t1 - t0;
+        if (left > 0) {
+            idx += C;
+            t0 = 0;
+            tail = false;
+            pair(p);
+            cut();
+        } else {
+            from_pool(p, s);
+        }
     }
     // key tiles of this segment that row tile g takes
     __device__ __forceinline__ int end(int g) const { return min(t1, g ? c.ng1 : c.ng0); }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == c.n; }
+    // Where a part of a pair is kept: the part that the pair's own run began, the first pool piece of
+    // such a pair, a piece that a run's share of the pool begins inside of, one that it ends inside of.
+    __device__ __forceinline__ int slot() const { return own ? run : tail ? C + source : t0 > 0 ? 2 * C + run : 3 * C + run; }
 };
-
-// Block-wide: the run's length, and for CTA blockIdx.x its first sequence and the units into it.
-template <int THREADS>
-__device__ __forceinline__ long long chunk_deal(const PagedParams& p, int n_ctas, long long first_of, long long* s_scr, bool report,
-                                                int* b_out, long long* at_out, long long* all_out) {
-    constexpr int W = THREADS / 32;
-    const int tid = threadIdx.x;
-    long long sum = 0;
-    for (int b = tid; b < p.B; b += THREADS) sum += chunk_units(p, b, report);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((tid & 31) == 0) s_scr[tid >> 5] = sum;
-    __syncthreads();
-    long long all = 0;
-    for (int w = 0; w < W; ++w) all += s_scr[w];
-    all *= p.c.Hkv;
-    const long long per = max(static_cast<long long>(p.min_units), (all + n_ctas - 1) / n_ctas);
-    const long long unit = first_of * per;
-    __syncthreads();
-    long long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
-        const int b = b0 + tid;
-        const long long n = b < p.B ? chunk_units(p, b, false) : 0;
-        long long incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-            if ((tid & 31) >= o) incl += t;
+// A segment as the CTA's warps see it.  The copying warp, which is ahead of the others, walks and
+// hands the segments round through a short ring in shared memory, so that the walk's state
+// takes no registers beside a softmax row's.
+constexpr int PC_SEGS = 4;
+struct ChunkSeg {
+    int b, h, t0, t1;                // key tiles [t0, t1); t1 = 0: no more segments
+    int n, ng0, ng1;                 // of the pair, and of each row tile
+    int tok0, ntok0, ntok1;
+    int kv, n_q, q0, slot;
+    __device__ __forceinline__ int end(int g) const { return min(t1, g ? ng1 : ng0); }
+};
+__device__ __forceinline__ ChunkSeg make_seg(const ChunkWalk& w) {
+    return {w.k.b, w.h, w.t0, w.t1, w.c.n, w.c.ng0, w.c.ng1, w.c.tok0, w.c.ntok0, w.c.ntok1, w.k.kv, w.k.n_q, w.k.q0, w.slot()};
+}
+// Producer (a converged warp whose lane 0 walks) and consumers (one arrival a warp) of the ring.
+struct SegRing {
+    ChunkSeg* seg;
+    uint32_t full, empty;            // barriers, PC_SEGS each
+    uint32_t i;
+    __device__ __forceinline__ bool put(const ChunkSeg& s, volatile int* abort_flag, unsigned long long limit) {
+        const uint32_t at = i % PC_SEGS;
+        if (!chunk_wait_warp(empty + 8 * at, ((i / PC_SEGS) & 1u) ^ 1u, abort_flag, limit)) return false;
+        if ((threadIdx.x & 31) == 0) {
+            seg[at] = s;
+            mbar_arrive(full + 8 * at);
         }
-        if ((tid & 31) == 31) s_scr[tid >> 5] = incl;
-        __syncthreads();
-        long long block = 0;
-        for (int w = 0; w < W; ++w) {
-            if (w < (tid >> 5)) incl += s_scr[w];
-            block += s_scr[w];
-        }
-        incl += base;
-        if (n > 0 && (incl - n) * p.c.Hkv <= unit && unit < incl * p.c.Hkv) {
-            s_scr[W] = b;
-            s_scr[W + 1] = unit - (incl - n) * p.c.Hkv;
-        }
-        base += block;
-        __syncthreads();
+        ++i;
+        __syncwarp();
+        return true;
     }
-    *b_out = static_cast<int>(s_scr[W]);
-    *at_out = s_scr[W + 1];
-    *all_out = all;
-    return per;
+    __device__ __forceinline__ const ChunkSeg* get(volatile int* abort_flag, unsigned long long limit) {
+        const uint32_t at = i % PC_SEGS;
+        if (!chunk_wait_warp(full + 8 * at, (i / PC_SEGS) & 1u, abort_flag, limit)) return nullptr;
+        return seg + at;
+    }
+    __device__ __forceinline__ void done() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * (i % PC_SEGS));
+        ++i;
+    }
+};
+// The records for the combine kernel: of the pair that the run began and did not finish, and of
+// the one that its share of the pool ends inside of.
+__device__ __forceinline__ void chunk_records(const PagedParams& p, const ChunkDeal* s, int run, int C) {
+    SharedPair rec[2] = {};
+    ChunkWalk w;                     // (by a converged warp)
+    for (w.begin(p, s, run, C); w.more(); w.next(p, s)) {
+        if (!w.own && w.t0 > 0 && !w.tail) rec[0].has_s = 1;
+        if (w.t1 == w.c.n || (!w.own && w.t0 > 0)) continue;
+        SharedPair& r = rec[w.own ? 0 : 1];
+        r.b = w.k.b;
+        r.h = w.h;
+        r.qt = w.qt;
+        if (w.own) {
+            const uint32_t x = s->E[run];                        // the rest is [x, x + n - t1) of the pool
+            r.parts = 2;
+            r.part[0] = w.slot();
+            r.part[1] = C + run;
+            r.s0 = deal_find(s->D, C, x) + 1;
+            r.s1 = deal_find(s->D, C, x + (w.c.n - w.t1) - 1);
+        } else {
+            r.parts = 1;
+            r.part[0] = w.slot();
+            r.s0 = run + 1;
+            r.s1 = deal_find(s->D, C, w.pool - w.left + w.c.n - 1);
+        }
+    }
+    if ((threadIdx.x & 31) == 0) {
+        p.shared[run] = rec[0];
+        p.shared[C + run] = rec[1];
+    }
 }
 
 // Sixteen codes of a row as bf16 values, to two 16-byte chunks (ch, ch + 1 before the swizzle)
@@ -265,28 +457,28 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PagedParams p, const int n_ctas) {
     using C = ChunkCfg<D, E4M3>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {   // swizzled tiles need it
+        if (threadIdx.x == 0) atomicOr(&g_paged_status, STATUS_LAYOUT);
+        return;
+    }
     uint8_t* sKV = smem + 2 * C::QT_BYTES;
     uint8_t* sStg = sKV + C::NS * C::SLOT;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sStg + C::NSTG * C::STG_BYTES);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + PCB_NUM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-    long long* s_scr = reinterpret_cast<long long*>(tmem_holder + 2);   // 18 words of 8 bytes
+    ChunkDeal* deal = reinterpret_cast<ChunkDeal*>(tmem_holder + 2);
+    SegRing segs = {reinterpret_cast<ChunkSeg*>(deal + 1), 0, 0, 0};
+    static_assert(PCB_NUM * 8 + 8 + sizeof(ChunkDeal) + PC_SEGS * sizeof(ChunkSeg) <= C::CTRL, "control area");
     const uint32_t bar0 = smem_u32(bars), sQ_addr = smem_u32(smem), sKV_addr = smem_u32(sKV);
 #define CBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     allow_next_kernel();
-    int b_first;
-    long long at, all;
-    const long long per = chunk_deal<C::THREADS>(p, n_ctas, blockIdx.x, s_scr, blockIdx.x == 0, &b_first, &at, &all);
-    const long long unit0 = blockIdx.x * per;
-    if (unit0 >= all) {
-        if (tid == 0) p.shared[blockIdx.x].n = 0;
-        return;
-    }
-    const long long run = min(per, all - unit0);
+    const int run = blockIdx.x;
+    segs.full = CBAR(PCB_GFULL);
+    segs.empty = CBAR(PCB_GEMPTY);
+    chunk_deal(p, n_ctas, deal, reinterpret_cast<int4*>(sKV), 4096);
 
     if (tid == 0) {
         mbar_init(CBAR(PCB_QFULL), 1);
@@ -307,6 +499,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             mbar_init(CBAR(PCB_SFULL + s), 33);    // the byte count's, and every copying lane's scale bytes
             mbar_init(CBAR(PCB_SEMPTY + s), 4);
         }
+        for (int i = 0; i < PC_SEGS; ++i) {
+            mbar_init(CBAR(PCB_GFULL + i), 1);
+            mbar_init(CBAR(PCB_GEMPTY + i), E4M3 ? 13 : 9);   // 8 softmax warps, MMA, converters
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -319,7 +515,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const unsigned long long wlim = p.wait_ns;
-    ChunkWalk w;
     if (warp < 8) {
         // ================================================================ softmax and epilogue
         const int g = warp >> 2, r = tid & 127;
@@ -338,15 +533,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
-            const bool live = r_tok < w.c.ntok(g) && r_tok < p.tpt;
-            const int i = w.c.tok(g) + r_tok;
-            const int seen = live ? keys_seen(p.causal, w.kv, w.n_q, i) : 0;
-            const int all_seen = keys_seen(p.causal, w.kv, w.n_q, w.c.tok(g));   // by every live row of the tile
+        while (ok) {
+            const ChunkSeg* sg = segs.get(abort_flag, wlim);
+            ok = sg != nullptr;
+            if (!ok || sg->t1 == 0) break;
+            const int i = sg->tok0 + g * p.tpt + r_tok;
+            const bool live = r_tok < (g ? sg->ntok1 : sg->ntok0) && r_tok < p.tpt;
+            const int seen = live ? keys_seen(p.causal, sg->kv, sg->n_q, i) : 0;
+            const int all_seen = keys_seen(p.causal, sg->kv, sg->n_q, sg->tok0 + g * p.tpt);   // by every live row of the tile
+            const int t0 = sg->t0;
             float m_ref = -INFINITY, l_sum = 0.0f;
-            const int j1 = w.end(g);
+            const int j1 = sg->end(g);
 #pragma unroll 1
-            for (int j = w.t0; j < j1; ++j) {
+            for (int j = t0; j < j1; ++j) {
                 ok = chunk_wait_warp(CBAR(PCB_S + g), cnt & 1u, abort_flag, wlim);
                 if (!ok) break;
                 tc_fence_after();
@@ -383,7 +582,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     tc_fence_after();
                 }
                 float factor = 1.0f;
-                if (j == w.t0) {
+                if (j == t0) {
                     m_ref = mx;
                 } else if (__any_sync(0xffffffffu, mx > m_ref + PC_RESCALE_LOG2)) {
                     const float m_new = fmaxf(m_ref, mx);
@@ -430,7 +629,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                 ++cnt;
             }
             if (!ok) break;
-            const bool has = j1 > w.t0;
+            const bool has = j1 > t0;
             if (has) {
                 // D <= 64: one phase per PV; 128: one per segment
                 ok = chunk_wait_warp(CBAR(PCB_O + g), C::AHEAD ? (cnt - 1) & 1u : o_phase, abort_flag, wlim);
@@ -441,10 +640,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             const bool some = !(l_sum == 0.0f);   // NaN counts
             const float inv = some ? 1.0f / l_sum : 0.0f;
             const float lse = some ? (m_ref + log2f(l_sum)) * 0.69314718055994530942f : -INFINITY;
-            const bool whole = w.whole();
-            const long long row = static_cast<long long>(w.q0) + i;
-            const int hq = w.h * p.G + r_head;
-            const long long part = ((2LL * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * 2 + g) * 128 + r;
+            const bool whole = t0 == 0 && sg->t1 == sg->n;
+            const long long row = static_cast<long long>(sg->q0) + i;
+            const int hq = sg->h * p.G + r_head;
+            const long long part = (sg->slot * 2LL + g) * 128 + r;
 #pragma unroll 1
             for (int oc = 0; oc < D / 32; ++oc) {
                 uint32_t o[32];
@@ -479,6 +678,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                 else if (p.lse != nullptr) p.lse[row * p.Hq + hq] = lse;
             }
             tc_fence_before();   // the reads of O_g above, before the next segment's first P
+            segs.done();
         }
     } else if (warp == C::WARP_MMA) {
         // ================================================================ MMA issuer
@@ -520,26 +720,30 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                 mma_ts_elect_x4<8, (2 * C::GROUP) / 16>(tmem + C::O_COL + static_cast<uint32_t>(g) * D, tmem + C::P_COL + static_cast<uint32_t>(g) * C::P_STEP + kb * 8u,
                                                         vd + static_cast<uint64_t>((kb * 2 * C::GROUP) >> 4), IDESC_PV, kb == 0 && first ? 0u : 1u);
         };
-        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
-            const int e0 = w.end(0), e1 = w.end(1), je = max(e0, e1);
-            if (je <= w.t0) continue;            // no keys: nothing was loaded
+        for (; ok; segs.done()) {
+            const ChunkSeg* sg = segs.get(abort_flag, wlim);
+            ok = sg != nullptr;
+            if (!ok || sg->t1 == 0) break;
+            const int t0 = sg->t0, kv = sg->kv;
+            const int e0 = sg->end(0), e1 = sg->end(1), je = max(e0, e1);
+            if (je <= t0) continue;              // no keys: nothing was loaded
             ok = chunk_wait_warp(CBAR(PCB_QFULL), q_phase, abort_flag, wlim);
             q_phase ^= 1u;
             if (!ok) break;
             k_slot = next_item();
             if (!ok) break;
-            if (w.t0 < e0) issue_s(0);
-            if (w.t0 < e1) issue_s(1);
+            if (t0 < e0) issue_s(0);
+            if (t0 < e1) issue_s(1);
             tc_commit_elect(CBAR(PCB_EMPTY + k_slot));
-            if (w.t0 + 1 == je) tc_commit_elect(CBAR(PCB_QEMPTY));   // the segment's last S: Q may be replaced
+            if (t0 + 1 == je) tc_commit_elect(CBAR(PCB_QEMPTY));   // the segment's last S: Q may be replaced
 #pragma unroll 1
-            for (int j = w.t0; j < je && ok; ++j) {
+            for (int j = t0; j < je && ok; ++j) {
                 v_slot = next_item();
                 if (!ok) break;
                 if constexpr (!E4M3) {
                     // rows of the last copied box that lie behind the sequence: cleared, since
                     // 0 * NaN would reach every row
-                    const int valid = w.kv - j * PC_BN;
+                    const int valid = kv - j * PC_BN;
                     const int dirty = valid < PC_BN ? (valid + p.box_rows - 1) / p.box_rows * p.box_rows : 0;
                     if (valid < dirty) {
                         constexpr int CH = C::SW / 16;
@@ -578,10 +782,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     if (j < eg) {
                         if (!arrived(PCB_P + g, p_phase[g])) break;
                         if constexpr (C::AHEAD) {
-                            issue_pv(g, j == w.t0, 0, PC_BN / 16);
+                            issue_pv(g, j == t0, 0, PC_BN / 16);
                             tc_commit_elect(CBAR(PCB_O + g));
                         } else {
-                            issue_pv(g, j == w.t0, 0, PC_BN / 32);
+                            issue_pv(g, j == t0, 0, PC_BN / 32);
                             if (!arrived(PCB_P + 2 + g, p_phase[g])) break;
                             issue_pv(g, false, PC_BN / 32, PC_BN / 16);
                             if (j + 1 == eg) tc_commit_elect(CBAR(PCB_O + g));
@@ -617,11 +821,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         uint32_t item = 0, qe_phase = 0;
         bool ok = true, first = true;
         const int boxes = PC_BN / p.box_rows;
-        w.begin(p, b_first, at, run);
-        if (lane == 0) p.shared[blockIdx.x] = {w.b, w.h, w.qt, w.t0, w.t0 > 0 ? w.c.n : 0, 0, per};
         constexpr int N = E4M3 ? C::NSTG : C::NS;          // the slots that are filled here
         constexpr int FULL = E4M3 ? PCB_SFULL : PCB_FULL, EMPTY = E4M3 ? PCB_SEMPTY : PCB_EMPTY;
-        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+        ChunkWalk w;
+        w.begin(p, deal, run, n_ctas);
+        for (; ok; w.next(p, deal)) {
+            ok = segs.put(w.more() ? make_seg(w) : ChunkSeg{}, abort_flag, wlim);
+            if (!ok || !w.more()) break;
             const int je = max(w.end(0), w.end(1));
             if (je <= w.t0) continue;
             if (!first) {
@@ -636,18 +842,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                 for (int g = 0; g < (both ? 2 : 1); ++g)
 #pragma unroll
                     for (int c = 0; c < C::NBLK; ++c)
-                        tma_load_4d(sQ_addr + g * C::QT_BYTES + c * 128 * C::SW, &tm_q, c * C::BLK, 0, w.h, w.q0 + w.c.tok(g), CBAR(PCB_QFULL));
+                        tma_load_4d(sQ_addr + g * C::QT_BYTES + c * 128 * C::SW, &tm_q, c * C::BLK, 0, w.h, w.k.q0 + w.c.tok(g), CBAR(PCB_QFULL));
             }
             // lane i < boxes copies box i of a tile (all lanes at once: one lane issuing them in
             // turn took 20 % longer with 16-row pages); its page is looked up one tile ahead
-            const int32_t* table = p.table + w.b * p.table_stride;
+            const int32_t* table = p.table + w.k.b * p.table_stride;
             auto lookup = [&](int j) {
                 const int key = j * PC_BN + lane * p.box_rows;
-                return page_ask(p, table, key, lane < boxes && j < je && key < w.kv);
+                return page_ask(p, table, key, lane < boxes && j < je && key < w.k.kv);
             };
             auto lookup_scale = [&](int j) {               // e4m3: lane's group of 8 rows
                 const int key = j * PC_BN + (lane & 15) * 8;
-                return page_ask(p, table, key, E4M3 && j < je && key < w.kv);
+                return page_ask(p, table, key, E4M3 && j < je && key < w.k.kv);
             };
             PageAsk ask = lookup(w.t0), scale_ask = lookup_scale(w.t0);
             for (int j = w.t0; j < je && ok; ++j) {
@@ -682,6 +888,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                 }
             }
         }
+        chunk_records(p, deal, run, n_ctas);
         if (*abort_flag || !ok) {
             // Copies in flight must land before the memory is reused; they have no one to wait for them.
             const uint64_t d0 = global_timer_ns();
@@ -700,15 +907,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             const int blk = c16 * 16 / C::BLK, ch = c16 * 16 % C::BLK / 8;
             uint32_t item = 0;
             bool ok = true;
-            for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
-                const int je = max(w.end(0), w.end(1));
-                for (int j2 = 2 * w.t0; j2 < 2 * je && ok; ++j2) {   // item: tile j2 / 2, K or V
+            for (; ok; segs.done()) {
+                const ChunkSeg* sg = segs.get(abort_flag, wlim);
+                ok = sg != nullptr;
+                if (!ok || sg->t1 == 0) break;
+                const int je = max(sg->end(0), sg->end(1)), kv = sg->kv;
+                for (int j2 = 2 * sg->t0; j2 < 2 * je && ok; ++j2) {   // item: tile j2 / 2, K or V
                     const int slot = static_cast<int>(item % C::NS), stg = static_cast<int>(item % C::NSTG);
                     ok = chunk_wait_warp(CBAR(PCB_SFULL + stg), (item / C::NSTG) & 1u, abort_flag, wlim) &&
                          chunk_wait_warp(CBAR(PCB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
                     if (!ok) break;
                     ++item;
-                    const int left = w.kv - (j2 >> 1) * PC_BN;       // rows of the tile that exist
+                    const int left = kv - (j2 >> 1) * PC_BN;       // rows of the tile that exist
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * (8 * C::SW);
                     // All of a thread's codes first: a load behind a store to shared memory would wait for it.
@@ -753,48 +963,66 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
 #undef CBAR
 }
 
-// Token tiles that several CTAs of paged_chunk_kernel shared.  Block c (x) looks at the border
-// between the runs of CTAs c and c + 1; the first border inside a tile puts the tile together, its
-// rows spread over blockIdx.y, one warp a row.  CTA c's part is slot 2c, or 2c + 1 where the
-// tile begins in its run.
+// Pairs that several CTAs worked on: one record of chunk_records a block (x), its rows spread over
+// blockIdx.y, one warp a row.
 template <int D>
-__global__ void __launch_bounds__(256) paged_chunk_combine_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(256) paged_chunk_combine_kernel(const PagedParams p, const int n_runs) {
     wait_for_main_kernel();                     // every block, so that this grid never ends before that one
-    const SharedAt s = p.shared[blockIdx.x + 1];
-    if (s.n == 0) return;                       // the border lies between two tiles
-    const long long u0 = (blockIdx.x + 1) * s.per - s.t0;   // the tile's first unit
-    const long long c0 = u0 / s.per, c1 = (u0 + s.n - 1) / s.per;
-    if (c0 != blockIdx.x) return;
+    const SharedPair s = p.shared[blockIdx.x];
+    if (s.parts == 0) return;
+    // the parts' slots, for all rows
+    __shared__ int s_slot[2 + PC_MAX_RUNS];
+    __shared__ int s_count[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int mine = s.s0 + static_cast<int>(threadIdx.x);        // (at most PC_MAX_RUNS of them, 256 threads)
+    const bool has = mine <= s.s1 && __ldcg(&p.shared[mine].has_s) != 0;
+    const unsigned bits = __ballot_sync(0xffffffffu, has);
+    if (lane == 0) s_count[warp] = __popc(bits);
+    __syncthreads();
+    int n = s.parts, rank = s.parts + __popc(bits & ((1u << lane) - 1u));
+    for (int w = 0; w < 8; ++w) {
+        if (w < warp) rank += s_count[w];
+        n += s_count[w];
+    }
+    if (has) s_slot[rank] = 2 * n_runs + mine;
+    if (static_cast<int>(threadIdx.x) < s.parts) s_slot[threadIdx.x] = s.part[threadIdx.x];
+    __syncthreads();
     const QueryRange qr = query_range(p, s.b, false);
     const int n_live = min(qr.n, p.max_q), tok0 = s.qt * 2 * p.tpt;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int V = D >= 128 ? 4 : D / 32, NV = D / (32 * V);   // floats per load, loads per lane
     for (int r = blockIdx.y * 8 + warp; r < 256; r += gridDim.y * 8) {
         const int g = r >> 7, rr = r & 127, tok = rr / p.G;
         const int i = tok0 + g * p.tpt + tok;
         if (tok >= p.tpt || i >= n_live) continue;
-        auto slot = [&](long long cc) { return ((2 * cc + (cc == c0 ? 1 : 0)) * 2 + g) * 128 + rr; };
+        auto at = [&](int k) { return (s_slot[k] * 2LL + g) * 128 + rr; };
         float M = -INFINITY;
-#pragma unroll 4
-        for (long long cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_lse + slot(cc)));
+        for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(p.part_lse + at(k)));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float sum = 0.0f, acc[NV * V];
 #pragma unroll
         for (int e = 0; e < NV * V; ++e) acc[e] = 0.0f;
-#pragma unroll 2
-        for (long long cc = c0; cc <= c1; ++cc) {
-            const float lc = __ldcg(p.part_lse + slot(cc));
-            if (lc == -INFINITY) continue;      // nothing was stored
-            const float wgt = expf(lc - M);
-            sum += wgt;
+        // weights 32 at a time, one per lane, so that the loads of consecutive parts overlap
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            const float lc = k0 + lane < n ? __ldcg(p.part_lse + at(k0 + lane)) : -INFINITY;
+            const float w_l = lc == -INFINITY ? 0.0f : expf(lc - M);
+            const unsigned there = __ballot_sync(0xffffffffu, lc != -INFINITY);   // (a part without keys stored no values)
+            const int m = min(32, n - k0);
+#pragma unroll 4
+            for (int k = 0; k < m; ++k) {
+                const float wgt = __shfl_sync(0xffffffffu, w_l, k);
+                sum += wgt;
+                if (!(there >> k & 1u)) continue;
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const float* src = p.part_out + slot(cc) * D + n * 32 * V + lane * V;
-                float v[V];
-                if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(src));
-                else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(src));
-                else v[0] = __ldcg(src);
+                for (int q = 0; q < NV; ++q) {
+                    const float* src = p.part_out + at(k0 + k) * D + q * 32 * V + lane * V;
+                    float v[V];
+                    if constexpr (V == 4) *reinterpret_cast<float4*>(v) = __ldcg(reinterpret_cast<const float4*>(src));
+                    else if constexpr (V == 2) *reinterpret_cast<float2*>(v) = __ldcg(reinterpret_cast<const float2*>(src));
+                    else v[0] = __ldcg(src);
 #pragma unroll
-                for (int e = 0; e < V; ++e) acc[n * V + e] += wgt * v[e];
+                    for (int e = 0; e < V; ++e) acc[q * V + e] += wgt * v[e];
+                }
             }
         }
         const bool some = !(sum == 0.0f);
@@ -803,10 +1031,10 @@ __global__ void __launch_bounds__(256) paged_chunk_combine_kernel(const PagedPar
         const int hq = s.h * p.G + rr - tok * p.G;
         __nv_bfloat16* dst = p.out + row * p.out_t + hq * p.out_h;
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            __nv_bfloat16* d = dst + n * 32 * V + lane * V;
+        for (int q = 0; q < NV; ++q) {
+            __nv_bfloat16* d = dst + q * 32 * V + lane * V;
             if constexpr (V == 4)
-                *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(acc[n * V] * inv, acc[n * V + 1] * inv), pack_bf16(acc[n * V + 2] * inv, acc[n * V + 3] * inv));
+                *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(acc[q * V] * inv, acc[q * V + 1] * inv), pack_bf16(acc[q * V + 2] * inv, acc[q * V + 3] * inv));
             else if constexpr (V == 2)
                 *reinterpret_cast<uint32_t*>(d) = pack_bf16(acc[0] * inv, acc[1] * inv);
             else

@@ -26,7 +26,7 @@ struct PagedPairCfg {
     static constexpr int NS = E4M3 ? 3 : 5;
     static constexpr int STG_BYTES = SLOT / 2 + 128;    // e4m3: staged codes of a half tile, scale bytes
     static constexpr int NSTG = E4M3 ? 4 : 0;
-    static constexpr int CTRL = 1024;
+    static constexpr int CTRL = 2048;
     static constexpr int SMEM = QT_BYTES + NS * SLOT + NSTG * STG_BYTES + CTRL;
     static_assert(SMEM <= 232448, "shared memory");
     static constexpr uint32_t O_COL = 256;
@@ -36,7 +36,7 @@ struct PagedPairCfg {
 };
 enum : int {
     PPB_QFULL = 0, PPB_QEMPTY = 1, PPB_S = 2 /* [2] */, PPB_P = 4 /* [2] */, PPB_PV = 6, PPB_DRAIN = 7,
-    PPB_FULL = 8 /* [5] */, PPB_EMPTY = 13 /* [5] */, PPB_SFULL = 18 /* [4] */, PPB_SEMPTY = 22 /* [4] */, PPB_NUM = 26
+    PPB_FULL = 8 /* [5] */, PPB_EMPTY = 13 /* [5] */, PPB_SFULL = 18 /* [4] */, PPB_SEMPTY = 22 /* [4] */, PPB_GFULL = 26 /* [4] segments */, PPB_GEMPTY = 30 /* [4] */, PPB_NUM = 34
 };
 
 // Arrival on a barrier of the pair's leader that orders this thread's earlier shared-memory
@@ -62,24 +62,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
     uint64_t* bars = reinterpret_cast<uint64_t*>(sStg + C::NSTG * C::STG_BYTES);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + PPB_NUM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-    long long* s_scr = reinterpret_cast<long long*>(tmem_holder + 2);
+    ChunkDeal* deal = reinterpret_cast<ChunkDeal*>(tmem_holder + 2);
+    SegRing segs = {reinterpret_cast<ChunkSeg*>(deal + 1), 0, 0, 0};
+    static_assert(PPB_NUM * 8 + 8 + sizeof(ChunkDeal) + PC_SEGS * sizeof(ChunkSeg) <= C::CTRL, "control area");
     const uint32_t bar0 = smem_u32(bars), sQ_addr = smem_u32(smem), sKV_addr = smem_u32(sKV);
 #define PPBAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
-    const long long pair = blockIdx.x >> 1;
+    const int run = static_cast<int>(blockIdx.x >> 1);
 
     allow_next_kernel();
-    int b_first;
-    long long at, all;
-    const long long per = chunk_deal<C::THREADS>(p, n_pairs, pair, s_scr, blockIdx.x == 0, &b_first, &at, &all);
-    const long long unit0 = pair * per;
-    if (unit0 >= all) {         // both CTAs of the pair
-        if (leader && tid == 0) p.shared[pair].n = 0;
-        return;
-    }
-    const long long run = min(per, all - unit0);
+    segs.full = PPBAR(PPB_GFULL);
+    segs.empty = PPBAR(PPB_GEMPTY);
+    chunk_deal(p, n_pairs, deal, reinterpret_cast<int4*>(sKV), 4096);
 
     if (tid == 0) {
         mbar_init(PPBAR(PPB_QFULL), 1);
@@ -98,6 +94,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             mbar_init(PPBAR(PPB_SFULL + s), 33);   // the byte count's, and every copying lane's scale bytes
             mbar_init(PPBAR(PPB_SEMPTY + s), 4);
         }
+        for (int i = 0; i < PC_SEGS; ++i) {
+            mbar_init(PPBAR(PPB_GFULL + i), 1);
+            mbar_init(PPBAR(PPB_GEMPTY + i), 4 + (leader ? 1 : 0) + (E4M3 ? 4 : 0));   // softmax, MMA, converters
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -110,7 +110,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const unsigned long long wlim = p.wait_ns;
-    ChunkWalk w;
 
     if (warp < 4) {
         // ================================================================ softmax and epilogue (both CTAs)
@@ -124,15 +123,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         const uint32_t p_bar[2] = {mapa_shared(PPBAR(PPB_P), 0), mapa_shared(PPBAR(PPB_P + 1), 0)};
         uint32_t cnt = 0;   // key tiles processed, over all segments
         bool ok = true;
-        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
-            const bool live = r_tok < w.c.ntok(g) && r_tok < p.tpt;
-            const int i = w.c.tok(g) + r_tok;
-            const int seen = live ? keys_seen(p.causal, w.kv, w.n_q, i) : 0;
-            const int all_seen = keys_seen(p.causal, w.kv, w.n_q, w.c.tok(g));
+        while (ok) {
+            const ChunkSeg* sg = segs.get(abort_flag, wlim);
+            ok = sg != nullptr;
+            if (!ok || sg->t1 == 0) break;
+            const int i = sg->tok0 + g * p.tpt + r_tok;
+            const bool live = r_tok < (g ? sg->ntok1 : sg->ntok0) && r_tok < p.tpt;
+            const int seen = live ? keys_seen(p.causal, sg->kv, sg->n_q, i) : 0;
+            const int all_seen = keys_seen(p.causal, sg->kv, sg->n_q, sg->tok0 + g * p.tpt);
+            const int t0 = sg->t0;
             float m_ref = -INFINITY, l_sum = 0.0f;
-            const int je = max(w.end(0), w.end(1));
+            const int je = max(sg->end(0), sg->end(1));
 #pragma unroll 1
-            for (int j = w.t0; j < je; ++j) {
+            for (int j = t0; j < je; ++j) {
                 ok = chunk_wait_warp(PPBAR(PPB_S + (cnt & 1)), (cnt >> 1) & 1, abort_flag, wlim);
                 if (!ok) break;
                 tc_fence_after();
@@ -154,7 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 const float mx = row_max(x) * mul;
                 float factor = 1.0f;
                 bool rescale = false;
-                if (j == w.t0) {
+                if (j == t0) {
                     m_ref = mx;
                 } else if (__any_sync(0xffffffffu, mx > m_ref + PC_RESCALE_LOG2)) {
                     const float m_new = fmaxf(m_ref, mx);
@@ -201,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 ++cnt;
             }
             if (!ok) break;
-            const bool has = je > w.t0;
+            const bool has = je > t0;
             if (has) {
                 // The last two PVs in turn: a parity wait tells one phase from the next only, and
                 // "S ready" of the last tile vouches for the PVs up to two before it.
@@ -213,10 +216,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             const bool some = !(l_sum == 0.0f);   // NaN counts
             const float inv = some ? 1.0f / l_sum : 0.0f;
             const float lse = some ? (m_ref + log2f(l_sum)) * 0.69314718055994530942f : -INFINITY;
-            const bool whole = w.whole();
-            const long long row = static_cast<long long>(w.q0) + i;
-            const int hq = w.h * p.G + r_head;
-            const long long part = ((2 * pair + (w.t0 == 0 ? 1 : 0)) * 2 + g) * 128 + r;
+            const bool whole = t0 == 0 && sg->t1 == sg->n;
+            const long long row = static_cast<long long>(sg->q0) + i;
+            const int hq = sg->h * p.G + r_head;
+            const long long part = (sg->slot * 2LL + g) * 128 + r;
 #pragma unroll 1
             for (int oc = 0; oc < D / 32; ++oc) {
                 uint32_t o[32];
@@ -251,6 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 else if (p.lse != nullptr) p.lse[row * p.Hq + hq] = lse;
             }
             tc_fence_before();   // the reads of O above, before the next segment's first P
+            segs.done();
         }
     } else if (warp == C::WARP_MMA) {
         // ================================================================ MMA issuer (leader)
@@ -281,17 +285,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 tc_commit_pair_elect(PPBAR(PPB_S + (s_cnt & 1)), 0x3);
                 ++s_cnt;
             };
-            for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
-                const int je = max(w.end(0), w.end(1));
-                if (je <= w.t0) continue;
+            for (; ok; segs.done()) {
+                const ChunkSeg* sg = segs.get(abort_flag, wlim);
+                ok = sg != nullptr;
+                if (!ok || sg->t1 == 0) break;
+                const int t0 = sg->t0, je = max(sg->end(0), sg->end(1));
+                if (je <= t0) continue;
                 ok = chunk_wait_warp(PPBAR(PPB_QFULL), q_phase, abort_flag, wlim);
                 q_phase ^= 1u;
                 if (!ok) break;
                 issue_s();
-                if (ok && w.t0 + 1 < je) issue_s();
-                if (ok && w.t0 + 2 >= je) tc_commit_pair_elect(PPBAR(PPB_QEMPTY), 0x3);   // the segment's last S
+                if (ok && t0 + 1 < je) issue_s();
+                if (ok && t0 + 2 >= je) tc_commit_pair_elect(PPBAR(PPB_QEMPTY), 0x3);   // the segment's last S
 #pragma unroll 1
-                for (int j = w.t0; j < je && ok; ++j) {
+                for (int j = t0; j < je && ok; ++j) {
                     const int slot = next_item();   // V
                     ok = ok && chunk_wait_warp(PPBAR(PPB_P + (p_cnt & 1)), (p_cnt >> 1) & 1, abort_flag, wlim);
                     if (!ok) break;
@@ -300,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
 #pragma unroll
                     for (int kb = 0; kb < PC_BN / 16; kb += 4)
                         mma_ts_pair_elect_x4<8, (2 * C::VGROUP) / 16>(tmem + C::O_COL, tmem + (p_cnt & 1) * PC_BN + kb * 8u,
-                                                                      vd + static_cast<uint64_t>((kb * 2 * C::VGROUP) >> 4), IDESC_PV, kb == 0 && j == w.t0 ? 0u : 1u);
+                                                                      vd + static_cast<uint64_t>((kb * 2 * C::VGROUP) >> 4), IDESC_PV, kb == 0 && j == t0 ? 0u : 1u);
                     tc_commit_pair_elect(PPBAR(PPB_EMPTY + slot), 0x3);
                     tc_commit_pair_elect(PPBAR(PPB_PV), 0x3);
                     ++p_cnt;
@@ -333,10 +340,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         const uint32_t l_q = mapa_shared(PPBAR(PPB_QFULL), 0);
         uint32_t item = 0, qe_phase = 0;
         bool ok = true, first = true;
-        w.begin(p, b_first, at, run);
-        if (leader && lane == 0) p.shared[pair] = {w.b, w.h, w.qt, w.t0, w.t0 > 0 ? w.c.n : 0, 0, per};
         const int k_boxes = C::KH >> p.box_shift, v_boxes = PC_BN >> p.box_shift;   // box_rows <= 64
-        for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
+        ChunkWalk w;
+        w.begin(p, deal, run, n_pairs);
+        for (; ok; w.next(p, deal)) {
+            ok = segs.put(w.more() ? make_seg(w) : ChunkSeg{}, abort_flag, wlim);
+            if (!ok || !w.more()) break;
             const int je = max(w.end(0), w.end(1));
             if (je <= w.t0) continue;
             if (!first) {
@@ -350,17 +359,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 if (w.c.ntok(rank) > 0)
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d_pair_hint(sQ_addr + c * 128 * 128, &tm_q, c * 64, 0, w.h, w.q0 + w.c.tok(rank), l_q, pol_q);
+                        tma_load_4d_pair_hint(sQ_addr + c * 128 * 128, &tm_q, c * 64, 0, w.h, w.k.q0 + w.c.tok(rank), l_q, pol_q);
             }
-            const int32_t* table = p.table + w.b * p.table_stride;
+            const int32_t* table = p.table + w.k.b * p.table_stride;
             // lane i copies box i of this CTA's K half / of V; pages are looked up a tile ahead
             auto lookup = [&](int j, bool k) {
                 const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * p.box_rows;
-                return page_ask(p, table, key, lane < (k ? k_boxes : v_boxes) && j < je && key < w.kv);
+                return page_ask(p, table, key, lane < (k ? k_boxes : v_boxes) && j < je && key < w.k.kv);
             };
             auto lookup_scale = [&](int j, bool k) {       // e4m3: the lane's group of 8 rows
                 const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * 8;
-                return page_ask(p, table, key, E4M3 && lane < (k ? 8 : 16) && j < je && key < w.kv);
+                return page_ask(p, table, key, E4M3 && lane < (k ? 8 : 16) && j < je && key < w.k.kv);
             };
             auto copy = [&](bool k, int j, const PageAsk& ask, const PageAsk& scale_ask) {
                 const PageAt a = page_at(p, ask, true), sa = page_at(p, scale_ask, false);
@@ -390,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     if (!ok) return;
                     ++item;
                     const uint32_t l_full = mapa_shared(PPBAR(PPB_FULL + slot), 0);
-                    const int valid = w.kv - j * PC_BN;      // rows of the tile that exist
+                    const int valid = w.k.kv - j * PC_BN;      // rows of the tile that exist
                     const int cut = !k && valid < PC_BN && (valid & (p.box_rows - 1)) != 0 ? valid >> p.box_shift : -1;   // the box to fill by hand
                     if (cut >= 0) {
                         const int pg = __shfl_sync(0xffffffffu, a.page, cut), r0 = __shfl_sync(0xffffffffu, a.row, cut);
@@ -438,6 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 vs = vns;
             }
         }
+        if (leader) chunk_records(p, deal, run, n_pairs);
         if (*abort_flag || !ok) {
             // copies in flight must land before the memory is reused
             const uint64_t d0 = global_timer_ns();
@@ -452,8 +462,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             const int t = tid - 32 * C::WARP_CONV;
             uint32_t item = 0;
             bool ok = true;
-            for (w.begin(p, b_first, at, run); w.more() && ok; w.next(p)) {
-                const int je = max(w.end(0), w.end(1));
+            for (; ok; segs.done()) {
+                const ChunkSeg* sg = segs.get(abort_flag, wlim);
+                ok = sg != nullptr;
+                if (!ok || sg->t1 == 0) break;
+                const int t0 = sg->t0, je = max(sg->end(0), sg->end(1)), kv = sg->kv;
                 // items: K(t0), K(t0+1), then V(j), K(j+2)
                 auto convert = [&](auto is_k, int j) {
                     constexpr bool k = decltype(is_k)::value;
@@ -465,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     // K: this rank's 64 rows of 16 chunks; V: 128 rows of this rank's 8 chunks
                     constexpr int CPR = k ? 16 : 8, RPX = 128 / CPR, GROUP = k ? C::KGROUP : C::VGROUP;
                     const int r0 = t / CPR, c16 = t % CPR, blk = c16 >> 2;
-                    const int left = w.kv - j * PC_BN - (k ? rank * C::KH : 0);   // rows that exist
+                    const int left = kv - j * PC_BN - (k ? rank * C::KH : 0);   // rows that exist
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * 1024;
                     uint4 d[X];                          // all loads first, as in paged_chunk.cuh
@@ -496,9 +509,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                         mbar_arrive(PPBAR(PPB_SEMPTY + stg));
                     }
                 };
-                if (w.t0 < je) convert(std::true_type{}, w.t0);
-                if (w.t0 + 1 < je) convert(std::true_type{}, w.t0 + 1);
-                for (int j = w.t0; j < je && ok; ++j) {
+                if (t0 < je) convert(std::true_type{}, t0);
+                if (t0 + 1 < je) convert(std::true_type{}, t0 + 1);
+                for (int j = t0; j < je && ok; ++j) {
                     convert(std::false_type{}, j);
                     if (j + 2 < je) convert(std::true_type{}, j + 2);
                 }

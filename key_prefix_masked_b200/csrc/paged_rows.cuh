@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
     long long unit = blockIdx.x * deal.per;
     const long long unit_end = min(all, unit + deal.per);
     if (unit >= all) {
-        if (tid == 0) p.shared[blockIdx.x].n = 0;
+        if (tid == 0) p.shared_at[blockIdx.x].n = 0;
         return;
     }
     rows_scan(p, s_sum, [&](int, long long lo, long long hi) { return lo * p.c.Hkv <= unit && unit < hi * p.c.Hkv; },
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
         const int h = static_cast<int>(rem / units);
         const int tile0 = static_cast<int>(rem - static_cast<long long>(h) * units);
         const int tile1 = static_cast<int>(min(static_cast<long long>(units), tile0 + (unit_end - unit)));
-        if (tid == 0 && unit == blockIdx.x * deal.per) p.shared[blockIdx.x] = {b, h, 0, tile0, tile0 > 0 ? units : 0, 0, deal.per};
+        if (tid == 0 && unit == blockIdx.x * deal.per) p.shared_at[blockIdx.x] = {b, h, tile0, tile0 > 0 ? units : 0, deal.per};
         const QueryRange qr = query_range(p, b, false);
         const int kv = paged_kv_len(p.kv_len, b, p.kv_cap, false);
         const int rows = min(qr.n, p.max_q) * p.G;
@@ -711,7 +711,7 @@ template <int D>
 __global__ void __launch_bounds__(PR_THREADS) paged_rows_combine_kernel(const PagedParams p) {
     const int tid = threadIdx.x;
     wait_for_main_kernel();   // every block, so that this grid never ends before that one
-    const SharedAt s = p.shared[blockIdx.x + 1];
+    const SharedAt s = p.shared_at[blockIdx.x + 1];
     if (s.n == 0) return;
     const int b = s.b, h = s.h;
     const long long u0 = (blockIdx.x + 1) * s.per - s.t0, c0 = u0 / s.per, c1 = (u0 + s.n - 1) / s.per;
