@@ -225,7 +225,7 @@ attn_status attn_prefix_fwd_splitkv_noalloc(const void* q, const void* k, const 
  *     for i < R/2, t = position * inv_freq[i], and (a, b) the pair i of the first R elements,
  *     (a, b) -> attn_factor * (a cos t - b sin t, b cos t + a sin t);   elements >= R: y
  * Pair i is elements (i, i + R/2), or (2i, 2i + 1) if `interleaved`.  fp32 arithmetic with
- * one rounding to bf16 at the end; the angle is formed and reduced in fp64, so positions
+ * one rounding to bf16 at the end (squares of elements beyond 10^19 overflow it); the angle is formed and reduced in fp64, so positions
  * over the whole int32 range (negative ones included) rotate as exactly as near ones.
  *   x, y:      bf16 [B, H, T, D] at their strides (see attn_strides; NULL: contiguous).
  *              y may be x itself; other overlaps give undefined values.
@@ -256,8 +256,10 @@ attn_status attn_qk_norm_rope(const attn_rope_operand* q, const attn_rope_operan
  *     value); every code * 2^e is a bf16 number (at e = 120 magnitudes above 240 * 2^120 are
  *     stored as that, the largest one below infinity).  A row that holds a NaN or an infinity
  *     is stored as NaN (scale byte 255), and reads back as NaN.
+ *     Scale bytes begin 8-byte aligned.
  * page_size: a multiple of 8.  Strides: multiples of 16 bytes, t >= D, h a multiple of
- * min(D, 64) elements (any layout of whole rows has that).
+ * min(D, 64) elements (any layout of whole rows has that), b and h not 0 where there are
+ * several pages or heads.
  * num_pages * page_size <= 2^31 - 1; element offsets are 64-bit. */
 #define ATTN_CACHE_BF16 0
 #define ATTN_CACHE_E4M3 1
@@ -304,7 +306,15 @@ attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table,
  *     leave [0, T] are clamped and rows beyond max_q are not computed; either raises
  *     ATTN_ERR_CACHE_RANGE.  kv_len and block_table as attn_cache_read, with
  *     max_pages * page_size in Tk's place.
- *   Hq: a multiple of Hkv, Hq / Hkv <= 128.
+ *   Hq: a multiple of Hkv, Hq / Hkv <= 128.  q, out: strides not 0 where there are several
+ *     heads or rows; out may not overlap q.
+ *   Infinities and NaN count as the formula has them: in a key or value row before kv_len[b] they
+ *     reach every query row whose sequence has it, also (0 * NaN) through values that `causal`
+ *     hides from the row.  Keys that are hidden, and whatever lies behind kv_len[b], do not matter.
+ *     Sums of weighted values are kept in fp32 before they are divided by the weights' sum: values
+ *     times kv_len[b] should stay below 10^36.
+ *   Work of 2^31 or more tiles of 256 rows and 128 keys is not done, and raises
+ *     ATTN_ERR_CACHE_RANGE.
  *   workspace: attn_paged_workspace_bytes of device memory with the same arguments (max_q = 1
  *     without q_start), 16-byte aligned, or NULL where that is 0; no initialisation needed.
  *     Calls that share a workspace must not overlap on the GPU. */

@@ -13,6 +13,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "attn_prefix.h"
@@ -183,7 +184,7 @@ attn_status cache_view(const attn_cache* c, CacheView* v) {
     if (c->format != ATTN_CACHE_BF16 && c->format != ATTN_CACHE_E4M3) return ATTN_ERR_UNSUPPORTED;
     if (!head_dim_ok(c->D) || (c->page_size & 7)) return ATTN_ERR_UNSUPPORTED;
     const bool e4m3 = c->format == ATTN_CACHE_E4M3;
-    if (e4m3 && (!c->k_scale || !c->v_scale)) return ATTN_ERR_INVALID_ARG;
+    if (e4m3 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 8) || !aligned(c->v_scale, 8))) return ATTN_ERR_INVALID_ARG;
     const int size = e4m3 ? 1 : 2;
     Strides s[2];
     if (!strides_of(&c->k_strides, c->Hkv, c->page_size, c->D, &s[0]) ||
@@ -192,8 +193,10 @@ attn_status cache_view(const attn_cache* c, CacheView* v) {
     memset(v, 0, sizeof *v);
     for (int i = 0; i < 2; ++i) {
         if ((s[i].b * size) & 15 || (s[i].h * size) & 15 || (s[i].t * size) & 15) return ATTN_ERR_INVALID_ARG;
+        const int blk = c->D < 64 ? c->D : 64;
         if (c->Hkv == 1) s[i].h = c->D;                                       // not used
-        if (s[i].h % (c->D < 64 ? c->D : 64) != 0) return ATTN_ERR_INVALID_ARG;
+        if (s[i].h % blk != 0 || s[i].h == 0 || (s[i].b == 0 && c->num_pages > 1)) return ATTN_ERR_INVALID_ARG;
+        if (s[i].h / blk > (0x7fffffffLL - c->D) / c->Hkv) return ATTN_ERR_INVALID_ARG;   // the kernels count heads in blocks
         v->data[i] = static_cast<uint8_t*>(i ? c->v : c->k);
         v->scale[i] = e4m3 ? (i ? c->v_scale : c->k_scale) : nullptr;
         v->sp[i] = s[i].b * size;
@@ -271,7 +274,8 @@ attn_status launch_read(const CacheReadParams& prm, int B, cudaStream_t stream) 
 // (every sequence of kv_cap keys) needs fewer.
 constexpr int ROWS_MIN_UNITS = 2;
 int rows_ctas(int per_sm, int tile_keys, int B, int Hkv, long long kv_cap) {
-    const long long units = static_cast<long long>(B) * Hkv * ((kv_cap + tile_keys - 1) / tile_keys);
+    const long long enough = static_cast<long long>(ROWS_MIN_UNITS) * SM_COUNT * per_sm;
+    const long long pairs = static_cast<long long>(B) * Hkv, units = pairs < enough ? pairs * ((kv_cap + tile_keys - 1) / tile_keys) : enough;
     const long long most = (units + ROWS_MIN_UNITS - 1) / ROWS_MIN_UNITS;
     return static_cast<int>(most < SM_COUNT * per_sm ? most : SM_COUNT * per_sm);
 }
@@ -333,8 +337,9 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
 constexpr int CHUNK_MIN_UNITS = 2;
 int chunk_runs(int B, int Hkv, int G, int D, long long max_q, long long kv_cap) {
     const int tokens = 2 * (128 / G), all = D == 256 ? SM_COUNT / 2 : SM_COUNT;
-    const long long tiles = static_cast<long long>(B) * Hkv * ((max_q + tokens - 1) / tokens);
-    const long long units = tiles * ((kv_cap + PC_BN - 1) / PC_BN);
+    const long long enough = static_cast<long long>(CHUNK_MIN_UNITS) * all;
+    long long units = static_cast<long long>(B) * Hkv;   // (each factor is below 2^31)
+    for (const long long f : {(max_q + tokens - 1) / tokens, (kv_cap + PC_BN - 1) / PC_BN}) units = units < enough ? units * f : enough;
     const long long most = (units + CHUNK_MIN_UNITS - 1) / CHUNK_MIN_UNITS;
     return static_cast<int>(most < all ? most : all);
 }
@@ -540,6 +545,8 @@ attn_status attn_paged_fwd(const attn_cache* cache, const void* q, const attn_st
     Strides sq, so;
     if (!token_strides_of(q_strides, Hq, cache->D, &sq) || !token_strides_of(out_strides, Hq, cache->D, &so))
         return ATTN_ERR_INVALID_ARG;
+    for (const Strides& s : {sq, so})   // rows of their own (no broadcast heads or tokens)
+        if ((Hq > 1 && s.h == 0) || (T > 1 && s.t == 0)) return ATTN_ERR_INVALID_ARG;
     const int rows_q = q_start == nullptr ? 1 : max_q < T ? max_q : T;
     const size_t need = attn_paged_workspace_bytes(B, T, Hq, cache->Hkv, cache->D, cache->page_size, max_pages, rows_q);
     if (need != 0 && (!workspace || !aligned16(workspace))) return ATTN_ERR_INVALID_ARG;

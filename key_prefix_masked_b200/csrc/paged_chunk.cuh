@@ -160,18 +160,22 @@ struct PairSeek {
 
 // The deal (in shared memory): C runs of T units (key tiles); run c's pairs exceed T by E[c+1] - E[c]
 // units, which are [E[c], E[c+1]) of the pool, and fall short of it by D[c+1] - D[c]: it takes
-// [D[c], D[c+1]) of the pool, as far as there is one.  (2^32 units would run for hours.)
+// [D[c], D[c+1]) of the pool, as far as there is one.  Pairs and units are counted in 32 bits: work of
+// PC_MAX_UNITS or more (seconds of it) is refused, with the range flag.
 constexpr int PC_MAX_RUNS = 148;
+constexpr unsigned long long PC_MAX_UNITS = 1ull << 31;
 struct ChunkDeal {
     uint32_t E[PC_MAX_RUNS + 1], D[PC_MAX_RUNS + 1];
     uint32_t scan[2][8];
-    uint32_t T, total;
+    uint32_t T, total, over;         // units per run, all units; too many
 };
 // Block-wide, at least PC_MAX_RUNS threads.  scratch: shared memory for `cap` sequences at a time,
 // {pairs before it, rows, keys, token tiles}.
 __device__ __forceinline__ void chunk_deal(const PagedParams& p, int C, ChunkDeal* s, int4* scratch, int cap) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t load = 0, before = 0;   // key tiles of run tid's pairs; pairs of the sequences before this batch
+    unsigned long long load = 0;     // key tiles of run tid's pairs
+    uint32_t before = 0;             // pairs of the sequences before this batch
+    if (tid == 0) s->over = 0u;
     for (int b0 = 0; b0 < p.B; b0 += cap) {
         const int nb = min(cap, p.B - b0);
         for (int i = tid; i < nb; i += blockDim.x) {
@@ -181,21 +185,25 @@ __device__ __forceinline__ void chunk_deal(const PagedParams& p, int C, ChunkDea
         }
         __syncthreads();
         if (warp == 0) {
-            uint32_t carry = 0;
+            unsigned long long carry = 0;
             for (int i0 = 0; i0 < nb; i0 += 32) {
-                const uint32_t v = i0 + lane < nb ? static_cast<uint32_t>(scratch[i0 + lane].w) * p.c.Hkv : 0u;
-                uint32_t incl = v;
+                const unsigned long long v = i0 + lane < nb ? static_cast<unsigned long long>(scratch[i0 + lane].w) * p.c.Hkv : 0ull;
+                unsigned long long incl = v;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+                    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
                     if (lane >= o) incl += t;
                 }
                 if (i0 + lane < nb) scratch[i0 + lane].x = static_cast<int>(carry + incl - v);
                 carry += __shfl_sync(0xffffffffu, incl, 31);
             }
-            if (lane == 0) s->total = carry;
+            if (lane == 0) {
+                if (before + carry >= PC_MAX_UNITS) s->over = 1u;
+                s->total = static_cast<uint32_t>(carry);
+            }
         }
         __syncthreads();
+        if (s->over) break;
         const uint32_t pairs = s->total;
         if (tid < C) {
             int i = 0;
@@ -208,16 +216,26 @@ __device__ __forceinline__ void chunk_deal(const PagedParams& p, int C, ChunkDea
         before += pairs;
         __syncthreads();
     }
-    uint32_t sum = load;
+    const bool mine_over = load >= PC_MAX_UNITS;
+    unsigned long long sum = load;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0 && warp < 5) s->scan[0][warp] = sum;
+    const bool over = __syncthreads_or(s->over || mine_over || sum >= PC_MAX_UNITS) != 0;
+    if (lane == 0 && warp < 5) s->scan[0][warp] = static_cast<uint32_t>(sum);
     __syncthreads();
     uint32_t total = 0;
-    for (int w = 0; w < 5; ++w) total += s->scan[0][w];
+    unsigned long long total64 = 0;
+    for (int w = 0; w < 5; ++w) total64 += s->scan[0][w];
+    if (over || total64 >= PC_MAX_UNITS) {   // uniform
+        if (blockIdx.x == 0 && tid == 0) atomicOr(&g_paged_status, STATUS_CACHE);
+        load = 0;                            // nothing is done
+    } else {
+        total = static_cast<uint32_t>(total64);
+    }
     const uint32_t T = max(static_cast<uint32_t>(p.min_units), (total + C - 1) / C);
     __syncthreads();
-    const uint32_t ex = load > T ? load - T : 0u, de = tid < C && load < T ? T - load : 0u;
+    const uint32_t mine = static_cast<uint32_t>(load);
+    const uint32_t ex = mine > T ? mine - T : 0u, de = tid < C && mine < T ? T - mine : 0u;
     uint32_t ie = ex, id = de;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -534,7 +552,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             if (lane == 0) mbar_arrive(bar);
         };
         while (ok) {
-            const ChunkSeg* sg = segs.get(abort_flag, wlim);
+            // (a pair without tokens for this group's tile leaves it waiting for the length of a segment)
+            const ChunkSeg* sg = segs.get(abort_flag, wlim < 1ull << 36 ? wlim * (deal->T + 1ull) : wlim);
             ok = sg != nullptr;
             if (!ok || sg->t1 == 0) break;
             const int i = sg->tok0 + g * p.tpt + r_tok;

@@ -23,15 +23,16 @@
 //   for Q and K.  Q is scaled to f16 by a power of two per row (its largest element in [2^14, 2^15),
 //   so what f16 drops is below 2^-39 of it); the key rows' scales multiply the scores; the
 //   value rows' scales 2^e multiply the weights, relative to E, the largest e seen: a weight
-//   times 2^(e-E) stays below 2^8.  Where e lies more than 12 below E in a tile, f16 would drop
+//   times 2^(e-E) stays below 2^15.  Where e lies more than 12 below E in a tile, f16 would drop
 //   bits of such weights, and the tile's V is widened to bf16 instead, exactly: a code's bits moved
 //   to a bf16's place are the value times 2^-120, and one packed multiply by 2^(120+e-E) does the rest.
 // - The running maximum moves only when a score exceeds it by 2^8 (a vote per tile): the
-//   weights stay below 2^8 and the result is the same up to rounding.
+//   weights stay below 2^8 (2^15 where they become f16) and the result is the same up to rounding.
 
 constexpr int PR_THREADS = 128;
 constexpr int PR_WARPS = 4;
 constexpr int PR_ROWS = 16;                // query rows per CTA
+constexpr float PR_RESCALE_LOG2 = 8.0f;    // how far a score may exceed the running maximum's reference
 
 template <int D, bool E4M3>
 struct RowsCfg {
@@ -55,6 +56,8 @@ struct RowsCfg {
     static constexpr int AREA = (RING > MERGE ? RING : MERGE) + 127 & ~127;
     static constexpr int SMEM = AREA + BARS + SCALES;
     static constexpr int PER_SM = SMEM > 110 * 1024 ? 1 : 2;
+    // e4m3: weights are kept 2^7 high, at most 2^15, so that f16 drops less than 2^-32 of a weight of one
+    static constexpr float HIGH_LOG2 = E4M3 ? 7.0f : 0.0f;
 };
 
 // Byte offset of 16-byte chunk c of row r in a stage's K or V part.  bf16: ldmatrix takes one
@@ -490,12 +493,14 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                     x[n][e] = y;
                     mx[e >> 1] = fmaxf(mx[e >> 1], y);
                 }
-            if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.0f || mx[1] > m[1] + 8.0f)) {
+            // m: the reference of the weights 2^(x - m), HIGH_LOG2 below a maximum of the scores so far
+            constexpr float LAZY = PR_RESCALE_LOG2 + C::HIGH_LOG2;
+            if (__any_sync(0xffffffffu, mx[0] > m[0] + LAZY || mx[1] > m[1] + LAZY)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float mn = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
                     mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
-                    mn = fmaxf(m[e], mn);
+                    mn = fmaxf(m[e], mn - C::HIGH_LOG2);
                     const float f = m[e] == -INFINITY ? 0.0f : exp2_approx(m[e] - mn);
                     m[e] = mn;
                     l[e] *= f;
@@ -620,19 +625,21 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                 while (global_timer_ns() - d0 < 2000000ull) {
                 }
             }
-            // O is in units of 2^E
-            const float f = e_ref <= -1000 ? 1.0f : __uint_as_float(static_cast<uint32_t>(e_ref) << 23);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][e] *= f;
         }
 
-        // ---- the four warps' results into one: m, l and o of each warp through shared memory
+        // ---- the four warps' results into one: m, l and o / l of each warp through shared memory
+        // (divided first: sums of values near bf16's largest would not fit fp32)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            float f = l[e] == 0.0f ? 0.0f : 1.0f / l[e];
+            if (E4M3 && e_ref > -1000) f *= __uint_as_float(static_cast<uint32_t>(e_ref) << 23);   // O is in units of 2^E
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                o[i][2 * e] *= f;
+                o[i][2 * e + 1] *= f;
+            }
         }
         __syncthreads();   // every warp is done with its ring
         float* so = reinterpret_cast<float*>(smem);                      // [4][16][D + 2]
@@ -668,8 +675,8 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
 #pragma unroll
             for (int w = 0; w < PR_WARPS; ++w) {
                 const float mw = sm[(w * PR_ROWS + r) * 2];
-                const float f = mw == -INFINITY ? 0.0f : exp2_approx(mw - mm);
-                ll += f * sm[(w * PR_ROWS + r) * 2 + 1];
+                const float f = (mw == -INFINITY ? 0.0f : exp2_approx(mw - mm)) * sm[(w * PR_ROWS + r) * 2 + 1];
+                ll += f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[e] += f * so[(w * PR_ROWS + r) * (D + 2) + d + e];
             }

@@ -164,6 +164,118 @@ def test_scales_and_spread(kp, n_q):
     check(kp, c)
 
 
+@pytest.mark.parametrize("n_q", [1, 100])
+@pytest.mark.parametrize("up", [10, 20])
+def test_large_values_with_small_weights(kp, n_q, up):
+    """Blocks of keys whose values are 2^up times the others' and whose weights are 2^-up: both count alike."""
+    c = make([3 * 256], [n_q], 2, 1, 64, 16, True, seed=12)
+    c["causal"] = False
+    c["q"] = torch.zeros_like(c["q"])
+    c["q"][..., 0] = 1.0
+    c["scale"] = math.log(2.0)                       # scores in powers of two: the key's first element
+    for j in range(3 * 256):
+        row = (int(c["table"][0, j // 16]), 0, j % 16)
+        big = j // 256 == 1
+        key = torch.zeros(1, 64, dtype=torch.bfloat16)
+        key[0, 0] = -up if big else 0.0
+        val = (c["vvals"][row].float() * (2.0 ** up if big else 1.0)).to(torch.bfloat16)[None]
+        for n, x in (("k", key), ("v", val)):
+            codes, s = ref.quantise(x)
+            c[n][row], c[n + "s"][row], c[n + "vals"][row] = codes[0], s[0], ref.dequantise(codes, s)[0]
+    check(kp, c)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n_q", [1, 60])
+@pytest.mark.parametrize("D", [64, 256])
+def test_nan_rows_reach_their_sequence_only(kp, D, n_q, e4m3):
+    c = make([100, 130, 70], [n_q] * 3, 4, 2, D, 16, e4m3, seed=14)
+    clean, _ = check(kp, c)
+    for n in ("k", "v"):
+        d = dict(c)
+        d[n] = c[n].clone()
+        at = (int(c["table"][1, 2]), 1, 5)                  # key 37 of sequence 1, key head 1
+        if e4m3:
+            d[n + "s"] = c[n + "s"].clone()
+            d[n][at], d[n + "s"][at] = 0x7F, 255
+        else:
+            d[n][at] = math.nan
+        out, lse = call(kp, d)
+        assert torch.equal(out[:n_q], clean[:n_q]) and torch.equal(out[2 * n_q:], clean[2 * n_q:])
+        assert torch.equal(out[n_q:2 * n_q, :2], clean[n_q:2 * n_q, :2])            # the other key head
+        assert torch.isnan(out[n_q:2 * n_q, 2:]).all()
+        assert torch.isnan(lse[n_q:2 * n_q, 2:]).all() == (n == "k")
+    assert kp.device_status() == kp.ATTN_OK
+
+
+@pytest.mark.parametrize("n_q", [1, 17])
+def test_thousands_of_sequences(kp, n_q):
+    rnd = random.Random(15)
+    kv = [rnd.choice((0, 1, 7, 18, 40)) for _ in range(4200)]
+    rows = [rnd.choice((0, n_q, n_q, n_q + 2)) if n_q > 1 else rnd.choice((0, 1)) for _ in kv]
+    check(kp, make(kv, rows, 2, 1, 32, 8, n_q > 1, seed=16), max_q=max(rows))
+
+
+def test_pages_shared_by_sequences(kp):
+    for n_q in (1, 50):
+        c = make([150, 150, 90], [n_q] * 3, 4, 2, 128, 16, False, seed=17)
+        c["table"][1:] = c["table"][0]
+        check(kp, c)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n_q", [1, 60])
+@pytest.mark.parametrize("D", [64, 256])
+def test_far_pages(kp, D, n_q, e4m3):
+    """Pages 2^32 bytes apart: offsets beyond 32 bits."""
+    c = make([40, 30], [n_q] * 2, 4, 2, D, 32, e4m3, seed=18)
+    want, want_lse = check(kp, c)
+    P, H, page, _ = c["k"].shape
+    size = 1 if e4m3 else 2
+    pool = torch.empty((P - 1) * 2 ** 32 // size + 2 * H * page * D, dtype=torch.uint8 if e4m3 else torch.bfloat16, device="cuda")
+    k, v = (pool.as_strided((P, H, page, D), (2 ** 32 // size, page * D, D, 1), i * H * page * D) for i in range(2))
+    k.copy_(c["k"])
+    v.copy_(c["v"])
+    d = {}
+    if e4m3:
+        k, v = k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn)
+        d = dict(k_scale=c["ks"].cuda(), v_scale=c["vs"].cuda())
+    out, lse = kp.attn_paged_fwd(c["q"].cuda(), k, v, c["table"].cuda(), torch.tensor(c["kv"], dtype=torch.int32).cuda(),
+                                 torch.tensor(c["start"], dtype=torch.int32).cuda(), n_q, scale=c["scale"], **d)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert kp.device_status() == kp.ATTN_OK
+
+
+def test_a_waiting_row_tile_is_no_timeout(kp):
+    """17 rows leave a block's second row tile without work for milliseconds; the limit is on steps."""
+    H, page, n = 148, 4096, 128
+    k = torch.zeros(1, H, page, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(17, H, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    kv = torch.tensor([n * page], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 17], dtype=torch.int32, device="cuda")
+    kp.set_wait_limit_ns(1_000_000)
+    try:
+        out, lse = kp.attn_paged_fwd(q, k, k, table, kv, start, 17, causal=False)
+        assert kp.device_status() == kp.ATTN_OK
+    finally:
+        kp.set_wait_limit_ns(1_000_000_000)
+    assert (out == 0).all() and (lse - math.log(n * page)).abs().max() < 1e-3
+
+
+def test_work_beyond_the_counters_is_refused(kp):
+    """32 sequences of 2^30 keys (one page again and again) over 32 key heads: 2^33 tiles."""
+    k = torch.zeros(1, 32, 2 ** 16, 32, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(32 * 17, 32, 32, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(32, 2 ** 14, dtype=torch.int32, device="cuda")
+    kv = torch.full((32,), 2 ** 30, dtype=torch.int32, device="cuda")
+    start = torch.arange(0, 32 * 17 + 1, 17, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 3.0)
+    kp.attn_paged_fwd(q, k, k, table, kv, start, 17, out=out)
+    assert kp.device_status() == kp.ATTN_ERR_CACHE_RANGE
+    assert (out == 3.0).all()
+
+
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("n_q", [1, 140])
 def test_rising_scores(kp, n_q, e4m3):

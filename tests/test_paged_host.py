@@ -50,6 +50,9 @@ BAD_CACHES = [
     (dict(page=12), 2), (dict(D=96), 2), (dict(kst=(1024, 60, 64)), 1), (dict(vst=(1024, 64, 32)), 1),
     (dict(kst=(4096, 72, 256)), 1),                                       # heads not a whole number of 64-column blocks apart
     (dict(fmt=1, ks=0x10000, vs=0x10000, kst=(1024, 72, 128)), 1),       # 8-byte rows in an e4m3 cache
+    (dict(fmt=1, ks=0x10004, vs=0x10000), 1), (dict(fmt=1, ks=0x10000, vs=0x10001), 1),
+    (dict(kst=(2048, 0, 64)), 1), (dict(vst=(0, 1024, 64)), 1),           # broadcast heads, pages
+    (dict(D=32, H=65535, kst=(1 << 40, 1 << 39, 32)), 1),                 # more column blocks than an int counts
 ]
 
 
@@ -92,8 +95,23 @@ def test_paged_rejects_bad_arguments(lib):
     for kw in (dict(q=NULL), dict(q=ctypes.c_void_p(0x10008)), dict(out=NULL), dict(table=NULL), dict(table=bad), dict(kv=NULL),
                dict(kv=bad), dict(qs=bad), dict(lse=bad), dict(stride=-1), dict(n=0), dict(n=1 << 28), dict(B=0), dict(T=0),
                dict(Hq=0), dict(Hq=5), dict(Hq=2 * 129), dict(mq=0), dict(scale=math.nan),
-               dict(qs=NULL), dict(ws=NULL, mq=1), dict(ws=ctypes.c_void_p(0x10008), mq=1), dict(qst=struct.pack("3q", 0, 64, 252))):
+               dict(qs=NULL), dict(ws=NULL, mq=1), dict(ws=ctypes.c_void_p(0x10008), mq=1), dict(qst=struct.pack("3q", 0, 64, 252)),
+               dict(qst=struct.pack("3q", 0, 0, 256)), dict(qst=struct.pack("3q", 0, 64, 0))):
         assert f(**kw) == 1, kw
+
+
+def test_workspace_of_any_size_of_work(lib):
+    w = lib.attn_paged_workspace_bytes
+    for D in (32, 64, 128, 256):
+        for max_q, G in ((1, 1), (16, 1), (17, 1), (4096, 4), (2 ** 31 - 1, 1), (2 ** 31 - 1, 128)):
+            small = w(1, 2 ** 31 - 1, G, 1, D, 16, 1, max_q)
+            large = w(2 ** 20, 2 ** 31 - 1, 16 * G, 16, D, 16, 4096, max_q)
+            most = w(2 ** 31 - 1, 2 ** 31 - 1, 65535 * G, 65535, D, 2 ** 20, 2 ** 11 - 1, max_q)     # products beyond 64 bits
+            assert 0 < small <= large == most < 2 ** 28
+    for bad in (dict(B=0), dict(T=0), dict(Hq=3), dict(Hkv=0), dict(D=0), dict(page=0), dict(pages=0), dict(mq=0)):
+        a = dict(B=2, T=8, Hq=4, Hkv=2, D=64, page=16, pages=4, mq=8)
+        a.update(bad)
+        assert w(a["B"], a["T"], a["Hq"], a["Hkv"], a["D"], a["page"], a["pages"], a["mq"]) == 0
 
 
 def test_python_checks_refuse(lib):
