@@ -33,6 +33,7 @@ _functions = {}
 # on every call (2 us); this one is what generated torch code uses.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(name, device, *args):
@@ -41,7 +42,7 @@ def _call(name, device, *args):
     if fn is None:
         fn = _functions[name] = getattr(lib(), name)
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
@@ -55,9 +56,19 @@ def _new(shape, strides, dtype, device):
     return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
+def _new_like(t):
+    """An uninitialised contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+_CONTIGUOUS = (0, 0, 0)                 # what the library takes for contiguous
+
+
 def _strides4(t, name):
     """(page or batch, head, row) strides of a [*, H, T, D] view; a dim of size 1 gets a stride that
     is never used but passes the checks."""
+    if t.is_contiguous():
+        return _CONTIGUOUS
     B, H, T, D = t.shape
     b, h, s, d = t.stride()
     if d != 1 and D != 1:
@@ -74,8 +85,11 @@ def _strides4(t, name):
 
 
 def _strides3(t, name):
-    """(0, head, token) strides of a [T, H, D] view."""
+    """(0, head, token) strides of a [T, H, D] view (not zeros for a contiguous one: the rotation,
+    which takes [B, H, T, D], would read those otherwise)."""
     T, H, D = t.shape
+    if t.is_contiguous():
+        return 0, D, H * D
     s, h, d = t.stride()
     if d != 1 and D != 1:
         raise ValueError(f"{name}: the head dim must be contiguous (stride 1)")
@@ -100,7 +114,7 @@ def _int32(t, shape, name, device):
 
 def _not_overlapping(t, name):
     """Rows that are written must not share memory (a broadcast head or batch)."""
-    if any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
+    if not t.is_contiguous() and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)):
         raise ValueError(f"{name} may not be a broadcast view")
 
 
@@ -145,25 +159,27 @@ def rope_inv_freq(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_c
 
 def _operand(x, out, weight, name):
     """(output, packed attn_rope_operand) of one operand; makes the output where none is given."""
-    shape, dev = x.shape, x.device
+    shape = x.shape
+    st = _strides4 if len(shape) == 4 else _strides3
+    x_st = st(x, name)
     if out is None:
-        *lead, n, D = shape
-        strides = (n * D, D, 1) if len(shape) == 3 else (lead[1] * n * D, n * D, D, 1)
-        out = _new(shape, strides, torch.bfloat16, dev)
+        out = _new_like(x)
+        out_st = x_st if x.is_contiguous() else st(out, name)
     else:
-        if out.shape != shape or out.dtype != torch.bfloat16 or out.device != dev:
-            raise ValueError(f"{name}_out must be a bf16 tensor of {name}'s shape on {dev}")
+        if out.shape != shape or out.dtype != torch.bfloat16 or out.device != x.device:
+            raise ValueError(f"{name}_out must be a bf16 tensor of {name}'s shape on {x.device}")
         _not_overlapping(out, name + "_out")
+        out_st = st(out, name + "_out")
     w = 0
     fp32 = False
     if weight is not None:
-        fp32 = weight.dtype == torch.float32
-        if (not (fp32 or weight.dtype == torch.bfloat16) or weight.device != dev or weight.shape != shape[-1:]
+        dtype = weight.dtype
+        fp32 = dtype == torch.float32
+        if (not (fp32 or dtype == torch.bfloat16) or weight.device != x.device or weight.shape != shape[-1:]
                 or not weight.is_contiguous()):
-            raise ValueError(f"{name}_weight must be a contiguous bf16 or fp32 tensor [D] on {dev}")
+            raise ValueError(f"{name}_weight must be a contiguous bf16 or fp32 tensor [D] on {x.device}")
         w = weight.data_ptr()
-    st = _strides4 if len(shape) == 4 else _strides3
-    return out, _OPERAND.pack(x.data_ptr(), out.data_ptr(), w, shape[1], fp32, *st(x, name), *st(out, name + "_out"))
+    return out, _OPERAND.pack(x.data_ptr(), out.data_ptr(), w, shape[1], fp32, *x_st, *out_st)
 
 
 def attn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -175,18 +191,20 @@ def attn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, e
     inv_freq: fp64 [R/2] (rope_inv_freq), R <= D elements of each head are rotated; None: norm only.
     A weight that is None leaves its operand unnormalised.  q_out may be q (in place)."""
     _bf16(q, (3, 4), "q")
-    four = q.dim() == 4
-    B, T = (q.shape[0], q.shape[2]) if four else (1, q.shape[0])
-    D = q.shape[-1]
+    shape, dev = q.shape, q.device
+    four = len(shape) == 4
+    B, T = (shape[0], shape[2]) if four else (1, shape[0])
+    D = shape[-1]
     R = 0
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != q.device or not inv_freq.is_contiguous():
-            raise ValueError(f"inv_freq must be a contiguous fp64 tensor [R / 2] on {q.device}")
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != dev or not inv_freq.is_contiguous():
+            raise ValueError(f"inv_freq must be a contiguous fp64 tensor [R / 2] on {dev}")
         R = 2 * inv_freq.numel()
-        _int32(positions, (B, T) if four else (T,), "positions", q.device)
+        _int32(positions, (B, T) if four else (T,), "positions", dev)
     if k is not None:
-        _bf16(k, (q.dim(),), "k")
-        if k.device != q.device or k.shape[-1] != D or (k.shape[0], k.shape[2] if four else 0) != (q.shape[0], T if four else 0):
+        _bf16(k, (len(shape),), "k")
+        ks = k.shape
+        if k.device != dev or ks[-1] != D or ks[0] != shape[0] or (four and ks[2] != T):
             raise ValueError("k must have q's tokens, head dim and device")
     if q.numel() == 0 or (k is not None and k.numel() == 0):
         raise ValueError("q and k may not be empty")
@@ -194,7 +212,7 @@ def attn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, e
     op_k = None
     if k is not None:
         k_out, op_k = _operand(k, k_out, k_weight, "k")
-    _call("attn_qk_norm_rope", q.device, op_q, op_k, positions.data_ptr() if R else None,
+    _call("attn_qk_norm_rope", dev, op_q, op_k, positions.data_ptr() if R else None,
           inv_freq.data_ptr() if R else None, B, T, D, R, bool(interleaved), eps, attn_factor)
     return q_out, k_out if k is not None else None
 
@@ -202,15 +220,16 @@ def attn_qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, e
 # ---------------------------------------------------------------------------------- cache
 def _cache(k_cache, v_cache, k_scale, v_scale):
     """The packed attn_cache of a pool's tensors."""
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
-    if not k_cache.is_cuda or k_cache.dim() != 4 or not (e4m3 or k_cache.dtype == torch.bfloat16):
+    dtype, shape = k_cache.dtype, k_cache.shape
+    e4m3 = dtype == torch.float8_e4m3fn
+    if not k_cache.is_cuda or len(shape) != 4 or not (e4m3 or dtype == torch.bfloat16):
         raise ValueError("k_cache must be a bf16 or float8_e4m3fn CUDA tensor [num_pages, Hkv, page_size, D]")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
+    if v_cache.shape != shape or v_cache.dtype != dtype or v_cache.device != k_cache.device:
         raise ValueError("v_cache must match k_cache")
-    P, H, page, D = k_cache.shape
+    P, H, page, D = shape
     if e4m3:
         for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if (s is None or s.dtype != torch.uint8 or s.device != k_cache.device or s.shape != k_cache.shape[:3]
+            if (s is None or s.dtype != torch.uint8 or s.device != k_cache.device or s.shape != shape[:3]
                     or not s.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous uint8 tensor [num_pages, Hkv, page_size]")
     elif k_scale is not None or v_scale is not None:
@@ -232,23 +251,25 @@ def attn_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
     _not_overlapping(v_cache, "v_cache")
     _bf16(k, (3,), "k")
     _bf16(v, (3,), "v")
-    T = k.shape[0]
-    if v.shape != k.shape or tuple(k.shape[1:]) != (k_cache.shape[1], k_cache.shape[3]):
+    shape, pool, dev = k.shape, k_cache.shape, k.device
+    T = shape[0]
+    if v.shape != shape or shape[1] != pool[1] or shape[2] != pool[3]:
         raise ValueError("k and v must be [T, Hkv, D] with the cache's Hkv and D")
-    if k.device != k_cache.device or v.device != k_cache.device:
+    if dev != k_cache.device or v.device != dev:
         raise ValueError("all tensors must be on one device")
-    _int32(slots, (T,), "slots", k.device)
+    _int32(slots, (T,), "slots", dev)
     if T == 0:
         return
-    _call("attn_cache_write", k.device, c, k.data_ptr(), v.data_ptr(), _STRIDES.pack(*_strides3(k, "k")),
+    _call("attn_cache_write", dev, c, k.data_ptr(), v.data_ptr(), _STRIDES.pack(*_strides3(k, "k")),
           _STRIDES.pack(*_strides3(v, "v")), slots.data_ptr(), T)
 
 
 def _table(block_table, kv_len, device):
-    if block_table.dtype != torch.int32 or block_table.device != device or block_table.dim() != 2 or (
-            block_table.stride(1) != 1 and block_table.shape[1] != 1):
+    shape = block_table.shape
+    if block_table.dtype != torch.int32 or block_table.device != device or len(shape) != 2 or (
+            block_table.stride(1) != 1 and shape[1] != 1):
         raise ValueError(f"block_table must be an int32 tensor [B, max_pages] on {device} with contiguous rows")
-    B, n = block_table.shape
+    B, n = shape
     if B == 0 or n == 0:
         raise ValueError("block_table may not be empty")
     _int32(kv_len, (B,), "kv_len", device)
@@ -262,24 +283,28 @@ def attn_cache_read(k_cache, v_cache, block_table, kv_len, Tk=None, k_scale=None
     block_table: int32 [B, max_pages]; kv_len: int32 [B].  Rows at or beyond kv_len[b] are left as
     they were (uninitialised where k_out, v_out are made here).  Tk: by default max_pages * page_size."""
     c = _cache(k_cache, v_cache, k_scale, v_scale)
-    B, n = _table(block_table, kv_len, k_cache.device)
+    dev = k_cache.device
+    B, n = _table(block_table, kv_len, dev)
     _, H, page, D = k_cache.shape
+    k_st = v_st = None                  # contiguous
     if k_out is None or v_out is None:
         if k_out is not None or v_out is not None:
             raise ValueError("k_out and v_out are given together")
-        shape = (B, H, n * page if Tk is None else int(Tk), D)
-        strides = (H * shape[2] * D, shape[2] * D, D, 1)
-        k_out, v_out = (_new(shape, strides, torch.bfloat16, k_cache.device) for _ in range(2))
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if (t.dim() != 4 or t.shape[:2] != (B, H) or t.shape[3] != D or t.dtype != torch.bfloat16
-                or t.device != k_cache.device or t.shape != k_out.shape or Tk not in (None, t.shape[2])):
-            raise ValueError(f"{name} must be a bf16 tensor [B, Hkv, Tk, D] on {k_cache.device}")
-        _not_overlapping(t, name)
-    if k_out.shape[2] == 0:
+        Tk = n * page if Tk is None else int(Tk)
+        k_out = _new((B, H, Tk, D), (H * Tk * D, Tk * D, D, 1), torch.bfloat16, dev)
+        v_out = torch.empty_like(k_out)
+    else:
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if (t.dim() != 4 or t.shape[:2] != (B, H) or t.shape[3] != D or t.dtype != torch.bfloat16
+                    or t.device != dev or t.shape != k_out.shape or Tk not in (None, t.shape[2])):
+                raise ValueError(f"{name} must be a bf16 tensor [B, Hkv, Tk, D] on {dev}")
+            _not_overlapping(t, name)
+        Tk = k_out.shape[2]
+        k_st, v_st = _STRIDES.pack(*_strides4(k_out, "k_out")), _STRIDES.pack(*_strides4(v_out, "v_out"))
+    if Tk == 0:
         return k_out, v_out
-    _call("attn_cache_read", k_cache.device, c, block_table.data_ptr(), block_table.stride(0), n, kv_len.data_ptr(),
-          k_out.data_ptr(), v_out.data_ptr(), _STRIDES.pack(*_strides4(k_out, "k_out")),
-          _STRIDES.pack(*_strides4(v_out, "v_out")), B, k_out.shape[2])
+    _call("attn_cache_read", dev, c, block_table.data_ptr(), block_table.stride(0), n, kv_len.data_ptr(),
+          k_out.data_ptr(), v_out.data_ptr(), k_st, v_st, B, Tk)
     return k_out, v_out
 
 
@@ -297,9 +322,9 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q
     c = _cache(k_cache, v_cache, k_scale, v_scale)
     B, n = _table(block_table, kv_len, k_cache.device)
     _bf16(q, (3,), "q")
-    T, Hq, D = q.shape
+    shape, dev = q.shape, q.device
+    T, Hq, D = shape
     _, Hkv, page, Dc = k_cache.shape
-    dev = q.device
     if D != Dc or dev != k_cache.device:
         raise ValueError("q must have the cache's head dim and device")
     if Hq == 0 or Hkv == 0 or Hq % Hkv:
@@ -308,12 +333,14 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q
         _int32(q_start, (B + 1,), "q_start", dev)
     elif T != B:
         raise ValueError("without q_start, q must have one row per sequence")
+    out_st = None                       # contiguous
     if out is None:
-        out = _new((T, Hq, D), (Hq * D, D, 1), torch.bfloat16, dev)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != dev:
+        out = _new_like(q)
+    elif out.shape != shape or out.dtype != torch.bfloat16 or out.device != dev:
         raise ValueError("out must be a bf16 tensor of q's shape on q's device")
     else:
         _not_overlapping(out, "out")
+        out_st = _STRIDES.pack(*_strides3(out, "out"))
     if lse is not None:
         if lse.shape != (T, Hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 tensor [T, Hq] on q's device")
@@ -334,7 +361,7 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q
         raise ValueError(f"workspace must be a contiguous CUDA buffer of at least {need} bytes")
     _call("attn_paged_fwd", dev, c, q.data_ptr(), _STRIDES.pack(*_strides3(q, "q")), block_table.data_ptr(),
           block_table.stride(0), n, kv_len.data_ptr(), None if q_start is None else q_start.data_ptr(), out.data_ptr(),
-          _STRIDES.pack(*_strides3(out, "out")), None if lse is None else lse.data_ptr(),
+          out_st, None if lse is None else lse.data_ptr(),
           workspace.data_ptr() if need else None, B, T, Hq, max_q, bool(causal), scale)
     return out, lse
 
