@@ -65,13 +65,15 @@ struct ChunkCfg {
     // PV_g(j), and P_g is announced in two halves, so that PV_g starts under the second.
     static constexpr bool AHEAD = D <= 64;
     static constexpr uint32_t P_COL = AHEAD ? O_COL + 128 : 0, P_STEP = AHEAD ? 64 : PC_BN;
-    // warps 0-7 softmax; bf16: 8 copies, 9 MMA; e4m3: 8-11 converters, 12 MMA, 13 copies
-    static constexpr int WARP_MMA = E4M3 ? 12 : 9;
-    static constexpr int WARP_COPY = E4M3 ? 13 : 8;
-    static constexpr int THREADS = E4M3 ? 512 : 320;
+    // warps 0-7 softmax; bf16: 8 copies, 9 MMA; e4m3: NCONV converters from 8 on, then MMA and copies
+    // (two converters keep up at 32 dims: 305 -> 277 us at 1200 rows on 30000 keys; at 64: 515 -> 604 us)
+    static constexpr int NCONV = !E4M3 ? 0 : D == 32 ? 2 : 4;
+    static constexpr int WARP_MMA = E4M3 ? 8 + NCONV : 9;
+    static constexpr int WARP_COPY = E4M3 ? 9 + NCONV : 8;
+    static constexpr int THREADS = !E4M3 ? 320 : D == 32 ? 384 : 512;
     // Score columns in a softmax thread's registers at once.  512 threads leave 128 registers
-    // each, so the e4m3 kernel reads the second half of a row twice (for its maximum first).
-    static constexpr int COLS = E4M3 ? 64 : 128;
+    // each, so the e4m3 kernels with four converters read the second half of a row twice (for its maximum first).
+    static constexpr int COLS = THREADS == 512 ? 64 : 128;
     static_assert(O_COL + 2 * D <= 512, "TMEM");
 };
 
@@ -109,52 +111,54 @@ __device__ __forceinline__ ChunkPair chunk_pair(const PagedParams& p, int n_q, i
 __device__ __forceinline__ int chunk_qtiles(const PagedParams& p, int n_live) { return (n_live + 2 * p.tpt - 1) / (2 * p.tpt); }
 
 // A pair by its number, counted over sequences, key heads and token tiles (fastest).  Used by a
-// converged warp: the lanes look at 32 sequences at a time.
+// converged warp, whose lanes hold 32 sequences at a time: steps inside those read nothing.
 struct PairSeek {
     int b, nq;                       // sequence and its token tiles
     int n_q, n_live, kv, q0;         // its rows (all, computed), keys, first row
     long long base;                  // pairs of the sequences before it
-    __device__ __forceinline__ void first() {
-        b = 0;
-        nq = 0;
-        base = 0;
-    }
-    // Forward to pair idx (there is one).
-    __device__ __forceinline__ void to(const PagedParams& p, long long idx) {
-        if (idx - base < static_cast<long long>(nq) * p.c.Hkv) return;
-        const int lane = threadIdx.x & 31;
-        while (b < p.B) {            // (base counts the pairs before sequence b)
-            const int mine = b + lane;
-            int m_n = 0, m_q0 = 0, m_kv = 0, m_nq = 0;
-            if (mine < p.B) {
-                const QueryRange r = query_range(p, mine, false);
-                m_n = r.n;
-                m_q0 = r.t0;
-                m_kv = paged_kv_len(p.kv_len, mine, p.kv_cap, false);
-                m_nq = chunk_qtiles(p, min(r.n, p.max_q));
-            }
-            const long long pairs = static_cast<long long>(m_nq) * p.c.Hkv;
-            long long incl = pairs;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += t;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, base + incl - pairs <= idx && idx < base + incl);
-            if (hit != 0u) {
-                const int l = __ffs(hit) - 1;
-                b += l;
-                base += __shfl_sync(0xffffffffu, incl - pairs, l);
-                nq = __shfl_sync(0xffffffffu, m_nq, l);
-                n_q = __shfl_sync(0xffffffffu, m_n, l);
-                q0 = __shfl_sync(0xffffffffu, m_q0, l);
-                kv = __shfl_sync(0xffffffffu, m_kv, l);
-                n_live = min(n_q, p.max_q);
-                return;
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
-            b += 32;
+    int w_b;                         // first of the 32 sequences
+    long long w_base, w_end;         // pairs before them, and with them
+    int l_n, l_q0, l_kv, l_nq;       // this lane's sequence
+    long long l_base;                // pairs before it
+    __device__ __forceinline__ void window(const PagedParams& p, int first, long long pairs_before) {
+        const int lane = threadIdx.x & 31, mine = first + lane;
+        w_b = first;
+        w_base = pairs_before;
+        l_n = l_q0 = l_kv = l_nq = 0;
+        if (mine < p.B) {
+            const QueryRange r = query_range(p, mine, false);
+            l_n = r.n;
+            l_q0 = r.t0;
+            l_kv = paged_kv_len(p.kv_len, mine, p.kv_cap, false);
+            l_nq = chunk_qtiles(p, min(r.n, p.max_q));
         }
+        const long long pairs = static_cast<long long>(l_nq) * p.c.Hkv;
+        long long incl = pairs;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        l_base = w_base + incl - pairs;
+        w_end = w_base + __shfl_sync(0xffffffffu, incl, 31);
+    }
+    __device__ __forceinline__ void begin(const PagedParams& p) { window(p, 0, 0); }
+    // To pair idx (there is one).
+    __device__ __forceinline__ void to(const PagedParams& p, long long idx) {
+        bool back = idx < w_base;
+        while (back || (idx >= w_end && w_b + 32 < p.B)) {
+            window(p, back ? 0 : w_b + 32, back ? 0 : w_end);
+            back = false;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, l_base <= idx && idx < l_base + static_cast<long long>(l_nq) * p.c.Hkv);
+        const int l = __ffs(hit | 0x80000000u) - 1;
+        b = w_b + l;
+        base = __shfl_sync(0xffffffffu, l_base, l);
+        nq = __shfl_sync(0xffffffffu, l_nq, l);
+        n_q = __shfl_sync(0xffffffffu, l_n, l);
+        q0 = __shfl_sync(0xffffffffu, l_q0, l);
+        kv = __shfl_sync(0xffffffffu, l_kv, l);
+        n_live = min(n_q, p.max_q);
     }
 };
 
@@ -306,7 +310,7 @@ struct ChunkWalk {
         left = s->T - (s->D[run + 1] - s->D[run]);   // its own pairs' units, at most T
         t0 = t1 = 0;
         idx = run;
-        k.first();
+        k.begin(p);
         if (left > 0) {
             pair(p);
             cut();
@@ -322,7 +326,6 @@ struct ChunkWalk {
         // skip runs without excess that share the table value
         uint32_t off = s->T + (pool - s->E[source]);   // units into that run's list
         idx = source;
-        k.first();
         pair(p);
         while (off >= static_cast<uint32_t>(c.n)) {
             off -= c.n;
@@ -397,35 +400,25 @@ struct SegRing {
     }
 };
 // The records for the combine kernel: of the pair that the run began and did not finish, and of
-// the one that its share of the pool ends inside of.
-__device__ __forceinline__ void chunk_records(const PagedParams& p, const ChunkDeal* s, int run, int C) {
-    SharedPair rec[2] = {};
-    ChunkWalk w;                     // (by a converged warp)
-    for (w.begin(p, s, run, C); w.more(); w.next(p, s)) {
-        if (!w.own && w.t0 > 0 && !w.tail) rec[0].has_s = 1;
-        if (w.t1 == w.c.n || (!w.own && w.t0 > 0)) continue;
-        SharedPair& r = rec[w.own ? 0 : 1];
-        r.b = w.k.b;
-        r.h = w.h;
-        r.qt = w.qt;
-        if (w.own) {
-            const uint32_t x = s->E[run];                        // the rest is [x, x + n - t1) of the pool
-            r.parts = 2;
-            r.part[0] = w.slot();
-            r.part[1] = C + run;
-            r.s0 = deal_find(s->D, C, x) + 1;
-            r.s1 = deal_find(s->D, C, x + (w.c.n - w.t1) - 1);
-        } else {
-            r.parts = 1;
-            r.part[0] = w.slot();
-            r.s0 = run + 1;
-            r.s1 = deal_find(s->D, C, w.pool - w.left + w.c.n - 1);
-        }
-    }
-    if ((threadIdx.x & 31) == 0) {
-        p.shared[run] = rec[0];
-        p.shared[C + run] = rec[1];
-    }
+// the one that its share of the pool ends inside of.  Written by one lane, segment by segment.
+__device__ __forceinline__ void chunk_record_none(const PagedParams& p, int run, int C) {
+    p.shared[run].parts = p.shared[C + run].parts = 0;
+    p.shared[run].has_s = 0;
+}
+__device__ __forceinline__ void chunk_record(const PagedParams& p, const ChunkDeal* s, const ChunkWalk& w) {
+    if (!w.own && w.t0 > 0 && !w.tail) p.shared[w.run].has_s = 1;
+    if (w.t1 == w.c.n || (!w.own && w.t0 > 0)) return;
+    SharedPair& r = p.shared[w.own ? w.run : w.C + w.run];
+    r.b = w.k.b;
+    r.h = w.h;
+    r.qt = w.qt;
+    r.parts = w.own ? 2 : 1;
+    r.part[0] = w.slot();
+    r.part[1] = w.C + w.run;
+    // own: the rest of the pair is the run's part of the pool; otherwise it lies behind this piece
+    const uint32_t x = w.own ? s->E[w.run] : w.pool;
+    r.s0 = w.own ? deal_find(s->D, w.C, x) + 1 : w.run + 1;
+    r.s1 = deal_find(s->D, w.C, x + (w.c.n - w.t1) - 1);
 }
 
 // Sixteen codes of a row as bf16 values, to two 16-byte chunks (ch, ch + 1 before the swizzle)
@@ -510,16 +503,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             mbar_init(CBAR(PCB_O + g), 1);
         }
         for (int s = 0; s < C::NS; ++s) {
-            mbar_init(CBAR(PCB_FULL + s), E4M3 ? 4 : 1);
+            mbar_init(CBAR(PCB_FULL + s), E4M3 ? C::NCONV : 1);
             mbar_init(CBAR(PCB_EMPTY + s), 1);
         }
         for (int s = 0; s < C::NSTG; ++s) {
             mbar_init(CBAR(PCB_SFULL + s), 33);    // the byte count's, and every copying lane's scale bytes
-            mbar_init(CBAR(PCB_SEMPTY + s), 4);
+            mbar_init(CBAR(PCB_SEMPTY + s), C::NCONV);
         }
         for (int i = 0; i < PC_SEGS; ++i) {
             mbar_init(CBAR(PCB_GFULL + i), 1);
-            mbar_init(CBAR(PCB_GEMPTY + i), E4M3 ? 13 : 9);   // 8 softmax warps, MMA, converters
+            mbar_init(CBAR(PCB_GEMPTY + i), 9 + C::NCONV);   // 8 softmax warps, MMA, converters
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -574,20 +567,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     uint32_t raw[C::COLS];
                     if constexpr (C::COLS == 128) tmem_ld128_wait(s_addr, raw);
                     else tmem_ld64_wait(s_addr + c0, raw);
-                    if ((j + 1) * PC_BN > all_seen) {
+                    if ((j + 1) * PC_BN > all_seen || !pos_scale) {
                         const int lim = seen - j * PC_BN - c0;   // columns this row sees
 #pragma unroll
                         for (int c = 0; c < C::COLS; ++c) x[c] = c < lim ? __uint_as_float(raw[c]) * (pos_scale ? 1.0f : sl2) : -INFINITY;
-                    } else if (pos_scale) {
-#pragma unroll
-                        for (int c = 0; c < C::COLS; ++c) x[c] = __uint_as_float(raw[c]);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < C::COLS; ++c) x[c] = __uint_as_float(raw[c]) * sl2;
+                        for (int c = 0; c < C::COLS; ++c) x[c] = __uint_as_float(raw[c]);
                     }
                 };
                 float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                 for (int c0 = PC_BN - C::COLS; c0 >= 0; c0 -= C::COLS) {
                     load(c0);
                     mx = fmaxf(mx, row_max(x));
@@ -621,25 +611,29 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) sp[t] = make_float2(0.0f, 0.0f);
                 const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(neg_m, neg_m);
-#pragma unroll
-                for (int cc = 0; cc < PC_BN / 32; ++cc) {
-                    constexpr int PER = C::COLS / 32;
-                    if (cc != 0 && cc % PER == 0) {
-                        load(cc * 32);
+                // (rolled where the columns come in halves: with the converters' code beside it, the kernel
+                // waits for instructions otherwise)
+#pragma unroll 1
+                for (int c0 = 0; c0 < PC_BN; c0 += C::COLS) {
+                    if (c0 != 0) {
+                        load(c0);
                         if constexpr (C::AHEAD) arrive(CBAR(PCB_READ + g));
                     }
-                    uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 y = fma2(make_float2(x[cc % PER * 32 + 2 * e], x[cc % PER * 32 + 2 * e + 1]), mul2, neg2);
-                        const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
-                        sp[e & 3] = add2(sp[e & 3], make_float2(p0, p1));   // the sum takes the weights unrounded
-                        pk[e] = pack_bf16(p0, p1);
-                    }
-                    tmem_st16(p_addr + cc * 16, pk);
-                    if (!C::AHEAD && cc == 1) {                             // the first 64 keys' weights
-                        tmem_wait_st();
-                        arrive(CBAR(PCB_P + g));
+                    for (int cc = 0; cc < C::COLS / 32; ++cc) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = fma2(make_float2(x[cc * 32 + 2 * e], x[cc * 32 + 2 * e + 1]), mul2, neg2);
+                            const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+                            sp[e & 3] = add2(sp[e & 3], make_float2(p0, p1));   // the sum takes the weights unrounded
+                            pk[e] = pack_bf16(p0, p1);
+                        }
+                        tmem_st16(p_addr + c0 / 2 + cc * 16, pk);
+                        if (!C::AHEAD && c0 == 0 && cc == 1) {                  // the first 64 keys' weights
+                            tmem_wait_st();
+                            arrive(CBAR(PCB_P + g));
+                        }
                     }
                 }
                 tmem_wait_st();
@@ -843,10 +837,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
         constexpr int N = E4M3 ? C::NSTG : C::NS;          // the slots that are filled here
         constexpr int FULL = E4M3 ? PCB_SFULL : PCB_FULL, EMPTY = E4M3 ? PCB_SEMPTY : PCB_EMPTY;
         ChunkWalk w;
+        if (lane == 0) chunk_record_none(p, run, n_ctas);
         w.begin(p, deal, run, n_ctas);
         for (; ok; w.next(p, deal)) {
             ok = segs.put(w.more() ? make_seg(w) : ChunkSeg{}, abort_flag, wlim);
             if (!ok || !w.more()) break;
+            if (lane == 0) chunk_record(p, deal, w);
             const int je = max(w.end(0), w.end(1));
             if (je <= w.t0) continue;
             if (!first) {
@@ -907,7 +903,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                 }
             }
         }
-        chunk_records(p, deal, run, n_ctas);
         if (*abort_flag || !ok) {
             // Copies in flight must land before the memory is reused; they have no one to wait for them.
             const uint64_t d0 = global_timer_ns();
@@ -915,12 +910,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (E4M3 && warp < 12) {
+    } else if (E4M3 && warp < 8 + C::NCONV) {
         // ================================================================ converters: e4m3 K and V
         if constexpr (E4M3) {
             constexpr int CPR = D / 16;          // 16-code chunks per row
-            constexpr int X = CPR;               // chunks per thread: 128 rows * CPR / 128 threads
-            constexpr int RPX = 128 / CPR;       // rows between a thread's chunks
+            constexpr int X = 4 * CPR / C::NCONV;       // chunks per thread: 128 rows * CPR over the converters' threads
+            constexpr int RPX = 32 * C::NCONV / CPR;    // rows between a thread's chunks
             const int t = tid - 256;
             const int r0 = t / CPR, c16 = t % CPR;
             const int blk = c16 * 16 / C::BLK, ch = c16 * 16 % C::BLK / 8;

@@ -143,16 +143,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 uint32_t raw[PC_BN];
                 tmem_ld128_wait(s_addr, raw);
                 float x[PC_BN];
-                if ((j + 1) * PC_BN > all_seen) {
+                if ((j + 1) * PC_BN > all_seen || !pos_scale) {
                     const int lim = seen - j * PC_BN;
 #pragma unroll
                     for (int c = 0; c < PC_BN; ++c) x[c] = c < lim ? __uint_as_float(raw[c]) * (pos_scale ? 1.0f : sl2) : -INFINITY;
-                } else if (pos_scale) {
-#pragma unroll
-                    for (int c = 0; c < PC_BN; ++c) x[c] = __uint_as_float(raw[c]);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < PC_BN; ++c) x[c] = __uint_as_float(raw[c]) * sl2;
+                    for (int c = 0; c < PC_BN; ++c) x[c] = __uint_as_float(raw[c]);
                 }
                 const float mx = row_max(x) * mul;
                 float factor = 1.0f;
@@ -342,10 +339,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         bool ok = true, first = true;
         const int k_boxes = C::KH >> p.box_shift, v_boxes = PC_BN >> p.box_shift;   // box_rows <= 64
         ChunkWalk w;
+        if (leader && lane == 0) chunk_record_none(p, run, n_pairs);
         w.begin(p, deal, run, n_pairs);
         for (; ok; w.next(p, deal)) {
             ok = segs.put(w.more() ? make_seg(w) : ChunkSeg{}, abort_flag, wlim);
             if (!ok || !w.more()) break;
+            if (leader && lane == 0) chunk_record(p, deal, w);
             const int je = max(w.end(0), w.end(1));
             if (je <= w.t0) continue;
             if (!first) {
@@ -447,7 +446,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 vs = vns;
             }
         }
-        if (leader) chunk_records(p, deal, run, n_pairs);
         if (*abort_flag || !ok) {
             // copies in flight must land before the memory is reused
             const uint64_t d0 = global_timer_ns();
