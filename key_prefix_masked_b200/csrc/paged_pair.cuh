@@ -39,6 +39,18 @@ enum : int {
     PPB_FULL = 8 /* [5] */, PPB_EMPTY = 13 /* [5] */, PPB_SFULL = 18 /* [4] */, PPB_SEMPTY = 22 /* [4] */, PPB_GFULL = 26 /* [4] segments */, PPB_GEMPTY = 30 /* [4] */, PPB_NUM = 34
 };
 
+// Item i of a segment of n key tiles in the MMA warp's order: K(0), K(1), then V(j), K(j+2).
+struct PairItem {
+    int j;
+    bool k;
+};
+__device__ __forceinline__ PairItem pair_item(int i, int n) {
+    const int ahead = min(2, n), m = i - ahead, mixed = 2 * (n - ahead);
+    if (m < 0) return {i, true};
+    if (m >= mixed) return {m - (n - ahead), false};
+    return {(m >> 1) + ((m & 1) ? 2 : 0), (m & 1) != 0};
+}
+
 // Arrival on a barrier of the pair's leader that orders this thread's earlier shared-memory
 // stores (after a proxy fence) before the leader's MMAs.
 __device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_addr) {
@@ -371,8 +383,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 return page_ask(p, table, key, E4M3 && lane < (k ? 8 : 16) && j < je && key < w.k.kv);
             };
             auto copy = [&](bool k, int j, const PageAsk& ask, const PageAsk& scale_ask) {
-                const PageAt a = page_at(p, ask, true), sa = page_at(p, scale_ask, false);
+                const PageAt a = page_at(p, ask, true);
                 if constexpr (E4M3) {
+                    const PageAt sa = page_at(p, scale_ask, false);
                     // into staging, on this CTA's own barriers
                     const int slot = static_cast<int>(item % C::NSTG);
                     ok = ok && chunk_wait_warp(PPBAR(PPB_SEMPTY + slot), ((item / C::NSTG) & 1u) ^ 1u, abort_flag, wlim);
@@ -427,23 +440,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     __syncwarp();
                 }
             };
-            // items in the MMA warp's order: K(t0), K(t0+1), then V(j), K(j+2)
-            PageAsk ka = lookup(w.t0, true), ks = lookup_scale(w.t0, true), va = lookup(w.t0, false), vs = lookup_scale(w.t0, false);
-            PageAsk kn = lookup(w.t0 + 1, true), kns = lookup_scale(w.t0 + 1, true);
-            copy(true, w.t0, ka, ks);
-            ka = lookup(w.t0 + 2, true);
-            ks = lookup_scale(w.t0 + 2, true);
-            if (w.t0 + 1 < je) copy(true, w.t0 + 1, kn, kns);
-            for (int j = w.t0; j < je && ok; ++j) {
-                kn = lookup(j + 3, true);
-                kns = lookup_scale(j + 3, true);
-                const PageAsk vn = lookup(j + 1, false), vns = lookup_scale(j + 1, false);
-                copy(false, j, va, vs);
-                if (j + 2 < je) copy(true, j + 2, ka, ks);
-                ka = kn;
-                ks = kns;
-                va = vn;
-                vs = vns;
+            // items in the MMA warp's order; their pages are looked up two items ahead
+            const int n = je - w.t0;
+            if constexpr (E4M3) {
+                // one copy of the code, as in the converters
+                PairItem it0 = pair_item(0, n), it1 = pair_item(1, n);
+                PageAsk a0 = lookup(w.t0 + it0.j, it0.k), s0 = lookup_scale(w.t0 + it0.j, it0.k);
+                PageAsk a1 = lookup(w.t0 + it1.j, it1.k), s1 = lookup_scale(w.t0 + it1.j, it1.k);
+#pragma unroll 1
+                for (int i = 0; i < 2 * n && ok; ++i) {
+                    const PairItem it2 = i + 2 < 2 * n ? pair_item(i + 2, n) : PairItem{n, false};   // (behind the segment: no lookup)
+                    const PageAsk a2 = lookup(w.t0 + it2.j, it2.k), s2 = lookup_scale(w.t0 + it2.j, it2.k);
+                    copy(it0.k, w.t0 + it0.j, a0, s0);
+                    it0 = it1;
+                    a0 = a1;
+                    s0 = s1;
+                    it1 = it2;
+                    a1 = a2;
+                    s1 = s2;
+                }
+            } else {
+                // (the loop above costs bf16, which has fewer instructions to wait for, 4 to 10 %)
+                PageAsk ka = lookup(w.t0, true), va = lookup(w.t0, false), kn = lookup(w.t0 + 1, true);
+                copy(true, w.t0, ka, ka);
+                ka = lookup(w.t0 + 2, true);
+                if (n > 1) copy(true, w.t0 + 1, kn, kn);
+                for (int j = w.t0; j < je && ok; ++j) {
+                    kn = lookup(j + 3, true);
+                    const PageAsk vn = lookup(j + 1, false);
+                    copy(false, j, va, va);
+                    if (j + 2 < je) copy(true, j + 2, ka, ka);
+                    ka = kn;
+                    va = vn;
+                }
             }
         }
         if (*abort_flag || !ok) {
@@ -465,17 +494,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 ok = sg != nullptr;
                 if (!ok || sg->t1 == 0) break;
                 const int t0 = sg->t0, je = max(sg->end(0), sg->end(1)), kv = sg->kv;
-                // items: K(t0), K(t0+1), then V(j), K(j+2)
-                auto convert = [&](auto is_k, int j) {
-                    constexpr bool k = decltype(is_k)::value;
+                const int n = max(0, je - t0);
+                // (one copy of the code for K and V: the kernel waits for instructions otherwise)
+#pragma unroll 1
+                for (int i = 0; i < 2 * n && ok; ++i) {
+                    const PairItem it = pair_item(i, n);
+                    const bool k = it.k;
+                    const int j = t0 + it.j;
                     const int slot = static_cast<int>(item % C::NS), stg = static_cast<int>(item % C::NSTG);
-                    ok = ok && chunk_wait_warp(PPBAR(PPB_SFULL + stg), (item / C::NSTG) & 1u, abort_flag, wlim) &&
+                    ok = chunk_wait_warp(PPBAR(PPB_SFULL + stg), (item / C::NSTG) & 1u, abort_flag, wlim) &&
                          chunk_wait_warp(PPBAR(PPB_EMPTY + slot), ((item / C::NS) & 1u) ^ 1u, abort_flag, wlim);
-                    if (!ok) return;
+                    if (!ok) break;
                     ++item;
                     // K: this rank's 64 rows of 16 chunks; V: 128 rows of this rank's 8 chunks
-                    constexpr int CPR = k ? 16 : 8, RPX = 128 / CPR, GROUP = k ? C::KGROUP : C::VGROUP;
-                    const int r0 = t / CPR, c16 = t % CPR, blk = c16 >> 2;
+                    const int lg = k ? 4 : 3, RPX = 128 >> lg, group = k ? C::KGROUP : C::VGROUP;   // log2 of a row's chunks
+                    const int r0 = t >> lg, c16 = t & ((1 << lg) - 1), blk = c16 >> 2;
                     const int left = kv - j * PC_BN - (k ? rank * C::KH : 0);   // rows that exist
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * 1024;
@@ -484,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int r = x * RPX + r0;
-                        d[x] = *reinterpret_cast<const uint4*>(src + (r * CPR + c16) * 16);
+                        d[x] = *reinterpret_cast<const uint4*>(src + (t + x * 128) * 16);
                         code[x] = src[C::SLOT / 2 + r];
                     }
                     if (left < 128 / (k ? 2 : 1)) {
@@ -498,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int r = x * RPX + r0;
-                        store_codes(d[x], code[x], dst + (r >> 3) * GROUP + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
+                        store_codes(d[x], code[x], dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();
@@ -506,12 +539,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                         mbar_arrive_cluster_release(mapa_shared(PPBAR(PPB_FULL + slot), 0));
                         mbar_arrive(PPBAR(PPB_SEMPTY + stg));
                     }
-                };
-                if (t0 < je) convert(std::true_type{}, t0);
-                if (t0 + 1 < je) convert(std::true_type{}, t0 + 1);
-                for (int j = t0; j < je && ok; ++j) {
-                    convert(std::false_type{}, j);
-                    if (j + 2 < je) convert(std::true_type{}, j + 2);
                 }
             }
         }
