@@ -423,7 +423,10 @@ __device__ __forceinline__ void chunk_record(const PagedParams& p, const ChunkDe
 
 // Sixteen codes of a row as bf16 values, to two 16-byte chunks (ch, ch + 1 before the swizzle)
 // of the row's 128-byte line; lanes with `flip` store the second first, so that a quarter
-// warp touches all banks.
+// warp touches all banks.  Without FAR, scales up to 2^7 (SCALE_ONE_STEP); their rest takes another
+// multiply, which only rows that have it pay for (5 % of the kernel at D = 128, 6 % at 256).
+constexpr uint32_t SCALE_ONE_STEP = 134;
+template <bool FAR>
 __device__ __forceinline__ void store_codes(const uint4& d, uint32_t code, uint8_t* line, int ch, int sw, bool flip) {
     const uint32_t f = scale_factor(code) * 0x10001u;
     const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
@@ -433,7 +436,7 @@ __device__ __forceinline__ void store_codes(const uint4& d, uint32_t code, uint8
         o[2 * e] = widen2(__byte_perm(wd[e], 0u, 0x1404), f);
         o[2 * e + 1] = widen2(__byte_perm(wd[e], 0u, 0x3424), f);
     }
-    if (code > 134u && code != SCALE_NAN) {   // a scale above 2^7: the rest of it
+    if (FAR && code > SCALE_ONE_STEP && code != SCALE_NAN) {
         const uint32_t f2 = ((code - 7u) << 7) * 0x10001u;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f2);
@@ -935,27 +938,40 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     const int left = kv - (j2 >> 1) * PC_BN;       // rows of the tile that exist
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * (8 * C::SW);
-                    // All of a thread's codes first: a load behind a store to shared memory would wait for it.
-                    uint4 d[X];
-                    uint32_t code[X];
+                    // Four loads, then their stores: a load behind a store to shared memory would wait for
+                    // it (and eight at once make more code than they save).
+                    constexpr int XB = X < 4 ? X : 4;
+                    uint32_t top = 0;
+#pragma unroll 1
+                    for (int xb = r0; xb < PC_BN; xb += XB * RPX) {
+                        uint4 d[XB];
+                        uint32_t code[XB];
 #pragma unroll
-                    for (int x = 0; x < X; ++x) {
-                        const int r = x * RPX + r0;
-                        d[x] = *reinterpret_cast<const uint4*>(src + r * D + c16 * 16);
-                        code[x] = src[PC_BN * D + r];
+                        for (int x = 0; x < XB; ++x) {
+                            const int r = x * RPX + xb;
+                            d[x] = *reinterpret_cast<const uint4*>(src + r * D + c16 * 16);
+                            code[x] = src[PC_BN * D + r];
+                        }
+                        if (left < PC_BN) {                          // a page's rows behind the sequence
+#pragma unroll
+                            for (int x = 0; x < XB; ++x)
+                                if (x * RPX + xb >= left) {
+                                    d[x] = make_uint4(0u, 0u, 0u, 0u);
+                                    code[x] = 127u;
+                                }
+                        }
+#pragma unroll
+                        for (int x = 0; x < XB; ++x) {
+                            const int r = x * RPX + xb;
+                            store_codes<false>(d[x], code[x], dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1);
+                            top = max(top, code[x]);
+                        }
                     }
-                    if (left < PC_BN) {                              // a page's rows behind the sequence
-#pragma unroll
-                        for (int x = 0; x < X; ++x)
-                            if (x * RPX + r0 >= left) {
-                                d[x] = make_uint4(0u, 0u, 0u, 0u);
-                                code[x] = 127u;
-                            }
-                    }
-#pragma unroll
-                    for (int x = 0; x < X; ++x) {
-                        const int r = x * RPX + r0;
-                        store_codes(d[x], code[x], dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1);
+                    if (top > SCALE_ONE_STEP) {
+#pragma unroll 1
+                        for (int r = r0; r < min(left, PC_BN); r += RPX)
+                            store_codes<true>(*reinterpret_cast<const uint4*>(src + r * D + c16 * 16), src[PC_BN * D + r],
+                                              dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();

@@ -513,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * 1024;
                     uint4 d[X];                          // all loads first, as in paged_chunk.cuh
-                    uint32_t code[X];
+                    uint32_t code[X], top = 0;
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int r = x * RPX + r0;
@@ -531,7 +531,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
 #pragma unroll
                     for (int x = 0; x < X; ++x) {
                         const int r = x * RPX + r0;
-                        store_codes(d[x], code[x], dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
+                        store_codes<false>(d[x], code[x], dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
+                        top = max(top, code[x]);
+                    }
+                    if (top > SCALE_ONE_STEP) {
+#pragma unroll 1
+                        for (int r = r0; r < min(left, 128 >> (k ? 1 : 0)); r += RPX)
+                            store_codes<true>(*reinterpret_cast<const uint4*>(src + (((r - r0) << lg) + t) * 16), src[C::SLOT / 2 + r],
+                                              dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();

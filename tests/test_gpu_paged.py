@@ -276,6 +276,15 @@ def test_work_beyond_the_counters_is_refused(kp):
     assert (out == 3.0).all()
 
 
+@pytest.mark.parametrize("n_q", [1, 150])
+@pytest.mark.parametrize("D", [32, 128, 256])
+def test_rows_of_far_scales(kp, D, n_q):
+    """Scales from 2^-40 to 2^30 in one sequence, beyond what one bf16 factor reaches, and a page of ordinary ones."""
+    c = make([250, 131], [n_q, n_q], 4, 2, D, 16, True, seed=19, spread=35)
+    c["q"] = (c["q"].float() * 2.0 ** -35).to(torch.bfloat16)
+    check(kp, c)
+
+
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("n_q", [1, 140])
 def test_rising_scores(kp, n_q, e4m3):
