@@ -512,27 +512,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     const int left = kv - j * PC_BN - (k ? rank * C::KH : 0);   // rows that exist
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * 1024;
-                    uint4 d[X];                          // all loads first, as in paged_chunk.cuh
-                    uint32_t code[X], top = 0;
+                    constexpr int XB = 4;                // loads before stores, as in paged_chunk.cuh
+                    uint32_t top = 0;
+#pragma unroll 1
+                    for (int xb = 0; xb < X; xb += XB) {
+                        uint4 d[XB];
+                        uint32_t code[XB];
+                        const int rb = r0 + xb * RPX;
 #pragma unroll
-                    for (int x = 0; x < X; ++x) {
-                        const int r = x * RPX + r0;
-                        d[x] = *reinterpret_cast<const uint4*>(src + (t + x * 128) * 16);
-                        code[x] = src[C::SLOT / 2 + r];
-                    }
-                    if (left < 128 / (k ? 2 : 1)) {
+                        for (int x = 0; x < XB; ++x) {
+                            d[x] = *reinterpret_cast<const uint4*>(src + (t + (xb + x) * 128) * 16);
+                            code[x] = src[C::SLOT / 2 + rb + x * RPX];
+                        }
+                        if (left < 128 / (k ? 2 : 1)) {
 #pragma unroll
-                        for (int x = 0; x < X; ++x)
-                            if (x * RPX + r0 >= left) {
-                                d[x] = make_uint4(0u, 0u, 0u, 0u);
-                                code[x] = 127u;
-                            }
-                    }
+                            for (int x = 0; x < XB; ++x)
+                                if (rb + x * RPX >= left) {
+                                    d[x] = make_uint4(0u, 0u, 0u, 0u);
+                                    code[x] = 127u;
+                                }
+                        }
 #pragma unroll
-                    for (int x = 0; x < X; ++x) {
-                        const int r = x * RPX + r0;
-                        store_codes<false>(d[x], code[x], dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
-                        top = max(top, code[x]);
+                        for (int x = 0; x < XB; ++x) {
+                            const int r = rb + x * RPX;
+                            store_codes<false>(d[x], code[x], dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
+                            top = max(top, code[x]);
+                        }
                     }
                     if (top > SCALE_ONE_STEP) {
 #pragma unroll 1
