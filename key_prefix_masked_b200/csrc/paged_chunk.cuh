@@ -1000,6 +1000,8 @@ __global__ void __launch_bounds__(256) paged_chunk_combine_kernel(const PagedPar
     wait_for_main_kernel();                     // every block, so that this grid never ends before that one
     const SharedPair s = p.shared[blockIdx.x];
     if (s.parts == 0) return;
+    const QueryRange qr = query_range(p, s.b, false);
+    const int n_live = min(qr.n, p.max_q), tok0 = s.qt * 2 * p.tpt;
     // the parts' slots, for all rows
     __shared__ int s_slot[2 + PC_MAX_RUNS];
     __shared__ int s_count[8];
@@ -1017,16 +1019,15 @@ __global__ void __launch_bounds__(256) paged_chunk_combine_kernel(const PagedPar
     if (has) s_slot[rank] = 2 * n_runs + mine;
     if (static_cast<int>(threadIdx.x) < s.parts) s_slot[threadIdx.x] = s.part[threadIdx.x];
     __syncthreads();
-    const QueryRange qr = query_range(p, s.b, false);
-    const int n_live = min(qr.n, p.max_q), tok0 = s.qt * 2 * p.tpt;
     constexpr int V = D >= 128 ? 4 : D / 32, NV = D / (32 * V);   // floats per load, loads per lane
     for (int r = blockIdx.y * 8 + warp; r < 256; r += gridDim.y * 8) {
         const int g = r >> 7, rr = r & 127, tok = rr / p.G;
         const int i = tok0 + g * p.tpt + tok;
         if (tok >= p.tpt || i >= n_live) continue;
         auto at = [&](int k) { return (s_slot[k] * 2LL + g) * 128 + rr; };
-        float M = -INFINITY;
-        for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(p.part_lse + at(k)));
+        const float first = lane < n ? __ldcg(p.part_lse + at(lane)) : -INFINITY;
+        float M = first;
+        for (int k = lane + 32; k < n; k += 32) M = fmaxf(M, __ldcg(p.part_lse + at(k)));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float sum = 0.0f, acc[NV * V];
@@ -1034,7 +1035,7 @@ __global__ void __launch_bounds__(256) paged_chunk_combine_kernel(const PagedPar
         for (int e = 0; e < NV * V; ++e) acc[e] = 0.0f;
         // weights 32 at a time, one per lane, so that the loads of consecutive parts overlap
         for (int k0 = 0; k0 < n; k0 += 32) {
-            const float lc = k0 + lane < n ? __ldcg(p.part_lse + at(k0 + lane)) : -INFINITY;
+            const float lc = k0 == 0 ? first : k0 + lane < n ? __ldcg(p.part_lse + at(k0 + lane)) : -INFINITY;
             const float w_l = lc == -INFINITY ? 0.0f : expf(lc - M);
             const unsigned there = __ballot_sync(0xffffffffu, lc != -INFINITY);   // (a part without keys stored no values)
             const int m = min(32, n - k0);
