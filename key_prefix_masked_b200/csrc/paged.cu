@@ -95,14 +95,6 @@ __device__ __forceinline__ QueryRange query_range(const PagedParams& p, int b, b
     if (report && (t0 != a || t1 != e || t1 - t0 > p.max_q)) atomicOr(&g_paged_status, STATUS_CACHE);
     return {t0, t1 - t0};
 }
-// The page that holds sequence b's keys [pj * page_size, ...), -1 if the table names none.
-__device__ __forceinline__ int checked_page(const PagedParams& p, int b, int pj, bool report) {
-    const int page = __ldg(p.table + b * p.table_stride + pj);
-    if (page >= 0 && page < p.c.num_pages) return page;
-    if (report) atomicOr(&g_paged_status, STATUS_CACHE);
-    return -1;
-}
-
 // Bounded waits on an mbarrier phase: false if the CTA's abort flag (where there is one) is set or
 // the time limit runs out, which sets it and the device timeout flag.
 template <bool CLUSTER>   // acquire at cluster scope

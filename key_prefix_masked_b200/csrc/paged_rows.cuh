@@ -4,14 +4,14 @@
 // What bounds it: every key and value row is read once, with at most 16 query rows to use it,
 // so HBM does.  The kernel is built around keeping loads in flight:
 //
-// - The keys of all (sequence, key head) pairs are cut into tiles of 64, laid end to end,
+// - The keys of all (sequence, key head) pairs are cut into tiles of 64 to 256, laid end to end,
 //   and dealt to the CTAs in equal contiguous runs, so a batch of ragged lengths keeps every
 //   SM busy to the end (each CTA finds its run with a scan over kv_len).  A pair whose tiles
 //   fall to several CTAs is put together by paged_rows_combine_kernel, by log-sum-exp weights.
-// - Each of a CTA's four warps takes 16 of a tile's keys through a ring of shared memory of
+// - Each of a CTA's four warps takes a quarter of a tile's keys through a ring of shared memory of
 //   its own, so no warp waits for another inside a run.  bf16 rows come by 16-byte cp.async
 //   (keys behind the sequence and pages that do not exist are filled with zeros).
-// - The 16 rows and 16 keys make one m16n8k16 tile: S = Q K^T (two MMAs per 16 dims), and
+// - 16 rows and 16 keys make one m16n8k16 tile: S = Q K^T (two MMAs per 16 dims), and
 //   P, already in the A layout, times V.  mma.sync is enough here: at HBM's rate the
 //   tensor work of a tile is a small part of its load time.
 // - e4m3 rows halve the bytes, and the instructions per byte become the bound (the first
@@ -28,6 +28,9 @@
 //   to a bf16's place are the value times 2^-120, and one packed multiply by 2^(120+e-E) does the rest.
 // - The running maximum moves only when a score exceeds it by 2^8 (a vote per tile): the
 //   weights stay below 2^8 (2^15 where they become f16) and the result is the same up to rounding.
+// Measured: 64 ragged sequences up to 32768 keys (32 heads on 8, D 128, bf16) 664 us, 6.5 TB/s; 32 up to
+// 65536 (64 on 8, e4m3) 431 us, 5.0 TB/s, where the ALU pipe is at 47 % and each warp waits out its own
+// instruction latencies (eight warps an SM: a ring of 96 KB and 246 registers).
 
 constexpr int PR_THREADS = 128;
 constexpr int PR_WARPS = 4;
