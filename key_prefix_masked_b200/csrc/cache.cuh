@@ -12,13 +12,13 @@
 //
 // Both kernels are copies: HBM bounds them.  A lane moves 8 elements (16 bytes of bf16; 16
 // codes, 32 bytes of bf16, where codes are read) and has several rows in flight.  Measured: 131072
-// tokens of 8 heads of 128 into random slots, bf16 170 us (6.3 TB/s), e4m3 202 us (4.0 TB/s: half
-// lines of 128 bytes scattered, and about twice the instructions per byte); 64 sequences of 4001
-// such rows read back, bf16 318 us (6.6 TB/s), e4m3 283 us (5.6 TB/s).
+// tokens of 8 heads of 128 into random slots, bf16 171 us (6.3 TB/s), e4m3 179 us (4.5 TB/s: scattered
+// lines of 128 bytes, and twice the instructions per byte, mostly the ALU's); 64 sequences of 4001
+// such rows read back, bf16 318 us (6.6 TB/s), e4m3 279 us (5.6 TB/s).
 
-constexpr int CACHE_THREADS = 256;
+constexpr int CACHE_THREADS = 128;     // (256: e4m3 1 to 3 % slower)
 template <bool E4M3>
-constexpr int CACHE_WRITE_U = E4M3 ? 2 : 4;   // rows in flight per thread (e4m3 at 4: 2 to 8 % slower)
+constexpr int CACHE_WRITE_U = E4M3 ? 2 : 4;   // rows in flight per thread (e4m3 at 4: up to 10 % slower, at 1: 11 %)
 constexpr int CACHE_READ_U = 2;       // (K and V each)
 constexpr int SCALE_EXP_MIN = -117, SCALE_EXP_MAX = 120;
 constexpr int SCALE_NAN = 255;
@@ -45,17 +45,23 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
     return static_cast<uint32_t>(min(max(e, SCALE_EXP_MIN), SCALE_EXP_MAX) + 127);
 }
 // Eight bf16 values (four words) to eight e4m3 codes; inv = 2^-e.  `last`: e = 120, where codes
-// end at 240 (below that exponent none exceeds 448).
+// end at 240 (below that exponent none exceeds 448), that is magnitudes at 240 * 2^120 (0x7f70).
 __device__ __forceinline__ uint2 quantise8(const uint4& x, float inv, bool last) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t h[4];
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (last) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 f = mul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), make_float2(inv, inv));
-        if (last) f = make_float2(fminf(fmaxf(f.x, -240.0f), 240.0f), fminf(fmaxf(f.y, -240.0f), 240.0f));
-        h[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+        for (int i = 0; i < 4; ++i) w[i] = (w[i] & 0x80008000u) | __vminu2(w[i] & 0x7fff7fffu, 0x7f707f70u);
     }
-    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    uint32_t h[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = mul2(make_float2(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i] & 0xffff0000u)), make_float2(inv, inv));
+        const float2 b = mul2(make_float2(__uint_as_float(w[2 * i + 1] << 16), __uint_as_float(w[2 * i + 1] & 0xffff0000u)), make_float2(inv, inv));
+        asm("{\n.reg .b16 lo, hi;\ncvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\ncvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\nmov.b32 %0, {lo, hi};\n}\n"
+            : "=r"(h[i])
+            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    }
+    return make_uint2(h[0], h[1]);
 }
 // Eight e4m3 codes to eight bf16 values code * scale (exact for scales the writer makes).
 __device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
@@ -73,7 +79,7 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
 struct CacheWriteParams {
     CacheView c;
     const __nv_bfloat16* src[2];
-    long long st[2], sh[2];     // element strides of the new rows: token, head
+    long long st[2], sh[2];     // strides of the new rows: token (elements), head (bytes)
     const int32_t* slots;
     int page_shift;             // log2(page_size), -1 if it is no power of two
     int parts, rows_per_part;   // warps per token, and of its 2 Hkv rows (k heads, v heads) each
@@ -98,6 +104,16 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheW
         return;
     }
     const int page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.c.page_size, row = slot - page * p.c.page_size;
+    // the token's first row at its source and in the pages, for k and v; a head further costs one multiply
+    const uint8_t* src[2];
+    uint8_t* dst[2];
+    uint8_t* scale[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        src[w] = reinterpret_cast<const uint8_t*>(p.src[w] + t * p.st[w]) + 16 * l;
+        dst[w] = p.c.data[w] + page * p.c.sp[w] + row * p.c.st[w] + (E4M3 ? 8 : 16) * l;
+        if (E4M3) scale[w] = p.c.scale[w] + static_cast<long long>(page) * p.c.Hkv * p.c.page_size + row;
+    }
 #pragma unroll 1
     for (int r0 = begin + lane / LPR; r0 - lane / LPR < end; r0 += U * RPW) {
         uint4 x[U];
@@ -106,8 +122,8 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheW
             const int r = r0 + u * RPW;
             x[u] = make_uint4(0u, 0u, 0u, 0u);
             if (r < end) {
-                const int w = r >= p.c.Hkv;
-                x[u] = __ldg(reinterpret_cast<const uint4*>(p.src[w] + t * p.st[w] + (w ? r - p.c.Hkv : r) * p.sh[w]) + l);
+                const bool w = r >= p.c.Hkv;
+                x[u] = __ldg(reinterpret_cast<const uint4*>((w ? src[1] : src[0]) + (w ? r - p.c.Hkv : r) * (w ? p.sh[1] : p.sh[0])));
             }
         }
 #pragma unroll
@@ -123,16 +139,16 @@ __global__ void __launch_bounds__(CACHE_THREADS) cache_write_kernel(const CacheW
                 code = scale_code(max(m & 0xffffu, m >> 16));
             }
             if (r >= end) continue;
-            const int w = r >= p.c.Hkv, head = w ? r - p.c.Hkv : r;
-            uint8_t* dst = p.c.data[w] + page * p.c.sp[w] + head * p.c.sh[w] + row * p.c.st[w];
+            const bool w = r >= p.c.Hkv;
+            const int head = w ? r - p.c.Hkv : r;
+            uint8_t* to = (w ? dst[1] : dst[0]) + head * (w ? p.c.sh[1] : p.c.sh[0]);
             if constexpr (E4M3) {
                 uint2 q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN
                 if (code != SCALE_NAN) q = quantise8(x[u], __uint_as_float((254u - code) << 23), code == SCALE_EXP_MAX + 127);
-                reinterpret_cast<uint2*>(dst)[l] = q;
-                if (l == 0)
-                    p.c.scale[w][(static_cast<long long>(page) * p.c.Hkv + head) * p.c.page_size + row] = static_cast<uint8_t>(code);
+                *reinterpret_cast<uint2*>(to) = q;
+                if (l == 0) (w ? scale[1] : scale[0])[static_cast<long long>(head) * p.c.page_size] = static_cast<uint8_t>(code);
             } else {
-                reinterpret_cast<uint4*>(dst)[l] = x[u];
+                *reinterpret_cast<uint4*>(to) = x[u];
             }
         }
     }

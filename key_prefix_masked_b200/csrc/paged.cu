@@ -467,7 +467,7 @@ attn_status attn_cache_write(const attn_cache* cache, const void* k, const void*
     p.src[1] = static_cast<const __nv_bfloat16*>(v);
     for (int i = 0; i < 2; ++i) {
         p.st[i] = s[i].t;
-        p.sh[i] = s[i].h;
+        p.sh[i] = 2 * s[i].h;
     }
     p.slots = slots;
 #define CALL(DD) launch_write<DD>(p, T, stream)
