@@ -271,7 +271,8 @@ int rows_ctas(int per_sm, int tile_keys, int B, int Hkv, long long kv_cap) {
     const long long most = (units + ROWS_MIN_UNITS - 1) / ROWS_MIN_UNITS;
     return static_cast<int>(most < SM_COUNT * per_sm ? most : SM_COUNT * per_sm);
 }
-// Few rows per key head: at most one m16 tile of them.
+// Few rows per key head: at most one m16 tile of them.  16 rows on the chunk kernels instead (64 heads
+// on 4, 32 sequences of 16384 keys, D 128): bf16 231 against 182 us, e4m3 319 against 147.
 bool few_rows(long long max_q, int G) { return max_q * G <= PR_ROWS; }
 
 // A combine kernel behind the main one, launched to overlap it (it waits on the device).
@@ -321,7 +322,7 @@ attn_status launch_rows(PagedParams p, void* workspace, cudaStream_t stream) {
             return ATTN_ERR_CUDA;
     }
     paged_rows_kernel<D, E4M3><<<n, PR_THREADS, C::SMEM, stream>>>(mk, mv, p, n);
-    return launch_combine(paged_rows_combine_kernel<D>, dim3(n - 1), PR_THREADS, stream, p);
+    return launch_combine(paged_rows_combine_kernel<D>, dim3(n - 1, p.max_q * p.G), PR_THREADS, stream, p);
 }
 
 // Runs of the chunk kernels: one per SM (per CTA pair at head dim 256), or fewer where the
