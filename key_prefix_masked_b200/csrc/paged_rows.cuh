@@ -29,7 +29,7 @@
 // - The running maximum moves only when a score exceeds it by 2^8 (a vote per tile): the
 //   weights stay below 2^8 (2^15 where they become f16) and the result is the same up to rounding.
 // Measured: 64 ragged sequences up to 32768 keys (32 heads on 8, D 128, bf16) 664 us, 6.5 TB/s; 32 up to
-// 65536 (64 on 8, e4m3) 431 us, 5.0 TB/s, where the ALU pipe is at 47 % and each warp waits out its own
+// 65536 (64 on 8, e4m3) 431 to 482 us, 4.5 to 5.0 TB/s, where the ALU pipe is at 47 % and each warp waits out its own
 // instruction latencies (eight warps an SM: a ring of 96 KB and 246 registers).
 
 constexpr int PR_THREADS = 128;
