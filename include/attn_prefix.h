@@ -345,6 +345,9 @@ void attn_set_wait_limit_ns(uint64_t ns);
 /* Test hook: run head dims 128 and 256 on the single-CTA kernel instead of the CTA-pair
  * kernel (for side-by-side checks of the two implementations). */
 #define ATTN_DEBUG_SINGLE_CTA 2u
+/* Test hook: every second softmax warp of the paged chunk kernels comes 20 us late to the end of
+ * its key tiles (results may not depend on when a warp gets there). */
+#define ATTN_DEBUG_LATE_SOFTMAX 4u
 void attn_set_debug_flags(unsigned flags);
 
 /* Human-readable name of a status code (static string). */

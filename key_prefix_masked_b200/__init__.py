@@ -31,6 +31,7 @@ from ._binding import (  # noqa: F401
     ATTN_ERR_KVLEN_RANGE,
     ATTN_ERR_CACHE_RANGE,
     ATTN_DEBUG_DROP_COPY,
+    ATTN_DEBUG_LATE_SOFTMAX,
     SUPPORTED_HEAD_DIMS,
     LIB_PATH,
     device_status,

@@ -24,6 +24,7 @@ ATTN_ERR_TIMEOUT = 4
 ATTN_ERR_KVLEN_RANGE = 5
 ATTN_ERR_CACHE_RANGE = 6
 ATTN_DEBUG_DROP_COPY = 1
+ATTN_DEBUG_LATE_SOFTMAX = 4
 
 SUPPORTED_HEAD_DIMS = (32, 64, 128, 256)
 

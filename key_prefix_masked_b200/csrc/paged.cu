@@ -121,6 +121,13 @@ __device__ __forceinline__ bool chunk_wait_warp(uint32_t bar, uint32_t parity, v
     return __all_sync(0xffffffffu, chunk_wait_slow<CLUSTER>(bar, parity, abort_flag, limit_ns)) != 0;
 }
 
+// ATTN_DEBUG_LATE_SOFTMAX: 20 us, in which every MMA that was issued completes.
+__device__ __forceinline__ void debug_pause() {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 20000ull) {
+    }
+}
+
 // A combine kernel's wait for the kernel before it in the stream to be complete (it is launched
 // without one); allow_next_kernel, in that kernel, lets it be launched.
 __device__ __forceinline__ void wait_for_main_kernel() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }

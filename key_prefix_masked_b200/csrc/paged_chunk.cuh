@@ -657,6 +657,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             if (!ok) break;
             const bool has = j1 > t0;
             if (has) {
+                if ((p.debug & ATTN_DEBUG_LATE_SOFTMAX) && (warp & 1)) debug_pause();
                 // D <= 64: one phase per PV; 128: one per segment
                 ok = chunk_wait_warp(CBAR(PCB_O + g), C::AHEAD ? (cnt - 1) & 1u : o_phase, abort_flag, wlim);
                 if (!ok) break;

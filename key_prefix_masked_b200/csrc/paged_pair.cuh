@@ -9,7 +9,8 @@
 //
 // MMA order per segment: S(0), S(1), then PV(j), S(j+2), P(j) stored over S(j).  The
 // softmax of tile j runs under the MMAs of its neighbours.  A rescale of O waits for
-// PV(j-1), announced by one commit per PV.
+// PV(j-1), announced by a commit per PV on two barriers in turn: a parity wait tells a phase from
+// the next one only, and a warp may come to its wait before or after the PV that it waits for.
 //
 // The pages behind a sequence: boxes that lie behind it entirely read as zeros (their page
 // coordinate is outside the pool); the rows of the last V box are loaded and stored by the
@@ -39,8 +40,8 @@ struct PagedPairCfg {
     static constexpr int THREADS = E4M3 ? 384 : 192;
 };
 enum : int {
-    PPB_QFULL = 0, PPB_QEMPTY = 1, PPB_S = 2 /* [2] */, PPB_P = 4 /* [2] */, PPB_PV = 6, PPB_DRAIN = 7,
-    PPB_FULL = 8 /* [5] */, PPB_EMPTY = 13 /* [5] */, PPB_SFULL = 18 /* [4] */, PPB_SEMPTY = 22 /* [4] */, PPB_GFULL = 26 /* [4] segments */, PPB_GEMPTY = 30 /* [4] */, PPB_NUM = 34
+    PPB_QFULL = 0, PPB_QEMPTY = 1, PPB_S = 2 /* [2] */, PPB_P = 4 /* [2] */, PPB_PV = 6 /* [2] */, PPB_DRAIN = 8,
+    PPB_FULL = 9 /* [5] */, PPB_EMPTY = 14 /* [5] */, PPB_SFULL = 19 /* [4] */, PPB_SEMPTY = 23 /* [4] */, PPB_GFULL = 27 /* [4] segments */, PPB_GEMPTY = 31 /* [4] */, PPB_NUM = 35
 };
 
 // Item i of a segment of n key tiles in the MMA warp's order: K(0), K(1), then V(j), K(j+2).
@@ -96,9 +97,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
     if (tid == 0) {
         mbar_init(PPBAR(PPB_QFULL), 1);
         mbar_init(PPBAR(PPB_QEMPTY), 1);
-        mbar_init(PPBAR(PPB_PV), 1);
         mbar_init(PPBAR(PPB_DRAIN), 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(PPBAR(PPB_PV + i), 1);
             mbar_init(PPBAR(PPB_S + i), 1);
             mbar_init(PPBAR(PPB_P + i), 8);
         }
@@ -139,6 +140,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
         const uint32_t p_bar[2] = {mapa_shared(PPBAR(PPB_P), 0), mapa_shared(PPBAR(PPB_P + 1), 0)};
         uint32_t cnt = 0;   // key tiles processed, over all segments
         bool ok = true;
+        // PV of the tile before tile cnt.  Its barrier's phase before is that of PV two tiles earlier, which
+        // "S ready" of its own tile vouched for, and the phase after needs this warp's P(cnt + 1).
+        auto wait_pv = [&]() { return chunk_wait_warp(PPBAR(PPB_PV + ((cnt - 1) & 1)), ((cnt - 1) >> 1) & 1, abort_flag, wlim); };
         while (ok) {
             const ChunkSeg* sg = segs.get(abort_flag, wlim);
             ok = sg != nullptr;
@@ -197,8 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 }
                 l_sum = l_sum * factor + (((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y)));
                 if (rescale) {
-                    // PV of the tile before: commit number cnt - 1 on its barrier, and none after it yet
-                    ok = chunk_wait_warp(PPBAR(PPB_PV), (cnt - 1) & 1, abort_flag, wlim);
+                    ok = wait_pv();
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -219,10 +222,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             if (!ok) break;
             const bool has = je > t0;
             if (has) {
-                // The last two PVs in turn: a parity wait tells one phase from the next only, and
-                // "S ready" of the last tile vouches for the PVs up to two before it.
-                ok = cnt < 2 || chunk_wait_warp(PPBAR(PPB_PV), cnt & 1, abort_flag, wlim);
-                ok = ok && chunk_wait_warp(PPBAR(PPB_PV), (cnt - 1) & 1, abort_flag, wlim);
+                if ((p.debug & ATTN_DEBUG_LATE_SOFTMAX) && (warp & 1)) debug_pause();
+                ok = wait_pv();
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -322,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                         mma_ts_pair_elect_x4<8, (2 * C::VGROUP) / 16>(tmem + C::O_COL, tmem + (p_cnt & 1) * PC_BN + kb * 8u,
                                                                       vd + static_cast<uint64_t>((kb * 2 * C::VGROUP) >> 4), IDESC_PV, kb == 0 && j == t0 ? 0u : 1u);
                     tc_commit_pair_elect(PPBAR(PPB_EMPTY + slot), 0x3);
-                    tc_commit_pair_elect(PPBAR(PPB_PV), 0x3);
+                    tc_commit_pair_elect(PPBAR(PPB_PV + (p_cnt & 1)), 0x3);
                     ++p_cnt;
                     if (j + 2 < je) {
                         issue_s();

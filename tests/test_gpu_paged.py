@@ -445,3 +445,22 @@ def test_refusals(kp):
     out, _ = kp.attn_paged_fwd(q[:0], c, c, table, kv, torch.zeros(3, dtype=torch.int32, device="cuda"))   # no rows
     assert out.shape == (0, 4, 64)
     assert kp.device_status() == kp.ATTN_OK
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_late_softmax_warps(kp, D, e4m3):
+    """Warps that come to the end of a run's tiles long after the last product is complete: one, two and
+    more tiles to a segment, several segments to a block, and the same bits as without the pause."""
+    for kv, n_q in (([100], [40]), ([200], [200]), ([700, 130, 385], [300, 1, 140]), ([129, 500, 0, 260] * 30, [30, 77, 5, 1] * 30)):
+        c = make(kv, n_q, 4, 1, D, 16, e4m3, seed=D + len(kv))
+        want, want_lse = check(kp, c)
+        kp.set_wait_limit_ns(20_000_000)
+        kp.set_debug_flags(kp.ATTN_DEBUG_LATE_SOFTMAX)
+        try:
+            out, lse = call(kp, c)
+            assert kp.device_status() == kp.ATTN_OK
+        finally:
+            kp.set_debug_flags(0)
+            kp.set_wait_limit_ns(1_000_000_000)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
