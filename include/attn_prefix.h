@@ -255,8 +255,9 @@ attn_status attn_qk_norm_rope(const attn_rope_operand* q, const attn_rope_operan
  *     exact and the only rounding is the one to e4m3 (half a step: 2^-4 of a normal
  *     value); every code * 2^e is a bf16 number (at e = 120 magnitudes above 240 * 2^120 are
  *     stored as that, the largest one below infinity).  A row that holds a NaN or an infinity
- *     is stored as NaN (scale byte 255), and reads back as NaN.
- *     Scale bytes begin 8-byte aligned.
+ *     is stored as NaN (scale byte 255), and reads back as NaN.  In pages that something else wrote, the
+ *     codes of NaN (0x7f, 0xff) are NaN under any scale.  Scale bytes: 10 to 247, or 255 (under others
+ *     a row's values leave bf16's normal range); they begin 8-byte aligned.
  * page_size: a multiple of 8.  Strides: multiples of 16 bytes, t >= D, h a multiple of
  * min(D, 64) elements (any layout of whole rows has that), b and h not 0 where there are
  * several pages or heads.

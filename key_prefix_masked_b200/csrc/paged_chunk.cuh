@@ -42,8 +42,8 @@
 // What bounds it, measured.  D 64: the softmax (the exponential unit is 63 % busy; 8192 rows on 16384
 // keys, 8 heads: 470 us, 585 TFLOP/s, the dense kernel 418 us).  D 128: the tensor pipe and shared
 // memory, and power in long runs (2048 causal rows on 32768 keys, 32 heads on 8: 884 us, 1.2 PFLOP/s).
-// e4m3: the converters' ALU work beside the softmax (the same chunk 1145 us; at D 64, 16 sequences of
-// 256 rows on 4096 keys, 164 us against 146 with bf16 pages).  A change of segment costs about 4 us: the
+// e4m3: the converters' ALU work beside the softmax (the same chunk 1180 us, 3 % of it to find codes
+// of NaN; at D 64, 16 sequences of 256 rows on 4096 keys, 164 us against 146 with bf16 pages).  A change of segment costs about 4 us: the
 // pipeline of S, softmax and PV drains and fills again.  (Copying a segment's first tiles before its Q
 // had room did not shorten that.)
 //
@@ -433,23 +433,38 @@ __device__ __forceinline__ void chunk_record(const PagedParams& p, const ChunkDe
 
 // Sixteen codes of a row as bf16 values, to two 16-byte chunks (ch, ch + 1 before the swizzle)
 // of the row's 128-byte line; lanes with `flip` store the second first, so that a quarter
-// warp touches all banks.  Without FAR, scales up to 2^7 (SCALE_ONE_STEP); their rest takes another
-// multiply, which only rows that have it pay for (5 % of the kernel at D = 128, 6 % at 256).
+// warp touches all banks.  ODD false: scales up to 2^7 (SCALE_ONE_STEP) and codes of numbers.  What lies
+// beyond takes another multiply or becomes NaN, in a second pass, so that only tiles that have it
+// pay for it (the multiply alone was 5 % of the kernel at D = 128, 6 % at 256).  `top` collects what tells (see
+// needs_odd): the largest scale code, and the largest magnitudes.
 constexpr uint32_t SCALE_ONE_STEP = 134;
-template <bool FAR>
-__device__ __forceinline__ void store_codes(const uint4& d, uint32_t code, uint8_t* line, int ch, int sw, bool flip) {
+struct TopCodes {
+    uint32_t scale = 0u, magnitudes = 0u;
+};
+__device__ __forceinline__ bool needs_odd(const TopCodes& t) { return t.scale > SCALE_ONE_STEP || nan_codes(t.magnitudes) != 0u; }
+template <bool ODD>
+__device__ __forceinline__ void store_codes(const uint4& d, uint32_t code, uint8_t* line, int ch, int sw, bool flip, TopCodes& top) {
     const uint32_t f = scale_factor(code) * 0x10001u;
     const uint32_t wd[4] = {d.x, d.y, d.z, d.w};
     uint32_t o[8];
+    if (!ODD) top.scale = max(top.scale, code);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        o[2 * e] = widen2(__byte_perm(wd[e], 0u, 0x1404), f);
-        o[2 * e + 1] = widen2(__byte_perm(wd[e], 0u, 0x3424), f);
-    }
-    if (FAR && code > SCALE_ONE_STEP && code != SCALE_NAN) {
-        const uint32_t f2 = ((code - 7u) << 7) * 0x10001u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f2);
+        const uint32_t t0 = __byte_perm(wd[e], 0u, 0x1404), t1 = __byte_perm(wd[e], 0u, 0x3424);
+        const uint32_t m0 = code_magnitudes(t0), m1 = code_magnitudes(t1);
+        o[2 * e] = mul_bf16x2(code_signs(t0) | m0, f);
+        o[2 * e + 1] = mul_bf16x2(code_signs(t1) | m1, f);
+        if constexpr (ODD) {
+            if (code > SCALE_ONE_STEP && code != SCALE_NAN) {
+                const uint32_t f2 = ((code - 7u) << 7) * 0x10001u;
+                o[2 * e] = mul_bf16x2(o[2 * e], f2);
+                o[2 * e + 1] = mul_bf16x2(o[2 * e + 1], f2);
+            }
+            o[2 * e] |= nan_codes(m0);
+            o[2 * e + 1] |= nan_codes(m1);
+        } else {
+            top.magnitudes = __vimax3_u16x2(top.magnitudes, m0, m1);
+        }
     }
     const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
     *reinterpret_cast<uint4*>(line + (((ch + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? hi : lo;
@@ -952,7 +967,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     // Four loads, then their stores: a load behind a store to shared memory would wait for
                     // it (and eight at once make more code than they save).
                     constexpr int XB = X < 4 ? X : 4;
-                    uint32_t top = 0;
+                    TopCodes top;
 #pragma unroll 1
                     for (int xb = r0; xb < PC_BN; xb += XB * RPX) {
                         uint4 d[XB];
@@ -974,15 +989,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
 #pragma unroll
                         for (int x = 0; x < XB; ++x) {
                             const int r = x * RPX + xb;
-                            store_codes<false>(d[x], code[x], dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1);
-                            top = max(top, code[x]);
+                            store_codes<false>(d[x], code[x], dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1, top);
                         }
                     }
-                    if (top > SCALE_ONE_STEP) {
+                    if (needs_odd(top)) {
 #pragma unroll 1
                         for (int r = r0; r < min(left, PC_BN); r += RPX)
                             store_codes<true>(*reinterpret_cast<const uint4*>(src + r * D + c16 * 16), src[PC_BN * D + r],
-                                              dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1);
+                                              dst + (r >> 3) * C::GROUP + (r & 7) * C::SW, ch, C::SW == 128 ? r & 7 : (r >> 1) & 3, blk & 1, top);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();

@@ -518,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                     const uint8_t* src = sStg + stg * C::STG_BYTES;
                     uint8_t* dst = sKV + slot * C::SLOT + blk * 1024;
                     constexpr int XB = 4;                // loads before stores, as in paged_chunk.cuh
-                    uint32_t top = 0;
+                    TopCodes top;
 #pragma unroll 1
                     for (int xb = 0; xb < X; xb += XB) {
                         uint4 d[XB];
@@ -540,15 +540,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
 #pragma unroll
                         for (int x = 0; x < XB; ++x) {
                             const int r = rb + x * RPX;
-                            store_codes<false>(d[x], code[x], dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
-                            top = max(top, code[x]);
+                            store_codes<false>(d[x], code[x], dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1, top);
                         }
                     }
-                    if (top > SCALE_ONE_STEP) {
+                    if (needs_odd(top)) {
 #pragma unroll 1
                         for (int r = r0; r < min(left, 128 >> (k ? 1 : 0)); r += RPX)
                             store_codes<true>(*reinterpret_cast<const uint4*>(src + (((r - r0) << lg) + t) * 16), src[C::SLOT / 2 + r],
-                                              dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1);
+                                              dst + (r >> 3) * group + (r & 7) * 128, (c16 & 3) * 2, r & 7, blk & 1, top);
                     }
                     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     __syncwarp();

@@ -138,10 +138,20 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// Two e4m3 codes in bytes 1 and 3 of t (other bytes: anything) to bf16: values times the
-// factors f (2^(120 + e)).  Sign to bit 15, exponent and mantissa to bits 10..4.
+// Two e4m3 codes in bytes 1 and 3 of t (other bytes: anything) as bf16 values times 2^-120: sign
+// to bit 15, exponent and mantissa (a magnitude) to bits 10..4.  Times 2^(120 + e) they are the row's
+// values, but the two codes of NaN would be 480: what nan_codes gives (all ones in their places: the sum's
+// sign bit, spread over the half by prmt) is or-ed to the product.
+__device__ __forceinline__ uint32_t code_magnitudes(uint32_t t) { return (t >> 4) & 0x07f007f0u; }
+__device__ __forceinline__ uint32_t code_signs(uint32_t t) { return t & 0x80008000u; }
+__device__ __forceinline__ uint32_t nan_codes(uint32_t magnitudes) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, 0, 0xbb99;\n" : "=r"(d) : "r"(magnitudes + 0x78107810u));
+    return d;
+}
 __device__ __forceinline__ uint32_t widen2(uint32_t t, uint32_t f) {
-    return mul_bf16x2((t & 0x80008000u) | ((t >> 4) & 0x07f007f0u), f);
+    const uint32_t m = code_magnitudes(t);
+    return mul_bf16x2(code_signs(t) | m, f) | nan_codes(m);
 }
 // bf16 pattern of 2^(120 + e) cut to 2^127, for a scale code e + 127; NaN for 255.
 __device__ __forceinline__ uint32_t scale_factor(uint32_t code) {

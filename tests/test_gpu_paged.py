@@ -464,3 +464,38 @@ def test_late_softmax_warps(kp, D, e4m3):
             kp.set_debug_flags(0)
             kp.set_wait_limit_ns(1_000_000_000)
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("spread", [0, 8])
+@pytest.mark.parametrize("n_q", [1, 60])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_nan_codes_under_ordinary_scales(kp, D, n_q, spread):
+    """A single code of NaN (0x7F, 0xFF) in a row whose scale is an ordinary one, as another quantiser stores it:
+    NaN for the rows and dims that the formula has it in, and nothing else changes.  spread: scales too far apart
+    for f16 weights.  Keys in whole tiles and in a sequence's last one."""
+    c = make([100, 300, 70], [n_q] * 3, 4, 2, D, 16, True, seed=21, spread=spread)
+    c["causal"] = False
+    if spread:
+        c["q"] = (c["q"].float() * 2.0 ** -8).to(torch.bfloat16)
+    clean, clean_lse = call(kp, c)
+    assert kp.device_status() == kp.ATTN_OK and not torch.isnan(clean).any()
+    rows = slice(n_q, 2 * n_q)                                  # of sequence 1
+    for key, d, code in ((37, 0, 0x7F), (200, 5, 0xFF), (299, D - 1, 0x7F), (288, D // 2 + 2, 0xFF), (140, D - 16, 0x7F)):
+        for n in ("k", "v"):
+            m = dict(c)
+            m[n] = c[n].clone()
+            m[n][int(c["table"][1, key // 16]), 1, key % 16, d] = code
+            out, lse = call(kp, m)
+            want, want_lse = clean.clone(), clean_lse.clone()
+            if n == "k":
+                want[rows, 2:], want_lse[rows, 2:] = math.nan, math.nan
+            else:
+                want[rows, 2:, d] = math.nan
+            bits = (x.view(torch.int16) for x in (out.nan_to_num(7.0), want.nan_to_num(7.0)))
+            assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(*bits), (key, n)
+            assert torch.equal(torch.isnan(lse), torch.isnan(want_lse)) and torch.equal(lse.nan_to_num(7.0), want_lse.nan_to_num(7.0))
+            read = dict(k=0, v=1)[n]
+            got = kp.attn_cache_read(*(m[x].cuda().view(torch.float8_e4m3fn) for x in ("k", "v")), m["table"][1:2].contiguous().cuda(),
+                                     torch.tensor([300], dtype=torch.int32).cuda(), k_scale=m["ks"].cuda(), v_scale=m["vs"].cuda())[read]
+            assert torch.isnan(got[0, 1, key, d]) and int(torch.isnan(got[0, :, :300]).sum()) == 1
+    assert kp.device_status() == kp.ATTN_OK
