@@ -79,6 +79,10 @@ struct PagedParams {
     unsigned long long wait_ns;
     float scale_log2;
 };
+// Tiles of `size` keys that hold `keys` keys, and key `at` of a tile.  A sequence has up to 2^31 - 1 keys, and
+// its last tile may end behind that: the sums are unsigned.
+__device__ __forceinline__ int tiles_of(int keys, int size) { return static_cast<int>((static_cast<uint32_t>(keys) + size - 1u) / size); }
+__device__ __forceinline__ int key_at(int tile, int size, int at) { return static_cast<int>(static_cast<uint32_t>(tile) * size + at); }
 // Index into the block table of the page that holds `key`.
 __device__ __forceinline__ int page_index(const PagedParams& p, int key) {
     return p.page_shift >= 0 ? key >> p.page_shift : key / p.c.page_size;

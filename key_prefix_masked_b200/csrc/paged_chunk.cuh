@@ -112,7 +112,7 @@ __device__ __forceinline__ ChunkPair chunk_pair(const PagedParams& p, int n_q, i
     c.tok0 = qt * 2 * p.tpt;
     c.ntok0 = max(0, min(p.tpt, n_live - c.tok0));
     c.ntok1 = max(0, min(p.tpt, n_live - c.tok0 - p.tpt));
-    auto tiles = [&](int tok, int n) { return n > 0 ? (keys_seen(p.causal, kv, n_q, tok + n - 1) + PC_BN - 1) / PC_BN : 0; };
+    auto tiles = [&](int tok, int n) { return n > 0 ? tiles_of(keys_seen(p.causal, kv, n_q, tok + n - 1), PC_BN) : 0; };
     c.ng0 = tiles(c.tok0, c.ntok0);
     c.ng1 = tiles(c.tok0 + p.tpt, c.ntok1);
     c.n = max(1, max(c.ng0, c.ng1));
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                     uint32_t raw[C::COLS];
                     if constexpr (C::COLS == 128) tmem_ld128_wait(s_addr, raw);
                     else tmem_ld64_wait(s_addr + c0, raw);
-                    if ((j + 1) * PC_BN > all_seen || !pos_scale) {
+                    if (all_seen - j * PC_BN < PC_BN || !pos_scale) {
                         const int lim = seen - j * PC_BN - c0;   // columns this row sees
 #pragma unroll
                         for (int c = 0; c < C::COLS; ++c) x[c] = c < lim ? __uint_as_float(raw[c]) * (pos_scale ? 1.0f : sl2) : -INFINITY;
@@ -892,11 +892,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             // turn took 20 % longer with 16-row pages); its page is looked up one tile ahead
             const int32_t* table = p.table + w.k.b * p.table_stride;
             auto lookup = [&](int j) {
-                const int key = j * PC_BN + lane * p.box_rows;
+                const int key = key_at(j, PC_BN, lane * p.box_rows);
                 return page_ask(p, table, key, lane < boxes && j < je && key < w.k.kv);
             };
             auto lookup_scale = [&](int j) {               // e4m3: lane's group of 8 rows
-                const int key = j * PC_BN + (lane & 15) * 8;
+                const int key = key_at(j, PC_BN, (lane & 15) * 8);
                 return page_ask(p, table, key, E4M3 && j < je && key < w.k.kv);
             };
             PageAsk ask = lookup(w.t0), scale_ask = lookup_scale(w.t0);

@@ -163,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 uint32_t raw[PC_BN];
                 tmem_ld128_wait(s_addr, raw);
                 float x[PC_BN];
-                if ((j + 1) * PC_BN > all_seen || !pos_scale) {
+                if (all_seen - j * PC_BN < PC_BN || !pos_scale) {
                     const int lim = seen - j * PC_BN;
 #pragma unroll
                     for (int c = 0; c < PC_BN; ++c) x[c] = c < lim ? __uint_as_float(raw[c]) * (pos_scale ? 1.0f : sl2) : -INFINITY;
@@ -380,11 +380,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             const int32_t* table = p.table + w.k.b * p.table_stride;
             // lane i copies box i of this CTA's K half / of V; pages are looked up a tile ahead
             auto lookup = [&](int j, bool k) {
-                const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * p.box_rows;
+                const int key = key_at(j, PC_BN, (k ? rank * C::KH : 0) + lane * p.box_rows);
                 return page_ask(p, table, key, lane < (k ? k_boxes : v_boxes) && j < je && key < w.k.kv);
             };
             auto lookup_scale = [&](int j, bool k) {       // e4m3: the lane's group of 8 rows
-                const int key = j * PC_BN + (k ? rank * C::KH : 0) + lane * 8;
+                const int key = key_at(j, PC_BN, (k ? rank * C::KH : 0) + lane * 8);
                 return page_ask(p, table, key, E4M3 && lane < (k ? 8 : 16) && j < je && key < w.k.kv);
             };
             auto copy = [&](bool k, int j, const PageAsk& ask, const PageAsk& scale_ask) {

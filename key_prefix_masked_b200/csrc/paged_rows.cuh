@@ -169,7 +169,7 @@ __device__ __forceinline__ int rows_units(const PagedParams& p, int b, bool repo
     const int n = query_range(p, b, report).n;
     const int kv = paged_kv_len(p.kv_len, b, p.kv_cap, report);
     if (n == 0) return 0;
-    return max(1, (kv + p.tile_keys - 1) / p.tile_keys);
+    return max(1, tiles_of(kv, p.tile_keys));
 }
 
 // The deal: `total` units per key head over the batch, `per` of all heads' units to a CTA.
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
         // ---- loads: this warp's 16 keys of tile t; two 8-key groups, each within one page
         const int32_t* table = p.table + b * p.table_stride;
         auto page_of = [&](int t) {   // lane g < WK / 8: the page of the 8-key group, -1: none
-            const int key = t * C::TK + warp * C::WK + (lane & (C::WK / 8 - 1)) * 8;
+            const int key = key_at(t, C::TK, warp * C::WK + (lane & (C::WK / 8 - 1)) * 8);
             int page = -1;
             if (t < tile1 && key < kv) {
                 page = __ldg(table + page_index(p, key));
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
                     kc[i] = *reinterpret_cast<const uint16_t*>(sc + 16 * i) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sc + 16 * i + 8)) << 16;
                     vc[i] = *reinterpret_cast<const uint16_t*>(sc + C::WK + 16 * i) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sc + C::WK + 16 * i + 8)) << 16;
                 }
-                if (key0 + C::WK > kv) {
+                if (kv - key0 < C::WK) {
                     // rows of a page behind the sequence hold anything: value codes of NaN, scale bytes
                     const int left = max(0, kv - key0);
                     for (int x = lane; x < (C::WK - left) * C::CPR; x += 32)
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
             }
             // ---- scores in the log2 domain, masked by selection
             float x[C::NT][4];
-            const bool masked = key0 + C::WK > all_seen;   // uniform
+            const bool masked = all_seen - key0 < C::WK;   // uniform
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int n = 0; n < C::NT; ++n)

@@ -499,3 +499,50 @@ def test_nan_codes_under_ordinary_scales(kp, D, n_q, spread):
                                      torch.tensor([300], dtype=torch.int32).cuda(), k_scale=m["ks"].cuda(), v_scale=m["vs"].cuda())[read]
             assert torch.isnan(got[0, 1, key, d]) and int(torch.isnan(got[0, :, :300]).sum()) == 1
     assert kp.device_status() == kp.ATTN_OK
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n_q", [1, 17])
+@pytest.mark.parametrize("D", [32, 64, 256])
+def test_longest_sequence(kp, D, n_q, e4m3):
+    """2^31 - 13 keys: one page 16382 times, then one whose keys outweigh all of those and whose last five rows, behind the
+    sequence, are NaN.  Tolerances as in paged_reference: the 2^31 weights of the first page sum to 2^-9 of
+    the others' rounding at most, and the 131075 keys of the last one are added to 8192 at a time in fp32 (2^-11)."""
+    page, n = 8 * 16385, 16383
+    kv = page * n - 5
+    assert kv == 2 ** 31 - 13
+    g = torch.Generator().manual_seed(D + n_q)
+    score = torch.randint(0, 4, (page,), generator=g) * 2.0 + 26.0         # every number here is one in e4m3, and in bf16
+    val = torch.randint(-8, 9, (page, D), generator=g).double() / 4
+    k = torch.zeros(2, 1, page, D)
+    k[1, 0, :, 0] = score
+    v = torch.ones(2, 1, page, D)
+    v[1, 0] = val.float()
+    dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    kc, vc = k.cuda().to(dtype), v.cuda().to(dtype)
+    ds = {}
+    if e4m3:
+        s = torch.full((2, 1, page), 127, dtype=torch.uint8)
+        s[1, 0, -5:] = 255
+        ds = dict(k_scale=s.cuda(), v_scale=s.cuda())
+        for c in (kc, vc):
+            c.view(torch.uint8)[1, 0, -5:] = 0x7F
+    else:
+        kc[1, 0, -5:] = vc[1, 0, -5:] = math.nan
+    q = torch.zeros(n_q, 1, D, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    table = torch.zeros(1, n, dtype=torch.int32)
+    table[0, -1] = 1
+    out, lse = kp.attn_paged_fwd(q.cuda(), kc, vc, table.cuda(), torch.tensor([kv], dtype=torch.int32).cuda(),
+                                 torch.tensor([0, n_q], dtype=torch.int32).cuda(), n_q, scale=1.0, **ds)
+    assert kp.device_status() == kp.ATTN_OK
+    w = (score - 32.0).double().exp()
+    first = page * (n - 1) * math.exp(-32.0)
+    r_out, mean, r_lse = torch.empty(n_q, 1, D, dtype=torch.float64), torch.empty(n_q, 1, D, dtype=torch.float64), torch.empty(n_q, 1, dtype=torch.float64)
+    for i in range(n_q):
+        m = page - 5 - (n_q - 1 - i)                                       # keys of the last page that row i sees
+        total = w[:m].sum() + first
+        r_out[i, 0], mean[i, 0] = (w[:m] @ val[:m] + first) / total, (w[:m] @ val[:m].abs() + first) / total
+        r_lse[i, 0] = total.log() + 32.0
+    err = torch.full((n_q, 1), (D + 4) * 2.0 ** -24 * 32.0, dtype=torch.float64)
+    ref.assert_paged_close(out, lse, (r_out, r_lse, mean, err))
