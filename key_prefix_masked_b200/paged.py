@@ -128,8 +128,11 @@ def rope_inv_freq(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_c
       "linear"  the same divided by factor (positions interpolated)
       "ntk"     base * factor^(rotary_dim / (rotary_dim - 2)): the slowest pair interpolated, the fastest kept
       "yarn"    by parts: pairs that turn more than beta_fast times over original_context are kept, those
-                that turn less than beta_slow times are divided by factor, a linear ramp in the number
-                of turns between; attn_factor 0.1 ln(factor) + 1 on the rotated values
+                that turn less than beta_slow times are divided by factor; attn_factor
+                0.1 ln(factor) + 1 on the rotated values.  Between, a linear ramp in the pair's index,
+                from the last pair that is kept to the first that is divided in full: what the
+                published models use (the code released with arXiv 2309.00071)
+      "yarn_turns"  the same with the ramp linear in the number of turns (that paper's equations)
     """
     R = int(rotary_dim)
     if R < 2 or R % 2:
@@ -145,11 +148,19 @@ def rope_inv_freq(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_c
     f = float(base) ** (-i / R)
     if scaling == "linear":
         f = f / factor
-    elif scaling == "yarn":
-        if not original_context:
-            raise ValueError("scaling 'yarn' needs original_context")
-        turns = original_context * f / (2 * math.pi)
-        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+    elif scaling in ("yarn", "yarn_turns"):
+        if not original_context or not original_context > 0:
+            raise ValueError(f"scaling {scaling!r} needs original_context")
+        if not beta_fast > beta_slow > 0.0 or not base > 1.0:
+            raise ValueError(f"scaling {scaling!r} needs beta_fast > beta_slow > 0 and base > 1")
+        if scaling == "yarn":
+            # a pair i of base^(-2i/R) turns n times where i = R ln(context / (2 pi n)) / (2 ln base)
+            first, last = (R * math.log(original_context / (2 * math.pi * n)) / (2 * math.log(base)) for n in (beta_fast, beta_slow))
+            first, last = max(math.floor(first), 0), min(math.ceil(last), R - 1)
+            keep = 1.0 - ((i / 2 - first) / max(last - first, 1e-3)).clamp(0.0, 1.0)
+        else:
+            turns = original_context * f / (2 * math.pi)
+            keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
         f = f * keep + f / factor * (1.0 - keep)
         attn_factor = 0.1 * math.log(factor) + 1.0
     elif scaling not in (None, "ntk"):

@@ -147,6 +147,38 @@ def test_inv_freq():
     assert mid.any() and ((y[mid] < g[mid]) & (y[mid] > g[mid] / 8)).all()
 
 
+@pytest.mark.parametrize("base,context,factor,first,last", [
+    # 128 ln(4096 / (32 * 2 pi)) / (2 ln 10^4) = 128 * 3.0142 / 18.4207 = 20.94, and 128 ln(4096 / (2 pi)) / 18.4207 =
+    # 128 * 6.4799 / 18.4207 = 45.03: pairs up to 20 are kept, those from 46 on divided in full
+    (1e4, 4096, 8.0, 20, 46),
+    # 128 * 5.0936 / 27.6310 = 23.60 and 128 * 8.5594 / 27.6310 = 39.65
+    (1e6, 32768, 4.0, 23, 40),
+    # 128 * -1.1447 / 18.4207 = -7.95, cut to 0, and 128 * 2.3210 / 18.4207 = 16.13
+    (1e4, 64, 16.0, 0, 17),
+])
+def test_yarn_ramps_over_the_pair_index(base, context, factor, first, last):
+    from key_prefix_masked_b200 import rope_inv_freq
+    f, a = rope_inv_freq(128, base=base, scaling="yarn", factor=factor, original_context=context, device="cpu")
+    assert abs(a - (0.1 * math.log(factor) + 1)) < 1e-15
+    for i in range(64):
+        kept = min(max((last - i) / (last - first), 0.0), 1.0)
+        want = base ** (-i / 64) * (kept + (1 - kept) / factor)
+        assert abs(f[i].item() / want - 1) < 1e-12, i
+
+
+def test_yarn_in_turns():
+    """Pair 35 at base 10^4 and R 128 turns 4096 * 10^(-4 * 35 / 64) / (2 pi) = 4.2333 times over 4096 positions."""
+    from key_prefix_masked_b200 import rope_inv_freq
+    f, a = rope_inv_freq(128, scaling="yarn_turns", factor=8.0, original_context=4096, device="cpu")
+    kept = (4.2333 - 1) / 31
+    assert abs(f[35].item() / (10 ** (-4 * 35 / 64) * (kept + (1 - kept) / 8)) - 1) < 1e-5
+    assert abs(a - (0.1 * math.log(8.0) + 1)) < 1e-15
+    for kw in (dict(original_context=-4), dict(beta_fast=1.0), dict(beta_slow=0.0), dict(base=1.0)):
+        for scaling in ("yarn", "yarn_turns"):
+            with pytest.raises(ValueError):
+                rope_inv_freq(**{**dict(rotary_dim=8, scaling=scaling, factor=4.0, original_context=64, device="cpu"), **kw})
+
+
 def test_reference_table_is_torchs():
     codes = torch.arange(256, dtype=torch.uint8)
     t = codes.view(torch.float8_e4m3fn).double()
