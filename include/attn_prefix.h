@@ -309,9 +309,12 @@ attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table,
  *     max_pages * page_size in Tk's place.
  *   Hq: a multiple of Hkv, Hq / Hkv <= 128.  q, out: strides not 0 where there are several
  *     heads or rows; out may not overlap q.
- *   Infinities and NaN count as the formula has them: in a key or value row before kv_len[b] they
- *     reach every query row whose sequence has it, also (0 * NaN) through values that `causal`
- *     hides from the row.  Keys that are hidden, and whatever lies behind kv_len[b], do not matter.
+ *   Infinities and NaN count as the formula has them: in a key or value row that a query row sees
+ *     they reach that row.  Keys that are hidden, and whatever lies behind kv_len[b], do not matter.
+ *     Values before kv_len[b] that `causal` hides from a row may reach it (0 * NaN) or not: it depends
+ *     on which rows and keys share a tile, and so on the head counts, D, the row's place in its chunk
+ *     and max_q.  They never reach another sequence or key head.  Who needs rows that do not depend on
+ *     later ones keeps values finite.
  *     Sums of weighted values are kept in fp32 before they are divided by the weights' sum: values
  *     times kv_len[b] should stay below 10^36.
  *   Work of 2^31 or more tiles of 256 rows and 128 keys is not done, and raises

@@ -546,3 +546,40 @@ def test_longest_sequence(kp, D, n_q, e4m3):
         r_lse[i, 0] = total.log() + 32.0
     err = torch.full((n_q, 1), (D + 4) * 2.0 ** -24 * 32.0, dtype=torch.float64)
     ref.assert_paged_close(out, lse, (r_out, r_lse, mean, err))
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("n_q,Hq,key", [(4, 4, 298), (300, 2, 290), (300, 4, 31)])
+def test_nan_that_causal_hides(kp, D, n_q, Hq, key, e4m3):
+    """A row of NaN that only later rows see.  In keys it does not matter to the others.  In values it reaches all who
+    see it; the others, and only those of its sequence and key head, have their values or NaN, by the tiles."""
+    c = make([90, 300, 70], [3, n_q, 2], Hq, 2, D, 16, e4m3, seed=22)
+    clean, clean_lse = check(kp, c)
+    rows = torch.arange(3, 3 + n_q)
+    sees = rows - 3 + 300 - n_q >= key
+    mine = torch.zeros(clean.shape[:2], dtype=torch.bool)                      # of key head 1 and this sequence
+    mine[rows, Hq // 2:] = True
+    seen = torch.zeros_like(mine)
+    seen[rows[sees], Hq // 2:] = True
+    assert seen.any() and (mine & ~seen).any()
+    seen, mine = seen.cuda(), mine.cuda()
+    at = (int(c["table"][1, key // 16]), 1, key % 16)
+    for n in ("k", "v"):
+        d = dict(c)
+        d[n] = c[n].clone()
+        if e4m3:
+            d[n + "s"] = c[n + "s"].clone()
+            d[n][at], d[n + "s"][at] = 0x7F, 255
+        else:
+            d[n][at] = math.nan
+        out, lse = call(kp, d)
+        assert torch.isnan(out[seen]).all()
+        same = (out.view(torch.int16) == clean.view(torch.int16)).all(-1)
+        hidden = mine & ~seen
+        assert same[~mine].all() and (same | torch.isnan(out).all(-1))[hidden].all()
+        assert torch.isnan(lse[seen]).all() if n == "k" else torch.equal(lse[seen], clean_lse[seen])
+        assert torch.equal(lse[~seen], clean_lse[~seen])
+        if n == "k":
+            assert same[hidden].all()
+    assert kp.device_status() == kp.ATTN_OK
