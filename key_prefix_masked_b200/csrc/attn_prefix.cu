@@ -1237,14 +1237,14 @@ attn_status attn_get_device_status(cudaStream_t stream) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
     }
-    unsigned int flags = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&flags, attn::g_attn_status, sizeof flags) != cudaSuccess ||
-        cudaMemcpyToSymbol(attn::g_attn_status, &zero, sizeof zero) != cudaSuccess) {
+    // Each copy blocks: flags that are not set need no clearing.
+    unsigned int flags = 0, paged = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&flags, attn::g_attn_status, sizeof flags) != cudaSuccess || !attn::read_paged_flags(&paged) ||
+        (flags != 0 && cudaMemcpyToSymbol(attn::g_attn_status, &zero, sizeof zero) != cudaSuccess) ||
+        (paged != 0 && !attn::clear_paged_flags())) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
     }
-    unsigned int paged = 0;
-    if (!attn::take_paged_flags(&paged)) return ATTN_ERR_CUDA;
     flags |= paged;
     if (flags & attn::STATUS_TIMEOUT) return ATTN_ERR_TIMEOUT;
     if (flags & attn::STATUS_KVLEN) return ATTN_ERR_KVLEN_RANGE;

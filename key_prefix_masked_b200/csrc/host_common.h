@@ -19,8 +19,9 @@ constexpr unsigned STATUS_KVLEN = 2u;
 constexpr unsigned STATUS_LAYOUT = 4u;   // dynamic shared memory not 1024-byte aligned
 constexpr unsigned STATUS_CACHE = 8u;    // a page, slot or query range outside its bounds
 
-// Reads and clears the sticky flags of paged.cu's kernels; false on a CUDA error.
-bool take_paged_flags(unsigned* flags);
+// The sticky flags of paged.cu's kernels: read, and cleared; false on a CUDA error.
+bool read_paged_flags(unsigned* flags);
+bool clear_paged_flags();
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

@@ -141,10 +141,10 @@ __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontr
 #include "paged_chunk.cuh"
 #include "paged_pair.cuh"
 
-bool take_paged_flags(unsigned* flags) {
+bool read_paged_flags(unsigned* flags) { return cudaMemcpyFromSymbol(flags, g_paged_status, sizeof *flags) == cudaSuccess; }
+bool clear_paged_flags() {
     const unsigned zero = 0;
-    return cudaMemcpyFromSymbol(flags, g_paged_status, sizeof *flags) == cudaSuccess &&
-           cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero) == cudaSuccess;
+    return cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero) == cudaSuccess;
 }
 
 }  // namespace attn

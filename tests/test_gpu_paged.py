@@ -583,3 +583,17 @@ def test_nan_that_causal_hides(kp, D, n_q, Hq, key, e4m3):
         if n == "k":
             assert same[hidden].all()
     assert kp.device_status() == kp.ATTN_OK
+
+
+def test_one_status_call_clears_the_flags_of_all_kernels(kp):
+    """The prefix kernels' flag and the paged ones', raised together: the first call reports the one with priority,
+    and none is left behind."""
+    x = torch.zeros(1, 1, 64, 64, dtype=torch.bfloat16, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    table = torch.full((1, 2), 9, dtype=torch.int32, device="cuda")
+    for bad_kv in (True, False):
+        if bad_kv:
+            kp.attn_prefix_fwd(x, x, x, one * 65)
+        kp.attn_paged_fwd(x[0, 0, :1, None], x, x, table, one)
+        assert kp.device_status() == (kp.ATTN_ERR_KVLEN_RANGE if bad_kv else kp.ATTN_ERR_CACHE_RANGE)
+        assert kp.device_status() == kp.ATTN_OK
