@@ -578,6 +578,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
             ok = sg != nullptr;
             if (!ok || sg->t1 == 0) break;
             const int i = sg->tok0 + g * p.tpt + r_tok;
+            // Rows that are not live hold another sequence's queries or what was in shared memory.  When a warp moves
+            // its maxima decides how its rows are rounded, so these have no say in it: their reference is infinite.
             const bool live = r_tok < (g ? sg->ntok1 : sg->ntok0) && r_tok < p.tpt;
             const int seen = live ? keys_seen(p.causal, sg->kv, sg->n_q, i) : 0;
             const int all_seen = keys_seen(p.causal, sg->kv, sg->n_q, sg->tok0 + g * p.tpt);   // by every live row of the tile
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
                 }
                 float factor = 1.0f;
                 if (j == t0) {
-                    m_ref = mx;
+                    m_ref = live ? mx : INFINITY;
                 } else if (__any_sync(0xffffffffu, mx > m_ref + PC_RESCALE_LOG2)) {
                     const float m_new = fmaxf(m_ref, mx);
                     factor = m_ref == -INFINITY ? 0.0f : exp2_approx(m_ref - m_new);

@@ -148,7 +148,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
             ok = sg != nullptr;
             if (!ok || sg->t1 == 0) break;
             const int i = sg->tok0 + g * p.tpt + r_tok;
-            const bool live = r_tok < (g ? sg->ntok1 : sg->ntok0) && r_tok < p.tpt;
+            const bool live = r_tok < (g ? sg->ntok1 : sg->ntok0) && r_tok < p.tpt;   // (others have no say, as in paged_chunk.cuh)
             const int seen = live ? keys_seen(p.causal, sg->kv, sg->n_q, i) : 0;
             const int all_seen = keys_seen(p.causal, sg->kv, sg->n_q, sg->tok0 + g * p.tpt);
             const int t0 = sg->t0;
@@ -175,7 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PagedPairCfg<E4M3>::
                 float factor = 1.0f;
                 bool rescale = false;
                 if (j == t0) {
-                    m_ref = mx;
+                    m_ref = live ? mx : INFINITY;
                 } else if (__any_sync(0xffffffffu, mx > m_ref + PC_RESCALE_LOG2)) {
                     const float m_new = fmaxf(m_ref, mx);
                     factor = m_ref == -INFINITY ? 0.0f : exp2_approx(m_ref - m_new);

@@ -597,3 +597,27 @@ def test_one_status_call_clears_the_flags_of_all_kernels(kp):
         kp.attn_paged_fwd(x[0, 0, :1, None], x, x, table, one)
         assert kp.device_status() == (kp.ATTN_ERR_KVLEN_RANGE if bad_kv else kp.ATTN_ERR_CACHE_RANGE)
         assert kp.device_status() == kp.ATTN_OK
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("G", [5, 33, 100])
+def test_rows_beside_a_sequences_own_change_nothing(kp, G, D, e4m3):
+    """Rows of a tile that are not the sequence's: the next sequence's queries, and (head counts that do not divide
+    128) what an earlier launch left in shared memory.  Bit for bit the same whatever they are."""
+    c = make([700, 600], [20, 300 // G], G, 1, D, 16, e4m3, seed=G)
+    big, fill = dict(c), make([300], [256], 1, 1, D, 16, e4m3, seed=1)
+    big["q"] = c["q"].clone()
+    big["q"][20:] *= 64.0
+    want = None
+    for size, case in ((0.0, c), (64.0, c), (0.0, big), (64.0, big)):
+        d = dict(fill)
+        d["kv"], d["table"] = [300] * 148, fill["table"].expand(148, -1).contiguous()
+        d["start"] = [256 * i for i in range(149)]
+        d["q"] = fill["q"].repeat(148, 1, 1) * size
+        call(kp, d)                                     # a block on every SM, all rows of its tiles
+        out, lse = call(kp, case)
+        got = out[:20].view(torch.int16).cpu(), lse[:20].cpu()
+        want = want or got
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert kp.device_status() == kp.ATTN_OK
