@@ -1020,8 +1020,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, E4M3>::THREADS, 1)
 #undef CBAR
 }
 
-// Pairs that several CTAs worked on: one record of chunk_records a block (x), its rows spread over
-// blockIdx.y, one warp a row.
+// Pairs that several CTAs worked on: a SharedPair, as chunk_record wrote it, to a block (x), its rows spread
+// over blockIdx.y, one warp a row.
 template <int D>
 __global__ void __launch_bounds__(256) paged_chunk_combine_kernel(const PagedParams p, const int n_runs) {
     wait_for_main_kernel();                     // every block, so that this grid never ends before that one

@@ -191,9 +191,10 @@ __device__ __forceinline__ RowsDeal rows_deal(const PagedParams& p, int n_ctas, 
     d.per = max(static_cast<long long>(p.min_units), (d.all(p.c.Hkv) + n_ctas - 1) / n_ctas);
     return d;
 }
-// Calls f(b, first unit of b, units of b) on the one thread whose sequence satisfies pick.
-template <typename Pick, typename F>
-__device__ __forceinline__ void rows_scan(const PagedParams& p, long long* s_sum, Pick pick, F f) {
+// Calls f(b, units of one key head before b) on the one thread whose sequence b holds `unit`, counted over all
+// heads of the sequences in turn.
+template <typename F>
+__device__ __forceinline__ void rows_scan(const PagedParams& p, long long* s_sum, long long unit, F f) {
     long long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += PR_THREADS) {
         const int b = b0 + threadIdx.x;
@@ -209,7 +210,7 @@ __device__ __forceinline__ void rows_scan(const PagedParams& p, long long* s_sum
         for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) incl += s_sum[w];
         const long long all = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
         incl += base;
-        if (n > 0 && pick(b, incl - n, incl)) f(b, incl - n, static_cast<int>(n));
+        if (n > 0 && (incl - n) * p.c.Hkv <= unit && unit < incl * p.c.Hkv) f(b, incl - n);
         base += all;
         __syncthreads();
     }
@@ -236,11 +237,10 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
         if (tid == 0) p.shared_at[blockIdx.x].n = 0;
         return;
     }
-    rows_scan(p, s_sum, [&](int, long long lo, long long hi) { return lo * p.c.Hkv <= unit && unit < hi * p.c.Hkv; },
-              [&](int b, long long lo, int) {
-                  s_b = b;
-                  s_first = lo;
-              });
+    rows_scan(p, s_sum, unit, [&](int b, long long before) {
+        s_b = b;
+        s_first = before;
+    });
     int b = s_b;
     long long rem = unit - s_first * p.c.Hkv;
     const uint32_t ring = smem_u32(smem) + warp * C::NST * C::STAGE;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(PR_THREADS, RowsCfg<D, E4M3>::PER_SM)
         }
         const int all_seen = p.causal ? max(0, kv - qr.n + 1) : kv;   // keys that every row sees
 
-        // ---- loads: this warp's 16 keys of tile t; two 8-key groups, each within one page
+        // ---- loads: this warp's WK keys of tile t, in groups of eight, each within one page
         const int32_t* table = p.table + b * p.table_stride;
         auto page_of = [&](int t) {   // lane g < WK / 8: the page of the 8-key group, -1: none
             const int key = key_at(t, C::TK, warp * C::WK + (lane & (C::WK / 8 - 1)) * 8);
