@@ -303,7 +303,8 @@ attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table,
  * lse stay as they were.
  *   q, out: bf16 [T, Hq, D] at strides (b ignored; NULL: contiguous).   lse: fp32 [T, Hq] or NULL.
  *   q_start: int32 [B + 1], non-decreasing within [0, T]; NULL: B = T, one row each (single
- *     tokens).  max_q: an upper bound on the rows of one sequence.  Bounds that decrease or
+ *     tokens).  max_q: an upper bound on the rows of one sequence; the kernel is chosen by it (up to
+ *     16 rows max_q * Hq / Hkv of a key head, or more), so a loose one costs time.  Bounds that decrease or
  *     leave [0, T] are clamped and rows beyond max_q are not computed; either raises
  *     ATTN_ERR_CACHE_RANGE.  kv_len and block_table as attn_cache_read, with
  *     max_pages * page_size in Tk's place.
@@ -315,6 +316,10 @@ attn_status attn_cache_read(const attn_cache* cache, const int32_t* block_table,
  *     on which rows and keys share a tile, and so on the head counts, D, the row's place in its chunk
  *     and max_q.  They never reach another sequence or key head.  Who needs rows that do not depend on
  *     later ones keeps values finite.
+ *     Scores, their maxima and sums are fp32, out is rounded to bf16 once.  Before they multiply the values,
+ *     the weights 2^(score - reference) are rounded to bf16, as attn_prefix_fwd does (few rows over
+ *     e4m3 pages: to f16 where the rows' scales lie within 2^12), while their sum takes them unrounded: an
+ *     error of up to 2^-8 of the weighted mean of |v|, beside out's own rounding.
  *     Sums of weighted values are kept in fp32 before they are divided by the weights' sum: values
  *     times kv_len[b] should stay below 10^36.
  *   Work of 2^31 or more tiles of 256 rows and 128 keys is not done, and raises

@@ -326,7 +326,9 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, kv_len, q_start=None, max_q
     lse fp32 [T, Hq]).
 
     q: bf16 [T, Hq, D], sequence b's rows at [q_start[b], q_start[b+1]) (int32 [B + 1]); without
-    q_start one row per sequence.  max_q: an upper bound on a sequence's rows (by default T).  The
+    q_start one row per sequence.  max_q: an upper bound on a sequence's rows.  By default it is T, which is
+    right but makes a batch of few rows each run as if one sequence had them all, several times slower: give
+    it with q_start.  The
     pages hold the new tokens' keys too; with `causal`, the rows are the last positions of their
     sequence.  Rows outside every sequence are left as they were (uninitialised where out is made
     here).  workspace: a buffer of attn_paged_workspace_bytes, allocated here when not given."""
