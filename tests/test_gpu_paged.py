@@ -621,3 +621,44 @@ def test_rows_beside_a_sequences_own_change_nothing(kp, G, D, e4m3):
         want = want or got
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert kp.device_status() == kp.ATTN_OK
+
+
+def test_threads_with_streams_of_their_own(kp):
+    """Four threads, each writing, attending and reading over caches of its own on its own stream."""
+    import threading
+    results, errors = {}, []
+
+    def work(i, key):
+        try:
+            g = torch.Generator(device="cuda").manual_seed(i)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                cache = kp.PagedCache(40, 16, 2, 64, quantised=i % 2 == 1)
+                q = torch.randn(300, 6, 64, generator=g, device="cuda").to(torch.bfloat16)
+                k, v = (torch.randn(300, 2, 64, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+                table = torch.randperm(40, generator=g, device="cuda").int()[:19].view(1, 19)
+                j = torch.arange(300, device="cuda")
+                slots = table[0][j // 16] * 16 + (j % 16).int()
+                start = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+                inv, _ = kp.rope_inv_freq(64)
+                kv = torch.tensor([300], dtype=torch.int32, device="cuda")
+                for _ in range(20):
+                    step = cache.step(q, k, v, j.int(), slots, table, kv, start, 300, inv_freq=inv)
+                    one = cache.attend(q[:1], table, kv)
+                read = cache.read(table, kv, 300)
+            stream.synchronize()
+            results[key] = [x.clone() for x in (*step, *one, *read)]
+        except Exception as e:                          # noqa: BLE001  (reported by the test's thread)
+            errors.append(e)
+
+    for i in range(4):
+        work(i, ("alone", i))
+    threads = [threading.Thread(target=work, args=(i, ("together", i))) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for i in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(results["alone", i], results["together", i]))
+    assert kp.device_status() == kp.ATTN_OK

@@ -214,3 +214,31 @@ def test_reference_attention_against_sdpa():
             want = torch.nn.functional.scaled_dot_product_attention(
                 q[start[b]:start[b + 1]].double().transpose(0, 1), kb, vb, attn_mask=mask, scale=0.2)
             assert (out[start[b]:start[b + 1]].transpose(0, 1) - want).abs().max() < 1e-12
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """With another device current, a call is made with the tensors' device current and on that one's stream."""
+    from key_prefix_masked_b200 import paged
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(paged, "_current_device", lambda: current[0])
+    monkeypatch.setattr(paged, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setitem(paged._functions, "f", lambda *args: seen.append((current[0], args)) or 0)
+    for index in (0, 1, 0):
+        paged._call("f", torch.device("cuda", index), 7)
+        assert seen[-1] == (index, (7, 1000 + index)) and current[0] == 0
+    monkeypatch.setitem(paged._functions, "f", lambda *args: 1)
+    with pytest.raises(paged._binding.AttnError):
+        paged._call("f", torch.device("cuda", 1), 7)
+    assert current[0] == 0
