@@ -12,9 +12,9 @@
 //
 // Both kernels are copies: HBM bounds them.  A lane moves 8 elements (16 bytes of bf16; 16
 // codes, 32 bytes of bf16, where codes are read) and has several rows in flight.  Measured: 131072
-// tokens of 8 heads of 128 into random slots, bf16 171 us (6.3 TB/s), e4m3 179 us (4.5 TB/s: scattered
+// tokens of 8 heads of 128 into random slots, bf16 172 us (6.2 TB/s), e4m3 182 us (4.4 TB/s: scattered
 // lines of 128 bytes, and twice the instructions per byte, mostly the ALU's); 64 sequences of 4001
-// such rows read back, bf16 318 us (6.6 TB/s), e4m3 279 us (5.6 TB/s).
+// such rows read back, bf16 320 us (6.6 TB/s), e4m3 283 us (5.6 TB/s).
 
 constexpr int CACHE_THREADS = 128;     // (256: e4m3 1 to 3 % slower)
 template <bool E4M3>

@@ -283,7 +283,9 @@ int rows_ctas(int per_sm, int tile_keys, int B, int Hkv, long long kv_cap) {
     return static_cast<int>(most < SM_COUNT * per_sm ? most : SM_COUNT * per_sm);
 }
 // Few rows per key head: at most one m16 tile of them.  16 rows on the chunk kernels instead (64 heads
-// on 4, 32 sequences of 16384 keys, D 128): bf16 231 against 182 us, e4m3 319 against 147.
+// on 4, 32 sequences of 16384 keys, D 128): bf16 231 against 182 us, e4m3 319 against 147.  Beyond the border the
+// chunk kernels' two 128-row tiles are mostly empty and a key costs as much as for full ones: 17 rows (4 heads on
+// 4, same keys) bf16 238 us, e4m3 325; 64 rows 252 and 322; 128 rows 270 and 341; 256 rows 326 and 407.
 bool few_rows(long long max_q, int G) { return max_q * G <= PR_ROWS; }
 
 // A combine kernel behind the main one, launched to overlap it (it waits on the device).

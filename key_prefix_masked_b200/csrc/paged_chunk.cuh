@@ -40,10 +40,11 @@
 // on 32768 keys, 32 heads on 8, D 128.)
 //
 // What bounds it, measured.  D 64: the softmax (the exponential unit is 63 % busy; 8192 rows on 16384
-// keys, 8 heads: 470 us, 585 TFLOP/s, the dense kernel 418 us).  D 128: the tensor pipe and shared
-// memory, and power in long runs (2048 causal rows on 32768 keys, 32 heads on 8: 884 us, 1.2 PFLOP/s).
+// keys, 8 heads: 472 us, 582 TFLOP/s, the dense kernel 424 us, whose softmax, unlike this one, does not spill:
+// 168 registers a thread for ten warps).  D 128: the tensor pipe and shared
+// memory, and power in long runs (2048 causal rows on 32768 keys, 32 heads on 8: 860 to 873 us, 1.2 PFLOP/s).
 // e4m3: the converters' ALU work beside the softmax (the same chunk 1180 us, 3 % of it to find codes
-// of NaN; at D 64, 16 sequences of 256 rows on 4096 keys, 164 us against 146 with bf16 pages).  A change of segment costs about 4 us: the
+// of NaN; at D 64, 16 sequences of 256 rows on 4096 keys, 167 us against 147 with bf16 pages).  A change of segment costs about 4 us: the
 // pipeline of S, softmax and PV drains and fills again.  (Copying a segment's first tiles before its Q
 // had room did not shorten that.)
 //

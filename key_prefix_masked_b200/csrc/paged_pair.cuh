@@ -16,8 +16,8 @@
 // coordinate is outside the pool); the rows of the last V box are loaded and stored by the
 // copying warp itself, zeros behind the sequence, and its arrival orders them before the MMA.
 //
-// Measured: 2000 rows on 100000 keys (8 heads, bf16) 1.10 ms, 1.49 PFLOP/s, in short runs, 1.28 ms under
-// the power cap; 2368 rows on 8192 keys 143 us, over e4m3 pages 237 us, where the four converter warps
+// Measured: 2000 rows on 100000 keys (8 heads, bf16) 1.08 to 1.11 ms, 1.5 PFLOP/s, in short runs, 1.28 to 1.31 ms under
+// the power cap; 2368 rows on 8192 keys 144 to 154 us, over e4m3 pages 243 to 247 us, where the four converter warps
 // of each CTA set the pace.
 
 template <bool E4M3>

@@ -28,9 +28,10 @@
 //   to a bf16's place are the value times 2^-120, and one packed multiply by 2^(120+e-E) does the rest.
 // - The running maximum moves only when a score exceeds it by 2^8 (a vote per tile): the
 //   weights stay below 2^8 (2^15 where they become f16) and the result is the same up to rounding.
-// Measured: 64 ragged sequences up to 32768 keys (32 heads on 8, D 128, bf16) 664 us, 6.5 TB/s; 32 up to
-// 65536 (64 on 8, e4m3) 431 to 482 us, 4.5 to 5.0 TB/s, where the ALU pipe is at 47 % and each warp waits out its own
-// instruction latencies (eight warps an SM: a ring of 96 KB and 246 registers).
+// Measured: 64 ragged sequences up to 32768 keys (32 heads on 8, D 128, bf16; six draws of the lengths) 6.4 to 6.6
+// TB/s, 630 us for a million keys in all; 32 up to 65536 (64 on 8, e4m3) 4.2 to 4.6 TB/s, 450 to 490 us for a million,
+// where the ALU pipe is at 47 % and each warp waits out its own instruction latencies (eight warps an SM: a ring of
+// 96 KB and 244 registers).
 
 constexpr int PR_THREADS = 128;
 constexpr int PR_WARPS = 4;

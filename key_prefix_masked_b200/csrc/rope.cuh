@@ -9,7 +9,8 @@
 // each lane computes the sines and cosines of its four pairs once, into registers, keeps the
 // weights of its eight elements there too, and then streams the heads' rows through, with
 // ROPE_U rows in flight.  No shared memory and no barrier, so the warps of an SM cover each
-// other's latencies.  Measured at 65536 tokens of 40 heads of 128 (1.34 GB): 255 us, 5.3 TB/s; one
+// other's latencies.  Measured at 65536 tokens of 40 heads of 128 (1.34 GB): 255 to 269 us, 5.0 to 5.3 TB/s
+// (R = 36 in the half layout, whose pairs lie at no 8-byte border and are moved two bytes at a time: 519 us); one
 // block per token, with the sines shared through shared memory, 394 us; one row in flight per lane
 // 281 us, three 298, four 284 (fewer warps fit), blocks of 256 threads 282.
 //
